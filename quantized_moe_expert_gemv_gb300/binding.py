@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libsimoe (include/si_moe.h).
+"""Thin ctypes binding of libsimoe (include/si_moe.h, include/si_kv.h).
 
 The functions below carry the C entry points' names and only marshal
 arguments: tensors become device pointers, torch streams become
@@ -17,6 +17,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "_build", "libsimoe.so")
 HEADER_PATH = os.path.join(ROOT, "include", "si_moe.h")
+KV_HEADER_PATH = os.path.join(ROOT, "include", "si_kv.h")
 
 SI_OK = 0
 SI_ERR_INVALID_ARG = 1
@@ -38,6 +39,14 @@ SI_MAX_EXPERTS = 256
 SI_MAX_TOPK = 16
 SI_MAX_DECODE_TOKENS = 4
 SI_STATIC_SCRATCH_BYTES = 1 << 20
+SI_KV_INT8 = 1
+SI_KV_E4M3 = 2
+SI_KV_BF16 = 1
+SI_KV_F16 = 2
+SI_KV_MAX_SEQS = 1024
+SI_KV_MAX_HEADS = 256
+SI_KV_MAX_LEN = 1 << 22
+SI_KV_MAX_EVICT_PAGES = 16384
 
 
 class SiError(RuntimeError):
@@ -63,6 +72,27 @@ class si_moe_route_out(ctypes.Structure):
     _fields_ = [("topk_ids", ctypes.c_void_p), ("topk_w", ctypes.c_void_p),
                 ("expert_counts", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p),
                 ("perm", ctypes.c_void_p), ("logits", ctypes.c_void_p)]
+
+
+class si_kv_desc(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("code", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class si_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("n_slots", ctypes.c_int32)]
+
+
+class si_kv_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("total_new", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("table_stride", ctypes.c_int32)]
+
+
+class si_kv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -128,15 +158,43 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.si_debug_topk.restype = ctypes.c_int
     lib.si_debug_topk.argtypes = [vp, i32, ctypes.POINTER(si_moe_desc),
                                   ctypes.POINTER(si_moe_route_out), vp]
+    _declare_kv(lib)
     if path is None:
         _lib = lib
     return lib
 
 
+def _declare_kv(lib) -> None:
+    """Argument and result types of include/si_kv.h's functions."""
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.si_kv_plan.restype = ctypes.c_int
+    lib.si_kv_plan.argtypes = [ctypes.POINTER(si_kv_desc), ctypes.c_int, ctypes.POINTER(vp)]
+    lib.si_kv_plan_destroy.restype = None
+    lib.si_kv_plan_destroy.argtypes = [vp]
+    lib.si_kv_scratch_bytes.restype = ctypes.c_int
+    lib.si_kv_scratch_bytes.argtypes = [vp, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.si_kv_scratch_init.restype = ctypes.c_int
+    lib.si_kv_scratch_init.argtypes = [vp, vp, sz, vp]
+    cache, batch, rows = ctypes.POINTER(si_kv_cache), ctypes.POINTER(si_kv_batch), ctypes.POINTER(si_kv_rows)
+    f32 = ctypes.c_float
+    for name, args in (
+            ("si_kv_append", [vp, cache, batch, rows, rows, vp, vp, sz, vp]),
+            ("si_kv_read", [vp, cache, vp, i32, vp, vp, vp, sz, vp]),
+            ("si_kv_attend", [vp, cache, batch, rows, rows, vp, f32, vp, sz, vp]),
+            ("si_kv_weigh", [vp, cache, batch, rows, vp, vp, vp, i64, f32, f32, vp, sz, vp]),
+            ("si_kv_evict", [vp, cache, batch, vp, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+            ("si_kv_read_status", [vp, vp, vp])):
+        f = getattr(lib, name)
+        f.restype = ctypes.c_int
+        f.argtypes = args
+
+
 def declared_symbols() -> list[str]:
-    """Names of the functions include/si_moe.h declares."""
-    with open(HEADER_PATH) as f:
-        text = f.read()
+    """Names of the functions include/si_moe.h and include/si_kv.h declare."""
+    text = ""
+    for path in (HEADER_PATH, KV_HEADER_PATH):
+        with open(path) as f:
+            text += f.read()
     return sorted(set(re.findall(r"^\s*(?:si_status|void|int|const char \*)\s*\*?\s*(si_\w+)\s*\(",
                                  text, flags=re.M)))
 
@@ -341,3 +399,135 @@ def si_moe_read_status_noalloc(stream=None) -> int:
 def si_debug_topk(logits, n, desc: si_moe_desc, route_out: si_moe_route_out, stream=None):
     _check(load_library().si_debug_topk(_ptr(logits), int(n), ctypes.byref(desc),
                                         ctypes.byref(route_out), _stream(stream)), "si_debug_topk")
+
+
+# ------------------------------------------------------------ attention block (include/si_kv.h)
+_KV_CODES = {"int8": SI_KV_INT8, "e4m3": SI_KV_E4M3}
+_KV_DTYPES = {"bf16": SI_KV_BF16, "f16": SI_KV_F16}
+
+
+def make_kv_desc(n_heads, n_kv_heads, head_dim, page_tokens, code="int8", dtype="bf16") -> si_kv_desc:
+    """code: "int8" or "e4m3"; dtype: "bf16" or "f16" (or the SI_KV_* numbers)."""
+    return si_kv_desc(n_heads, n_kv_heads, head_dim, page_tokens, _KV_CODES.get(code, code),
+                      _KV_DTYPES.get(dtype, dtype))
+
+
+class KvPlan:
+    """Owns an si_kv_plan_t (host memory only)."""
+
+    def __init__(self, handle: int, desc: si_kv_desc):
+        self.handle = handle
+        self.desc = desc
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.si_kv_plan_destroy(self.handle)
+            self.handle = None
+
+
+def si_kv_plan(desc: si_kv_desc, cuda_device: int = 0) -> KvPlan:
+    h = ctypes.c_void_p()
+    _check(load_library().si_kv_plan(ctypes.byref(desc), cuda_device, ctypes.byref(h)), "si_kv_plan")
+    return KvPlan(h.value, desc)
+
+
+def si_kv_plan_status(desc: si_kv_desc, cuda_device: int = 0) -> int:
+    """si_kv_plan's status without raising (frees a plan it made)."""
+    lib = load_library()
+    h = ctypes.c_void_p()
+    st = lib.si_kv_plan(ctypes.byref(desc), cuda_device, ctypes.byref(h))
+    if st == SI_OK:
+        lib.si_kv_plan_destroy(h)
+    return st
+
+
+def kv_cache(k_codes, v_codes, k_scale, v_scale, k_tail, v_tail) -> si_kv_cache:
+    """k_codes, v_codes [n_pages, Hkv, P, D] 8-bit; k_scale, v_scale [n_pages, Hkv] float32; k_tail, v_tail
+    [n_slots, Hkv, 2P, D] 16-bit; all contiguous.  The structure keeps them alive."""
+    for t in (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail):
+        if not t.is_contiguous():
+            raise ValueError("the cache's tensors are contiguous")
+    c = si_kv_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail), _ptr(v_tail),
+                    k_codes.shape[0], k_tail.shape[0])
+    c.held = (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail)
+    return c
+
+
+def kv_batch(n_seqs, total_new, max_new, max_len, q_start, lens, page_table, slots=None) -> si_kv_batch:
+    """q_start [n_seqs + 1], lens [n_seqs], page_table [n_seqs, columns] and slots [n_seqs]: int32 on the device
+    (page_table's rows may be strided).  The structure keeps them alive."""
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table is [n_seqs, columns] with columns next to each other")
+    stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+    b = si_kv_batch(n_seqs, total_new, max_new, max_len, _ptr(q_start), _ptr(lens), _ptr(page_table), _ptr(slots),
+                    stride)
+    b.held = (q_start, lens, page_table, slots)
+    return b
+
+
+def _rows(t) -> si_kv_rows:
+    """A [rows, heads, D] tensor (or a view with D contiguous) as si_kv_rows."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError("q, k, v and out are [rows, heads, D] with D contiguous")
+    return si_kv_rows(_ptr(t), t.stride(0), t.stride(1))
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def _kv_call(name, plan, args, scratch, stream, raw_status):
+    st = getattr(load_library(), name)(plan.handle, *args, _ptr(scratch), _nbytes(scratch), _stream(stream))
+    if not raw_status:
+        _check(st, name)
+    return st
+
+
+def si_kv_scratch_bytes(plan: KvPlan, n_seqs, total_new, max_new, max_len) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().si_kv_scratch_bytes(plan.handle, n_seqs, total_new, max_new, max_len, ctypes.byref(out)),
+           "si_kv_scratch_bytes")
+    return out.value
+
+
+def si_kv_scratch_init(plan: KvPlan, scratch, stream=None):
+    _check(load_library().si_kv_scratch_init(plan.handle, _ptr(scratch), _nbytes(scratch), _stream(stream)),
+           "si_kv_scratch_init")
+
+
+def si_kv_append(plan, cache: si_kv_cache, batch: si_kv_batch, k, v, lens_out, scratch, stream=None,
+                 raw_status=False):
+    return _kv_call("si_kv_append", plan, (ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(_rows(k)),
+                                           ctypes.byref(_rows(v)), _ptr(lens_out)), scratch, stream, raw_status)
+
+
+def si_kv_read(plan, cache: si_kv_cache, pages, n, k_out, v_out, scratch, stream=None, raw_status=False):
+    return _kv_call("si_kv_read", plan, (ctypes.byref(cache), _ptr(pages), int(n), _ptr(k_out), _ptr(v_out)),
+                    scratch, stream, raw_status)
+
+
+def si_kv_attend(plan, cache: si_kv_cache, batch: si_kv_batch, q, out, lse, sm_scale, scratch, stream=None,
+                 raw_status=False):
+    return _kv_call("si_kv_attend", plan, (ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(_rows(q)),
+                                           ctypes.byref(_rows(out)), _ptr(lse), float(sm_scale)), scratch, stream,
+                    raw_status)
+
+
+def si_kv_weigh(plan, cache: si_kv_cache, batch: si_kv_batch, q, lse, acc_in, acc_out, decay, sm_scale, scratch,
+                stream=None, raw_status=False):
+    """acc_in (or None) and acc_out: [n_seqs, Hkv, acc_stride] float32, contiguous."""
+    return _kv_call("si_kv_weigh", plan, (ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(_rows(q)), _ptr(lse),
+                                          _ptr(acc_in), _ptr(acc_out), acc_out.shape[2], float(decay),
+                                          float(sm_scale)), scratch, stream, raw_status)
+
+
+def si_kv_evict(plan, cache: si_kv_cache, batch: si_kv_batch, acc_in, acc_out, budget, sink, recent, new_table,
+                new_slots, keep, lens_out, scratch, stream=None, raw_status=False):
+    """new_table [n_seqs, budget], keep [n_seqs, Hkv, budget] int32; acc_in, acc_out [n_seqs, Hkv, acc_stride]."""
+    return _kv_call("si_kv_evict", plan, (ctypes.byref(cache), ctypes.byref(batch), _ptr(acc_in), _ptr(acc_out),
+                                          acc_in.shape[2], int(budget), int(sink), int(recent), _ptr(new_table),
+                                          _ptr(new_slots), _ptr(keep), _ptr(lens_out)), scratch, stream, raw_status)
+
+
+def si_kv_read_status(plan: KvPlan, scratch, stream=None) -> int:
+    return load_library().si_kv_read_status(plan.handle, _ptr(scratch), _stream(stream))

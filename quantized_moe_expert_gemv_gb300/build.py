@@ -1,4 +1,4 @@
-"""Build libsimoe.so (the C ABI in include/si_moe.h) for sm_103a, in tree.
+"""Build libsimoe.so (the C ABI in include/) for sm_103a, in tree.
 
     python -m quantized_moe_expert_gemv_gb300.build
 
@@ -35,7 +35,7 @@ def _nvcc() -> str:
 
 def _headers() -> list[str]:
     return (glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
-            [os.path.join(ROOT, "include", "si_moe.h")])
+            glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
 def _stale(target: str, deps: list[str]) -> bool:

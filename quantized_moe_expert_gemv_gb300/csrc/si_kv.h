@@ -1,0 +1,60 @@
+// si_kv.h -- the attention block's internals: the plan, the scratch layout,
+// the arguments every kernel gets, and the launchers.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/si_kv.h"
+
+namespace si {
+namespace kv {
+
+// Scratch: control words (the status first), then arrival counters of the
+// attention's split rows (one for each CTA; the last to arrive puts its counter
+// back to zero), then partial results.
+constexpr int kCtrlWords = 64;
+constexpr int kCounters = 4096;
+constexpr size_t kCtrlBytes = (kCtrlWords + kCounters) * sizeof(int32_t);
+
+struct Plan {
+    si_kv_desc desc;
+    int device;
+    int sm_count;
+    int smem_optin;
+    long long wait_budget;  // SM cycles a device-side wait may spin before reporting SI_ERR_TIMEOUT
+};
+
+// What every kernel knows of the cache and the call.
+struct Ctx {
+    uint8_t *kc, *vc;
+    float *ks, *vs;
+    uint16_t *kt, *vt;
+    const int32_t *q_start, *lens, *table, *slots;
+    int32_t *status;
+    int64_t n_pages;
+    int32_t n_slots, table_stride;
+    int32_t B, T, max_new, max_len;
+    int32_t H, Hk, G, D, P;
+};
+
+struct Rows {
+    uint16_t *p;
+    int64_t row, head;  // strides in elements
+};
+
+size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int max_len);
+
+cudaError_t launch_append(const Plan &p, const Ctx &c, Rows k, Rows v, int32_t *lens_out, cudaStream_t s);
+cudaError_t launch_read(const Plan &p, const Ctx &c, const int32_t *pages, int n, uint16_t *k_out, uint16_t *v_out,
+                        cudaStream_t s);
+cudaError_t launch_attend(const Plan &p, const Ctx &c, Rows q, Rows out, float *lse, float sm_scale, void *scratch,
+                          cudaStream_t s);
+cudaError_t launch_weigh(const Plan &p, const Ctx &c, Rows q, const float *lse, const float *acc_in, float *acc_out,
+                         int64_t acc_stride, float decay, float sm_scale, cudaStream_t s);
+cudaError_t launch_evict(const Plan &p, const Ctx &c, const float *acc_in, float *acc_out, int64_t acc_stride,
+                         int budget, int sink, int recent, const int32_t *new_table, const int32_t *new_slots,
+                         int32_t *keep, int32_t *lens_out, cudaStream_t s);
+
+}  // namespace kv
+}  // namespace si

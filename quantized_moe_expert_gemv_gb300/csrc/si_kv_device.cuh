@@ -1,0 +1,102 @@
+// si_kv_device.cuh -- device functions shared by the cache's kernels.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "si_device.cuh"
+#include "si_kv.h"
+
+namespace si {
+namespace kv {
+
+// One sequence of the call, checked against the host's bounds: a sequence
+// that breaks one has no rows and no tokens here, and the status says so.
+struct Seq {
+    int row0, n, len, slot;  // first row, rows, tokens, ring slot (-1: outside the cache)
+};
+__device__ __forceinline__ Seq load_seq(const Ctx &c, int b, bool rows = true) {
+    Seq s;
+    const int r0 = rows ? c.q_start[b] : 0, r1 = rows ? c.q_start[b + 1] : 0;
+    s.len = c.lens[b];
+    s.slot = c.slots ? c.slots[b] : b;
+    const bool rows_ok = r0 >= 0 && r1 >= r0 && r1 <= c.T && r1 - r0 <= c.max_new;
+    if (!rows_ok || s.len < 0 || s.len > c.max_len) {
+        set_status(c.status, SI_ERR_DEVICE);
+        s.row0 = s.n = s.len = 0;
+    } else {
+        s.row0 = r0;
+        s.n = r1 - r0;
+    }
+    if (s.slot < 0 || s.slot >= c.n_slots) {
+        set_status(c.status, SI_ERR_DEVICE);
+        s.slot = -1;
+    }
+    return s;
+}
+// Page j of sequence b; -1 (and the status) where the table names none of the cache's.
+__device__ __forceinline__ int64_t load_page(const Ctx &c, int b, int j) {
+    const int p = c.table[(int64_t)b * c.table_stride + j];
+    if (p < 0 || p >= c.n_pages) {
+        set_status(c.status, SI_ERR_DEVICE);
+        return -1;
+    }
+    return p;
+}
+// Element offsets: of a page's head in the codes, of ring row t of a slot's head.
+__device__ __forceinline__ int64_t page_at(const Ctx &c, int64_t page, int h) {
+    return (page * c.Hk + h) * ((int64_t)c.P * c.D);
+}
+__device__ __forceinline__ int64_t ring_at(const Ctx &c, int slot, int h, int t) {
+    return (((int64_t)slot * c.Hk + h) * (2 * c.P) + (t & (2 * c.P - 1))) * c.D;
+}
+
+// ------------------------------------------------------------------ 16-bit values
+template <int DT>
+__device__ __forceinline__ float to_float(uint16_t v) {
+    return DT == SI_KV_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+}
+template <int DT>
+__device__ __forceinline__ uint16_t from_float(float v) {
+    return DT == SI_KV_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+// Two values, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (DT == SI_KV_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// ------------------------------------------------------------------ codes
+constexpr float kQInt8 = 127.0f, kQE4m3 = 448.0f;
+
+template <int CODE>
+__device__ __forceinline__ float code_value(uint8_t c) {
+    if constexpr (CODE == SI_KV_INT8) return (float)(int8_t)c;
+    __nv_fp8_e4m3 v;
+    v.__x = c;
+    return (float)v;
+}
+// Four scaled values to four codes, the first in the low byte.  (An amax whose
+// reciprocal rounds up gives at most Q(1 + 2^-23), which rounds to Q.)
+template <int CODE>
+__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
+    if constexpr (CODE == SI_KV_INT8) {
+        const uint32_t x = (uint32_t)__float2int_rn(a) & 255u, y = (uint32_t)__float2int_rn(b) & 255u;
+        const uint32_t z = (uint32_t)__float2int_rn(c) & 255u, w = (uint32_t)__float2int_rn(d) & 255u;
+        return x | (y << 8) | (z << 16) | (w << 24);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+}
+
+}  // namespace kv
+}  // namespace si

@@ -1,0 +1,197 @@
+// si_kv_evict.cu -- eviction by accumulated attention weight: the choice of
+// each kv head's pages, and their move.
+//
+// Choice (k_kv_choose, one CTA for each sequence and kv head).  A page's score
+// is the sum of acc over its tokens in 64 bits (a page that is kept by a last-bit
+// difference of a 32-bit sum would depend on the order of the sum).  Scores
+// become 64-bit keys whose unsigned order is the scores' order, the protected
+// pages get the largest key, and a radix selection finds the key of the last
+// page that stays: 8 bits a pass from the top, a histogram of the keys that
+// still share the prefix, until the digit's bin holds exactly the pages still
+// wanted.  Equal keys go to the lower page, by a count over the pages in order.
+// Move (k_kv_move, one CTA for each new page, and one for the rest): codes,
+// scale and sums are copied as they are.
+// Bound: HBM for the move (each kept byte read and written once); the choice reads
+// acc once and is a chain of block-wide steps.
+#include "si_kv_device.cuh"
+
+namespace si {
+namespace kv {
+
+constexpr int kChooseThreads = 512;
+constexpr int kMoveThreads = 256;
+
+// Order-preserving key of a score; NaN counts as largest, -0 as +0.
+__device__ __forceinline__ unsigned long long score_key(double x) {
+    if (x != x) return ~0ull - 1;
+    if (x == 0.0) x = 0.0;
+    const unsigned long long u = (unsigned long long)__double_as_longlong(x == 0.0 ? 0.0 : x);
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+// Exclusive prefix of a 0/1 flag over the CTA's threads in order; `total` = their sum.
+__device__ __forceinline__ int block_prefix(bool flag, int *s_warp, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kChooseThreads / 32;
+    const unsigned m = __ballot_sync(0xffffffffu, flag);
+    __syncthreads();  // s_warp's earlier use is over
+    if (lane == 0) s_warp[warp] = __popc(m);
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < warps; ++w) {
+        before += w < warp ? s_warp[w] : 0;
+        total += s_warp[w];
+    }
+    return before + __popc(m & ((1u << lane) - 1));
+}
+
+__global__ void __launch_bounds__(kChooseThreads) k_kv_choose(Ctx c, const float *acc, int64_t acc_stride, int budget,
+                                                              int sink, int recent, int32_t *keep, int32_t *lens_out) {
+    extern __shared__ unsigned long long s_key[];  // [max_len / P]
+    __shared__ int s_hist[256], s_warp[kChooseThreads / 32], s_digit, s_above, s_in;
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, P = c.P;
+    const Seq s = load_seq(c, b, false);
+    const int F = s.len / P, n_keep = min(F, budget);
+    keep += ((int64_t)b * c.Hk + h) * budget;
+    if (h == 0 && tid == 0) lens_out[b] = n_keep * P + s.len % P;
+    for (int i = n_keep + tid; i < budget; i += kChooseThreads) keep[i] = -1;
+    if (F <= budget) {
+        for (int i = tid; i < F; i += kChooseThreads) keep[i] = i;
+        return;
+    }
+    // A group of P/4.. threads per page would share lanes; 8 lanes a page read P/8 values each.
+    const float *a = acc + ((int64_t)b * c.Hk + h) * acc_stride;
+    const int lane8 = tid & 7;
+    for (int j0 = 0; j0 < F; j0 += kChooseThreads / 8) {
+        const int j = j0 + (tid >> 3);
+        double sum = 0.0;
+        if (j < F)
+            for (int t = lane8; t < P; t += 8) sum += (double)a[(int64_t)j * P + t];
+        for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (j < F && lane8 == 0) s_key[j] = j < sink || j >= F - recent ? ~0ull : score_key(sum);
+    }
+    __syncthreads();
+    unsigned long long prefix = 0, mask = 0;
+    int want = n_keep;  // pages still to be taken among those that share the prefix
+    bool ties = true;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += kChooseThreads) s_hist[i] = 0;
+        __syncthreads();
+        for (int j = tid; j < F; j += kChooseThreads)
+            if ((s_key[j] & mask) == prefix) atomicAdd(&s_hist[(s_key[j] >> shift) & 255], 1);
+        __syncthreads();
+        if (tid < 32) {  // the digit whose bin the last wanted page falls in, from the top
+            int mine[8], sum = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += mine[e] = s_hist[255 - (tid * 8 + e)];
+            int before = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, before, o);
+                if (tid >= o) before += up;
+            }
+            before -= sum;
+            if (before < want && want <= before + sum) {
+                int e = 0;
+                while (before + mine[e] < want) before += mine[e++];
+                s_digit = 255 - (tid * 8 + e);
+                s_above = before;
+                s_in = mine[e];
+            }
+        }
+        __syncthreads();
+        prefix |= (unsigned long long)s_digit << shift;
+        mask |= 255ull << shift;
+        want -= s_above;
+        if (s_in == want) {  // all of the bin stay: the lower bits do not matter
+            ties = false;
+            break;
+        }
+    }
+    // Taken: keys above the prefix, and of those that share it all, or the first `want`.
+    int kept = 0, tied = 0;
+    for (int j0 = 0; j0 < F; j0 += kChooseThreads) {
+        const int j = j0 + tid;
+        const unsigned long long k = j < F ? s_key[j] & mask : 0;
+        bool take = j < F && k >= prefix;
+        int total;
+        if (ties) {
+            const bool eq = j < F && k == prefix;
+            const int at = tied + block_prefix(eq, s_warp, total);
+            tied += total;
+            if (eq) take = at < want;
+        }
+        const int at = kept + block_prefix(take, s_warp, total);
+        if (take) keep[at] = j;
+        kept += total;
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) k_kv_move(Ctx c, const float *acc_in, float *acc_out, int64_t acc_stride,
+                                                          int budget, int most, const int32_t *new_table,
+                                                          const int32_t *new_slots, const int32_t *keep) {
+    const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, P = c.P;
+    const Seq s = load_seq(c, b, false);
+    const int F = s.len / P, n_keep = min(F, budget);
+    const int64_t bh = (int64_t)b * c.Hk + h;
+    if (i < n_keep) {
+        const int j = keep[bh * budget + i];
+        const int64_t src = load_page(c, b, j);
+        const int dst = new_table[(int64_t)b * budget + i];
+        if (tid < P) acc_out[bh * acc_stride + i * P + tid] = acc_in[bh * acc_stride + (int64_t)j * P + tid];
+        if (dst < 0 || dst >= c.n_pages) {
+            if (tid == 0) set_status(c.status, SI_ERR_DEVICE);
+            return;
+        }
+        const int units = P * c.D / 16;
+        const int64_t from = page_at(c, src < 0 ? 0 : src, h), to = page_at(c, dst, h);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int u = tid; u < units; u += kMoveThreads) {
+            const uint4 k = src < 0 ? zero : *reinterpret_cast<const uint4 *>(c.kc + from + u * 16);
+            const uint4 v = src < 0 ? zero : *reinterpret_cast<const uint4 *>(c.vc + from + u * 16);
+            *reinterpret_cast<uint4 *>(c.kc + to + u * 16) = k;
+            *reinterpret_cast<uint4 *>(c.vc + to + u * 16) = v;
+        }
+        if (tid < 2) {
+            float *sc = tid ? c.vs : c.ks;
+            sc[(int64_t)dst * c.Hk + h] = src < 0 ? __int_as_float(0x7fc00000) : sc[src * c.Hk + h];
+        }
+        return;
+    }
+    if (i != most) return;
+    // the unfinished page: its sums, and its rows where their ring place changes
+    const int r = s.len - F * P;
+    if (tid < r) acc_out[bh * acc_stride + n_keep * P + tid] = acc_in[bh * acc_stride + (int64_t)F * P + tid];
+    const int slot = new_slots ? new_slots[b] : s.slot;
+    if (slot < 0 || slot >= c.n_slots) {
+        if (tid == 0) set_status(c.status, SI_ERR_DEVICE);
+        return;
+    }
+    if (s.slot < 0 || (slot == s.slot && ((F ^ n_keep) & 1) == 0)) return;
+    const int upr = c.D / 8;
+    for (int u = tid; u < r * upr; u += kMoveThreads) {
+        const int t = u / upr, d = u % upr * 8;
+        const int64_t from = ring_at(c, s.slot, h, F * P + t) + d, to = ring_at(c, slot, h, n_keep * P + t) + d;
+        *reinterpret_cast<uint4 *>(c.kt + to) = *reinterpret_cast<const uint4 *>(c.kt + from);
+        *reinterpret_cast<uint4 *>(c.vt + to) = *reinterpret_cast<const uint4 *>(c.vt + from);
+    }
+}
+
+cudaError_t launch_evict(const Plan &, const Ctx &c, const float *acc_in, float *acc_out, int64_t acc_stride, int budget,
+                         int sink, int recent, const int32_t *new_table, const int32_t *new_slots, int32_t *keep,
+                         int32_t *lens_out, cudaStream_t s) {
+    const size_t smem = (size_t)(c.max_len / c.P) * sizeof(unsigned long long);
+    cudaError_t e = cudaFuncSetAttribute(k_kv_choose, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SI_KV_MAX_EVICT_PAGES * (int)sizeof(unsigned long long));
+    if (e != cudaSuccess) return e;
+    k_kv_choose<<<dim3(c.Hk, c.B), kChooseThreads, smem, s>>>(c, acc_in, acc_stride, budget, sink, recent, keep,
+                                                              lens_out);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int most = min(budget, c.max_len / c.P);  // no sequence keeps more
+    k_kv_move<<<dim3(most + 1, c.Hk, c.B), kMoveThreads, 0, s>>>(c, acc_in, acc_out, acc_stride, budget, most,
+                                                                 new_table, new_slots, keep);
+    return cudaGetLastError();
+}
+
+}  // namespace kv
+}  // namespace si
