@@ -1,0 +1,136 @@
+// si_kv_mma.cuh -- pieces of the cache's warp-level matrix kernels: the fp16
+// m16n8k16 product, codes to fp16 operands, and rows to scaled fp16 operands.
+//
+// All products run on fp16 operands with fp32 sums: an int8 or E4M3 code is
+// exact in fp16.  A row of 16-bit values (q, or an unfinished page's K or V) is
+// multiplied by a power of two that brings its largest value below 128, so
+// bf16's range fits and what is lost lies 2^-31 below the row's largest value;
+// the power of two goes into the row's fp32 factor.  A row with a value that
+// is not finite has zero operands and the factor NaN.
+#pragma once
+#include "si_kv_device.cuh"
+
+namespace si {
+namespace kv {
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {  // a in the low half
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Codes of a word to fp16 pairs: (byte 0, byte 1) and (byte 2, byte 3).  int8: the
+// byte with its sign bit flipped is code + 128; as the low byte of 0x6400 it reads 1024 + code + 128.
+// bias() is done once for a word before its bytes may be interleaved.
+template <int CODE>
+__device__ __forceinline__ uint32_t code_bias(uint32_t w) {
+    return CODE == SI_KV_INT8 ? w ^ 0x80808080u : w;
+}
+template <int CODE>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (CODE == SI_KV_INT8) {
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+        uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off);
+        const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
+        lo = *reinterpret_cast<const uint32_t *>(&x);
+        hi = *reinterpret_cast<const uint32_t *>(&y);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    }
+}
+
+// The power-of-two scaling of a row whose largest magnitude is amax: values
+// are multiplied by `mul`, and `factor` undoes it.  mul is zero, and factor NaN,
+// for a row that is not finite.
+__device__ __forceinline__ void row_scale(float amax, float &mul, float &factor) {
+    int e = (int)((__float_as_uint(amax) >> 23) & 255) - 127 - 6;  // amax / 2^e in [64, 128)
+    e = max(e, -100);
+    mul = __uint_as_float((uint32_t)(127 - e) << 23);
+    factor = __uint_as_float((uint32_t)(127 + e) << 23);
+    if (!(amax <= 3.4e38f)) {
+        mul = 0.0f;
+        factor = __int_as_float(0x7fc00000);
+    }
+}
+// max|x| over 8 packed 16-bit values (NaN becomes infinity).
+template <typename T4>
+__device__ __forceinline__ float amax8(const T4 &x, bool bf16) {
+    // Magnitudes of either type order as their 15 low bits, and those above the infinity are NaN.
+    const uint32_t w[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    if (bf16) return top >= 0x7f80u ? __int_as_float(0x7f800000) : __uint_as_float(top << 16);
+    return top >= 0x7c00u ? __int_as_float(0x7f800000) : __half2float(__ushort_as_half((unsigned short)top));
+}
+// Two packed 16-bit values times mul, as fp16.  mul = 0 gives zeros, whatever the values.
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float mul, bool bf16) {
+    float a, b;
+    if (bf16) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&w));
+        a = f.x;
+        b = f.y;
+    }
+    return mul == 0.0f ? 0u : half2_bits(a * mul, b * mul);
+}
+
+// Where 16-byte chunk c of row r lies in a tile of D-byte rows, so that the
+// loads of either product's operand (rows 2m, 2m+1 with chunks of one parity;
+// rows of one parity with two chunks) touch every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+    if constexpr (D == 64) {
+        const int p = r ^ ((r >> 1) & 1);
+        return (uint32_t)(p * 64 + ((c ^ (((r >> 2) & 1) << 1)) << 4));
+    }
+    return (uint32_t)(r * D + (((c & ~7) | ((c ^ r) & 7)) << 4));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+// Which d's a lane's operand bytes hold.  Lane (g, j) = (lane / 4, lane % 4).  In
+// the first product its bytes of a key are D/4 values in D/64 chunks of 16: chunk
+// i starts at d = k_dim(j, i), and step s of the product (k = 16) takes 4 of
+// them.  (The order of d is free as long as q has the same one.)
+template <int D>
+__device__ __forceinline__ constexpr int k_dim(int j, int i) {
+    return D == 64 ? j * 16 : 128 * (i >> 1) + j * 32 + 16 * (i & 1);
+}
+// The 16 rows' q operand of step s: rows g and g + 8, four d's each, the row's
+// first two d's for k = 2j, 2j+1 and the others for k = 2j+8, 2j+9.
+
+}  // namespace kv
+}  // namespace si
