@@ -147,6 +147,16 @@ si_status si_kv_plan(const si_kv_desc *desc, int cuda_device, si_kv_plan_t *out)
     h->p.sm_count = sms;
     h->p.smem_optin = smem;
     h->p.wait_budget = khz > 0 ? (long long)khz * 1000 : 2000000000ll;  // about one second
+    // SI_FAULT_WAIT_BUDGET as for si_moe_plan: its cycle count is the budget, and a wait runs out for certain
+    h->p.fault_wait = false;
+    if (const char *env = std::getenv("SI_FAULT_WAIT_BUDGET")) {
+        char *end = nullptr;
+        const long long v = std::strtoll(env, &end, 10);
+        if (end && end != env && *end == '\0' && v >= 0) {
+            h->p.wait_budget = v;
+            h->p.fault_wait = true;
+        }
+    }
     *out = h;
     return SI_OK;
 }

@@ -1,11 +1,27 @@
 // si_kv_attend.cu -- which kernel a call of si_kv_attend takes, and the scratch it needs.
-#include "si_kv_decode.cuh"
+#include "si_kv_prompt.cuh"
 
 namespace si {
 namespace kv {
 
 cudaError_t launch_decode_int8(const Plan &p, const DecodeArgs &a, int mt, cudaStream_t s);
 cudaError_t launch_decode_e4m3(const Plan &p, const DecodeArgs &a, int mt, cudaStream_t s);
+cudaError_t launch_prompt_int8(const Plan &p, const PromptArgs &a, cudaStream_t s);
+cudaError_t launch_prompt_e4m3(const Plan &p, const PromptArgs &a, cudaStream_t s);
+
+// Many rows: the tensor-core kernel's tile of 128 rows is at least half full.
+static bool many_rows(const Plan &p, int max_new) {
+    return p.desc.head_dim <= 128 && (int64_t)max_new * (p.desc.n_heads / p.desc.n_kv_heads) > 64;
+}
+// Its CTAs are split along the keys where a call has too few row blocks for
+// the SMs, as long as a part has four tiles of keys.
+static int prompt_splits(const Plan &p, int n_seqs, int max_new, int max_len) {
+    const int64_t G = p.desc.n_heads / p.desc.n_kv_heads;
+    const int64_t ctas = (max_new * G + kPrRows - 1) / kPrRows * p.desc.n_kv_heads * n_seqs;
+    const int64_t parts = ctas > 0 ? p.sm_count / ctas : 1, most = max_len / kPrKeys / 4;
+    const int64_t n = parts < most ? parts : most;
+    return n < 1 ? 1 : n > 32 ? 32 : (int)n;
+}
 
 // Row groups of 16 (one group for a decode step) or 32 rows.
 static int row_tiles(const Plan &p, int max_new) {
@@ -19,16 +35,46 @@ static int decode_ctas(const Plan &p, int mt) {
                                              : (mt == 1 ? DecodeCfg<64, 1>::ctas : DecodeCfg<64, 2>::ctas));
 }
 
-size_t scratch_bytes(const Plan &p, int, int, int, int) {
+size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int max_len) {
+    // A buffer for larger bounds serves smaller ones, so this takes the most that any call within the bounds needs:
+    // a call with fewer sequences or rows may be split more (at most sm_count CTAs of 256 rows together).
+    const size_t D = p.desc.head_dim;
     size_t most = 0;
     for (int mt = 1; mt <= 2; ++mt) {
         const size_t n = (size_t)decode_ctas(p, mt) * 2 * (size_t)partial_floats(16 * mt, p.desc.head_dim) * sizeof(float);
+        most = n > most ? n : most;
+    }
+    if (many_rows(p, max_new)) {
+        const size_t row_heads = (size_t)total_new * p.desc.n_heads;
+        size_t n = row_heads * 32;                                         // 32 splits at most, and
+        const size_t cap = (size_t)p.sm_count * kPrRows;                   // splits x CTAs <= sm_count: rows x splits
+        n = n < cap ? n : cap;
+        n = n > row_heads ? n : row_heads;
+        (void)n_seqs;
+        (void)max_len;
+        n = n * (D + 2) * sizeof(float);
         most = n > most ? n : most;
     }
     return kCtrlBytes + most;
 }
 
 cudaError_t launch_attend(const Plan &p, const Ctx &c, Rows q, Rows out, float *lse, float sm, void *scratch, cudaStream_t s) {
+    const int log_page = p.desc.page_tokens == 16 ? 4 : p.desc.page_tokens == 32 ? 5 : 6;
+    if (many_rows(p, c.max_new)) {
+        PromptArgs a{};
+        a.c = c;
+        a.q = q;
+        a.out = out;
+        a.lse = lse;
+        a.scale2 = sm * kLog2e;
+        a.bf16 = p.desc.dtype == SI_KV_BF16;
+        a.log_page = log_page;
+        a.splits = prompt_splits(p, c.B, c.max_new, c.max_len);
+        a.fault = p.fault_wait;
+        a.budget = p.wait_budget;
+        a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + kCtrlBytes);
+        return p.desc.code == SI_KV_INT8 ? launch_prompt_int8(p, a, s) : launch_prompt_e4m3(p, a, s);
+    }
     DecodeArgs a{};
     a.c = c;
     a.q = q;
@@ -36,7 +82,7 @@ cudaError_t launch_attend(const Plan &p, const Ctx &c, Rows q, Rows out, float *
     a.lse = lse;
     a.scale2 = sm * kLog2e;
     a.bf16 = p.desc.dtype == SI_KV_BF16;
-    a.log_page = p.desc.page_tokens == 16 ? 4 : p.desc.page_tokens == 32 ? 5 : 6;
+    a.log_page = log_page;
     a.counters = static_cast<int32_t *>(scratch) + kCtrlWords;
     a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + kCtrlBytes);
     const int mt = row_tiles(p, c.max_new);

@@ -1,0 +1,643 @@
+// si_kv_prompt.cuh -- attention of many rows over the cache (a prompt, a chunk
+// of one) on the tcgen05 tensor cores, head_dim 64 and 128.
+//
+// One CTA for 256 rows (query token, query head of the kv head) of one sequence
+// and kv head: two tiles of 128 rows, which share every K and V tile.
+//   S = Q K^T (fp16 operands, fp32 sums in tensor memory), p = 2^(f S - m),
+//   O += (p times the page's V scale, fp16, in tensor memory) V
+// The running maximum m is lazy and the V scale is relative to a running
+// reference, as in the few-row kernel (si_kv_decode.cuh), so both are rarely
+// moved and O is rarely rescaled.
+// Roles: warps 0-3 and 4-7 are the softmax of the two row tiles, a thread a row;
+// warps 8-11 turn codes into fp16 tiles in shared memory (K with d innermost, V
+// with d innermost too: the second product takes V as its transposed operand);
+// one thread of warp 12 issues the products.  While one row tile's products run,
+// the other's softmax does.
+// Bound: at D = 128 a pair of row tiles and 128 keys takes 2048 cycles of the
+// tensor cores and 2048 of the exponential unit (256 x 128 at 16 a cycle), so
+// the two have to overlap; at D = 64 the exponential alone bounds it.
+#pragma once
+#include "si_kv_decode.cuh"
+#include "si_tc.cuh"
+
+namespace si {
+namespace kv {
+
+constexpr int kPrRows = 256, kPrKeys = 128;
+constexpr int kPrThreads = 13 * 32;
+constexpr int kPrFactorSlots = 4;
+
+template <int D>
+struct PromptCfg {
+    static constexpr int tile = kPrKeys * D * 2;  // bytes of one fp16 tile of 128 rows
+    static constexpr int q = 0;
+    static constexpr int k = 2 * tile;
+    static constexpr int v = k + 2 * tile;
+    static constexpr int factors = v + 2 * tile;                       // [slots][2][128] floats
+    static constexpr int bars = factors + kPrFactorSlots * 2 * 128 * 4;
+    static constexpr int smem = bars + 32 * 8 + 1024;                  // + alignment slack
+};
+enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarNever = 15, kBars = 16 };
+
+struct PromptArgs {
+    Ctx c;
+    Rows q, out;
+    float *lse;
+    float scale2;
+    int bf16;
+    int log_page;
+    int splits;
+    int fault;
+    long long budget;
+    float *partial;  // [splits][T][H][D], then [splits][T][H][2]
+};
+
+// Tensor-memory stores and the product with its first operand in tensor memory.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// Descriptor of an operand whose 64 innermost values (128 swizzled bytes) run
+// along M or N: 8-row groups of K follow each other at 1024 bytes (stride
+// offset), the next 64 values along M or N lie `next` bytes on (leading offset).
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t smem_addr, uint32_t next) {
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(next >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// Byte offset of 16-byte unit u (8 values of d) of row r in an fp16 tile of 128
+// rows: 64 values of d (128 bytes) a row and half, halves 16 KB apart.
+__device__ __forceinline__ uint32_t f16_tile_at(int r, int u) {
+    return (uint32_t)((u >> 3) * 16384 + r * 128 + (((u ^ r) & 7) << 4));
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pk2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void up2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int CODE, int D>
+__global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a) {
+    using Cfg = PromptCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem;
+    const Ctx &c = a.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool bf16 = a.bf16;
+
+    // ---- which rows: the last ones of each sequence first (they see the most keys)
+    const int bh = c.B * c.Hk;
+    const int split = blockIdx.x % a.splits, id = blockIdx.x / a.splits;
+    const int b = id % bh / c.Hk, h = id % c.Hk;
+    const Seq s = load_seq(c, b);
+    const int blocks = (s.n * c.G + kPrRows - 1) / kPrRows;
+    const int rb = blocks - 1 - id / bh;
+    if (rb < 0) return;
+    const int old = s.len - s.n, paged = s.len & ~(c.P - 1);
+    const int rows = min(kPrRows, s.n * c.G - rb * kPrRows);
+    int t_from[2], t_to[2];  // key tiles of the two row tiles
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int last = rb * kPrRows + min(rows, 128 * (x + 1)) - 1;
+        const int see = rows > 128 * x ? max(0, old + last / c.G + 1) : 0;
+        t_to[x] = (see + kPrKeys - 1) / kPrKeys;
+    }
+    const int nt_all = max(t_to[0], t_to[1]);
+    const int t_first = (int)((int64_t)nt_all * split / a.splits), t_last = (int)((int64_t)nt_all * (split + 1) / a.splits);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        t_from[x] = t_first;
+        t_to[x] = max(t_first, min(t_to[x], t_last));
+    }
+    const int nt = max(t_to[0], t_to[1]) - t_first;  // tiles of this CTA
+    const int ntx[2] = {t_to[0] - t_first, t_to[1] - t_first};
+
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    float *factors = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)) + Cfg::factors);
+    auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
+
+    if (tid == 0) {
+        mbar_init(bar(kBarQ), 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarKFull + i), 128);
+            mbar_init(bar(kBarKEmpty + i), 1);
+            mbar_init(bar(kBarVFull + i), 128);
+            mbar_init(bar(kBarVEmpty + i), 1);
+            mbar_init(bar(kBarS + i), 1);
+            mbar_init(bar(kBarP + i), 128);
+            mbar_init(bar(kBarO + i), 1);
+        }
+        mbar_init(bar(kBarNever), 1);
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        tc::tmem_alloc(smem_addr(&s_tmem), 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    // Bounded waits, of a warp (its lanes give up together) and of the one thread that issues the
+    // products.  A role that gives up goes on to the end of the kernel; the others run out in turn.
+    auto wait = [&](int i, int parity) {
+        if (ok && !mbar_wait_warp(bar(i), (uint32_t)parity, a.budget)) {
+            ok = false;
+            if (lane == 0) set_status(c.status, SI_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+    auto wait_one = [&](int i, int parity) {
+        if (ok && !mbar_wait_spin(bar(i), (uint32_t)parity, a.budget)) {
+            ok = false;
+            set_status(c.status, SI_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+
+    if (warp < 8) {
+        // ================================================= softmax: a thread a row
+        const int x = warp >> 2, r = tid & 127;
+        const int rr = rb * kPrRows + x * 128 + r;
+        const bool live = x * 128 + r < rows;
+        const int row = s.row0 + (live ? rr / c.G : 0), head = h * c.G + (live ? rr % c.G : 0);
+        const int lim = live ? old + rr / c.G + 1 : 0;
+        const uint16_t *src = a.q.p + row * a.q.row + head * a.q.head;
+        float qf;
+        {
+            uint4 v[D / 8];
+            float amax = 0.0f;
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u) {
+                v[u] = live ? *reinterpret_cast<const uint4 *>(src + 8 * u) : make_uint4(0, 0, 0, 0);
+                amax = fmaxf(amax, amax8(v[u], bf16));
+            }
+            float mul;
+            row_scale(amax, mul, qf);
+            qf *= a.scale2;
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u)
+                sts128(base + Cfg::q + x * Cfg::tile + f16_tile_at(r, u), scale2(v[u].x, mul, bf16),
+                       scale2(v[u].y, mul, bf16), scale2(v[u].z, mul, bf16), scale2(v[u].w, mul, bf16));
+            tc::fence_proxy_async_smem();
+            mbar_arrive(bar(kBarQ));
+        }
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+        float m = kNoScore, v_ref = 1e-30f;
+        f32x2 l2 = pk2(0.0f, 0.0f);
+        const int n = ntx[x];
+        for (int i = 0; i < n; ++i) {
+            const int key0 = (t_first + i) * kPrKeys;
+            const float *kf = factors + (i % kPrFactorSlots) * 256, *vf = kf + 128;
+            if (!wait(kBarS + x, i & 1)) break;
+            tc::fence_after_sync();
+            const bool whole = key0 + kPrKeys <= paged;                 // a factor for every 16 keys
+            const bool all = __all_sync(0xffffffffu, !live || key0 + kPrKeys <= lim) && whole;
+            // the largest score
+            float top = -INFINITY, v_top = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t z[32];
+                tc::tmem_ld32(ts + 32 * q, z);
+                tc::tmem_wait_ld();
+                if (all) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float t = __uint_as_float(z[16 * e]);
+#pragma unroll
+                        for (int k = 1; k < 16; ++k) t = fmaxf(t, __uint_as_float(z[16 * e + k]));
+                        top = fmaxf(top, t * kf[32 * q + 16 * e]);
+                        v_top = fmaxf(v_top, vf[32 * q + 16 * e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int col = 32 * q + k;
+                        if (key0 + col < lim) top = fmaxf(top, __uint_as_float(z[k]) * kf[col]);
+                        v_top = fmaxf(v_top, vf[col]);
+                    }
+                }
+            }
+            top *= qf;
+            const bool grow = top > m + 8.0f, scale = v_top > 4.0f * v_ref;
+            if (__any_sync(0xffffffffu, grow || scale)) {
+                float f = 1.0f;
+                if (grow) {
+                    f = ex2(m - top);
+                    m = top;
+                    l2 = mul2(l2, pk2(f, f));
+                }
+                if (scale) {
+                    f *= v_ref / v_top;
+                    v_ref = v_top;
+                }
+                if (i > 0) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(to + 32 * q, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(to + 32 * q, o);
+                    }
+                }
+            }
+            const float inv = 16.0f / v_ref;
+            const f32x2 m2 = pk2(-m, -m);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t z[32], p[16];
+                tc::tmem_ld32(ts + 32 * q, z);
+                tc::tmem_wait_ld();
+                if (all) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = kf[32 * q + 16 * e] * qf, w = vf[32 * q + 16 * e] * inv;
+                        const f32x2 f2 = pk2(f, f), w2 = pk2(w, w);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const f32x2 t = fma2(pk2(__uint_as_float(z[16 * e + k]), __uint_as_float(z[16 * e + k + 1])), f2, m2);
+                            float t0, t1;
+                            up2(t, t0, t1);
+                            const f32x2 pp = pk2(ex2(t0), ex2(t1));
+                            l2 = add2(l2, pp);
+                            up2(mul2(pp, w2), t0, t1);
+                            p[8 * e + k / 2] = half2_bits(t0, t1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float w[2], pp[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int col = 32 * q + k + e;
+                            pp[e] = key0 + col < lim ? ex2(fmaf(__uint_as_float(z[k + e]), kf[col] * qf, -m)) : 0.0f;
+                            w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (vf[col] * inv);
+                        }
+                        l2 = add2(l2, pk2(pp[0], pp[1]));
+                        p[k / 2] = half2_bits(w[0], w[1]);
+                    }
+                }
+                tmem_st16(ts + 16 * q, p);
+            }
+            tmem_wait_st();
+            tc::fence_before_sync();
+            mbar_arrive(bar(kBarP + x));
+        }
+        // ---- the rows' results
+        if (n > 0) wait(kBarO + x, 0);
+        tc::fence_after_sync();
+        float l, l_odd;
+        up2(l2, l, l_odd);
+        l += l_odd;
+        if (ok) {
+            const float f = v_ref * 0.0625f, inv = l == 0.0f ? 0.0f : f / l;
+            if (a.splits == 1) {
+                uint16_t *dst = a.out.p + row * a.out.row + head * a.out.head;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tc::tmem_ld32(to + 32 * q, o);
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = __uint_as_float(o[k + 2 * e]) * inv, v = __uint_as_float(o[k + 2 * e + 1]) * inv;
+                            y[e] = bf16 ? pack2<SI_KV_BF16>(u, v) : pack2<SI_KV_F16>(u, v);
+                        }
+                        if (live) *reinterpret_cast<uint4 *>(dst + 32 * q + k) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                if (live && a.lse) a.lse[(int64_t)row * c.H + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            } else {
+                const int64_t at = ((int64_t)split * c.T + row) * c.H + head;
+                float *dst = a.partial + at * D;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tc::tmem_ld32(to + 32 * q, o);
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        if (live)
+                            *reinterpret_cast<float4 *>(dst + 32 * q + k) =
+                                make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
+                                            __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+                }
+                if (live)
+                    *reinterpret_cast<float2 *>(a.partial + (int64_t)a.splits * c.T * c.H * D + at * 2) = make_float2(m, l);
+            }
+        }
+        tc::fence_before_sync();
+    } else if (warp < 12) {
+        // ================================================= codes to fp16 tiles
+        const int pt = tid - 256;              // 0..127
+        const int ch = pt & 3, r0 = pt >> 2;   // chunks ch, ch + 4 of rows r0 + 32 k
+        constexpr int CC = D / 64;             // chunks of 16 codes of one row that a thread takes
+        uint4 kx[4 * CC], vx[4 * CC];
+        float kfx = 0.0f, vfx = 0.0f;          // factors of column pt
+        const float nan = __int_as_float(0x7fc00000);
+        // (a tile of full pages: the pages of this thread's four rows and of its column, then their codes)
+        auto page_of = [&](int t) -> int64_t { return load_page(c, b, t >> a.log_page); };
+        auto load = [&](int i, bool v) {
+            const int key0 = (t_first + i) * kPrKeys;
+            if (key0 + kPrKeys > paged) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = key0 + r0 + 32 * k;
+                const int64_t p = page_of(t);
+                const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, p < 0 ? 0 : p, h) + (int64_t)(t & (c.P - 1)) * D + ch * 16;
+#pragma unroll
+                for (int q = 0; q < CC; ++q) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(at + 64 * q);
+                    if (v)
+                        vx[k * CC + q] = y;
+                    else
+                        kx[k * CC + q] = y;
+                }
+            }
+            if (!v) {
+                const int64_t p = page_of(key0 + pt);
+                kfx = p < 0 ? nan : c.ks[p * c.Hk + h];
+                vfx = p < 0 ? nan : c.vs[p * c.Hk + h];
+            }
+        };
+        auto store = [&](uint32_t tile, int i, bool v) {
+            const int key0 = (t_first + i) * kPrKeys;
+            float *kf = factors + (i % kPrFactorSlots) * 256;
+            if (key0 + kPrKeys <= paged) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int q = 0; q < CC; ++q) {
+                        const uint4 y = v ? vx[k * CC + q] : kx[k * CC + q];
+                        uint32_t o[8];
+                        codes_to_half<CODE>(code_bias<CODE>(y.x), o[0], o[1]);
+                        codes_to_half<CODE>(code_bias<CODE>(y.y), o[2], o[3]);
+                        codes_to_half<CODE>(code_bias<CODE>(y.z), o[4], o[5]);
+                        codes_to_half<CODE>(code_bias<CODE>(y.w), o[6], o[7]);
+                        const int row = r0 + 32 * k, u = 2 * (ch + 4 * q);
+                        sts128(tile + f16_tile_at(row, u), o[0], o[1], o[2], o[3]);
+                        sts128(tile + f16_tile_at(row, u + 1), o[4], o[5], o[6], o[7]);
+                    }
+                if (!v) {
+                    kf[pt] = kfx;
+                    kf[128 + pt] = vfx;
+                }
+                return;
+            }
+            // a tile that reaches past the full pages: page rows, the ring's rows, and zeros
+            for (int k = 0; k < 4; ++k) {
+                const int row = r0 + 32 * k, t = key0 + row;
+                if (t < paged) {
+                    const int64_t p = page_of(t);
+                    const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, p < 0 ? 0 : p, h) + (int64_t)(t & (c.P - 1)) * D + ch * 16;
+#pragma unroll
+                    for (int q = 0; q < CC; ++q) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(at + 64 * q);
+                        uint32_t o[8];
+                        codes_to_half<CODE>(code_bias<CODE>(y.x), o[0], o[1]);
+                        codes_to_half<CODE>(code_bias<CODE>(y.y), o[2], o[3]);
+                        codes_to_half<CODE>(code_bias<CODE>(y.z), o[4], o[5]);
+                        codes_to_half<CODE>(code_bias<CODE>(y.w), o[6], o[7]);
+                        const int u = 2 * (ch + 4 * q);
+                        sts128(tile + f16_tile_at(row, u), o[0], o[1], o[2], o[3]);
+                        sts128(tile + f16_tile_at(row, u + 1), o[4], o[5], o[6], o[7]);
+                    }
+                    if (ch == 0) kf[(v ? 128 : 0) + row] = p < 0 ? nan : (v ? c.vs : c.ks)[p * c.Hk + h];
+                } else {
+                    const bool in = t < s.len && s.slot >= 0;
+                    const uint16_t *at = (v ? c.vt : c.kt) + ring_at(c, in ? s.slot : 0, h, t) + ch * 16;
+                    uint4 y[CC][2];
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < CC; ++q)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            y[q][e] = in ? *reinterpret_cast<const uint4 *>(at + 64 * q + 8 * e) : make_uint4(0, 0, 0, 0);
+                            amax = fmaxf(amax, amax8(y[q][e], bf16));
+                        }
+                    // (the four threads of a row are neighbours and take this branch together)
+                    const unsigned quad = 0xfu << (lane & 28);
+                    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+                    float mul, f;
+                    row_scale(amax, mul, f);
+                    if (t < s.len && s.slot < 0) f = nan;
+                    if (t >= s.len) f = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < CC; ++q)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            sts128(tile + f16_tile_at(row, 2 * (ch + 4 * q) + e), scale2(y[q][e].x, mul, bf16),
+                                   scale2(y[q][e].y, mul, bf16), scale2(y[q][e].z, mul, bf16), scale2(y[q][e].w, mul, bf16));
+                    if (ch == 0) kf[(v ? 128 : 0) + row] = f;
+                }
+            }
+        };
+        if (nt > 0) {
+            load(0, false);
+            load(0, true);
+        }
+        for (int i = 0; i < nt; ++i) {
+            const int st = i & 1;
+            const bool whole = (t_first + i + 1) * kPrKeys <= paged;
+            if (i >= 2 && !wait(kBarKEmpty + st, ((i >> 1) - 1) & 1)) break;
+            store(base + Cfg::k + st * Cfg::tile, i, false);
+            // the softmax reads the tile's V factors with its K factors, so a tile without a page's scale
+            // for each column has V in place before K is handed on
+            if (!whole) {
+                if (i >= 2 && !wait(kBarVEmpty + st, ((i >> 1) - 1) & 1)) break;
+                store(base + Cfg::v + st * Cfg::tile, i, true);
+            }
+            tc::fence_proxy_async_smem();
+            mbar_arrive(bar(kBarKFull + st));
+            if (i + 1 < nt) load(i + 1, false);
+            if (whole) {
+                if (i >= 2 && !wait(kBarVEmpty + st, ((i >> 1) - 1) & 1)) break;
+                store(base + Cfg::v + st * Cfg::tile, i, true);
+                tc::fence_proxy_async_smem();
+            }
+            mbar_arrive(bar(kBarVFull + st));
+            if (i + 1 < nt) load(i + 1, true);
+        }
+    } else if (lane == 0) {
+        // ================================================= the products
+        constexpr uint32_t id_qk = tc::idesc_f16_f32(128, kPrKeys);
+        constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // V: transposed operand
+        auto qk = [&](int x, int st) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+                tc::mma_f16kind(tmem + x * 128, tc::sdesc_sw128(base + Cfg::q + x * Cfg::tile + at),
+                                tc::sdesc_sw128(base + Cfg::k + st * Cfg::tile + at), id_qk, k > 0);
+            }
+            tc::mma_commit(bar(kBarS + x));
+        };
+        auto pv = [&](int x, int st, bool acc) {
+#pragma unroll
+            for (int k = 0; k < kPrKeys / 16; ++k)
+                mma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + 8 * k,
+                           sdesc_sw128_mn(base + Cfg::v + st * Cfg::tile + k * 2048, 16384), id_pv, acc || k > 0);
+        };
+        if (a.fault) wait_one(kBarNever, 0);
+        if (nt > 0 && wait_one(kBarQ, 0) && wait_one(kBarKFull, 0)) {
+            tc::fence_after_sync();
+            for (int x = 0; x < 2; ++x)
+                if (ntx[x] > 0) qk(x, 0);
+            if (nt > 2) tc::mma_commit(bar(kBarKEmpty));
+            for (int i = 0; i < nt; ++i) {
+                const int st = i & 1;
+                if (!wait_one(kBarVFull + st, (i >> 1) & 1)) break;
+                if (i + 1 < nt && !wait_one(kBarKFull + (st ^ 1), ((i + 1) >> 1) & 1)) break;
+                for (int x = 0; x < 2; ++x) {
+                    if (i >= ntx[x]) continue;
+                    if (!wait_one(kBarP + x, i & 1)) break;
+                    tc::fence_after_sync();
+                    pv(x, st, i > 0);
+                    if (i + 1 < ntx[x])
+                        qk(x, st ^ 1);
+                    else
+                        tc::mma_commit(bar(kBarO + x));
+                }
+                if (!ok) break;
+                // (only what the producers will wait for: nothing arrives after the CTA's end)
+                if (i + 2 < nt) tc::mma_commit(bar(kBarVEmpty + st));
+                if (i + 3 < nt) tc::mma_commit(bar(kBarKEmpty + (st ^ 1)));
+            }
+        }
+        // whatever was issued is over before the tensor memory goes back
+        if (!ok) {
+            tc::mma_commit(bar(kBarNever));
+            mbar_wait_bounded(bar(kBarNever), 0, 4000000000LL);
+        }
+        tc::fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 12) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// The splits' partial sums joined in their order: a thread four values of a row.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
+    const Ctx &c = a.c;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t rh = at / (D / 4);
+    if (rh >= (int64_t)c.T * c.H) return;
+    const int d = (int)(at % (D / 4)) * 4;
+    const int row = (int)(rh / c.H), head = (int)(rh % c.H);
+    // rows of no sequence were not computed: the sequence of a row is the last one that starts at or before it
+    int lo = 0, hi = c.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (c.q_start[mid] <= row)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Seq s = load_seq(c, lo);
+    if (row < s.row0 || row >= s.row0 + s.n) return;
+    const float *ml = a.partial + (int64_t)a.splits * c.T * c.H * D;
+    float m = kNoScore, l = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, ml[((int64_t)k * c.T * c.H + rh) * 2]);
+    for (int k = 0; k < a.splits; ++k) {
+        const int64_t i = (int64_t)k * c.T * c.H + rh;
+        const float2 v = *reinterpret_cast<const float2 *>(ml + i * 2);
+        const float4 y = *reinterpret_cast<const float4 *>(a.partial + i * D + d);
+        const float f = ex2(v.x - m);
+        l = fmaf(v.y, f, l);
+        o.x = fmaf(y.x, f, o.x);
+        o.y = fmaf(y.y, f, o.y);
+        o.z = fmaf(y.z, f, o.z);
+        o.w = fmaf(y.w, f, o.w);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint2 y;
+    if (a.bf16)
+        y = make_uint2(pack2<SI_KV_BF16>(o.x * inv, o.y * inv), pack2<SI_KV_BF16>(o.z * inv, o.w * inv));
+    else
+        y = make_uint2(pack2<SI_KV_F16>(o.x * inv, o.y * inv), pack2<SI_KV_F16>(o.z * inv, o.w * inv));
+    *reinterpret_cast<uint2 *>(a.out.p + row * a.out.row + head * a.out.head + d) = y;
+    if (a.lse && d == 0) a.lse[rh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int CODE, int D>
+cudaError_t prompt_launch(const PromptArgs &a, cudaStream_t s) {
+    using Cfg = PromptCfg<D>;
+    cudaError_t e = cudaFuncSetAttribute(k_kv_prompt<CODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = ((int64_t)a.c.max_new * a.c.G + kPrRows - 1) / kPrRows * a.c.Hk * a.c.B * a.splits;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    k_kv_prompt<CODE, D><<<(unsigned)blocks, kPrThreads, Cfg::smem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+    const int64_t n = (int64_t)a.c.T * a.c.H * (D / 4);
+    k_kv_join<D><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kv
+}  // namespace si

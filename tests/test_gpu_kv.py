@@ -236,6 +236,24 @@ def test_indices_outside_the_cache_are_not_followed():
     run(lambda d: d.q_start.__setitem__(4, 99), 3, False)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_reports_a_wait_that_runs_out(monkeypatch, dim):
+    """The many-row kernel's waits are bounded: with a short budget and a wait that nothing ends, the call
+    returns, the status says so, and the next call (of a plan without the test mode) is right."""
+    shape = Shape(8, 2, dim, 64, "int8", "bf16")
+    c = ref.make_cache(shape, [500], [200], seed=3)
+    q, qd = make_q(c, 4)
+    monkeypatch.setenv("SI_FAULT_WAIT_BUDGET", "20000")
+    d = Dev(c)
+    d.attend(qd, 0.1)
+    assert d.status() == si.SI_ERR_TIMEOUT
+    monkeypatch.delenv("SI_FAULT_WAIT_BUDGET")
+    d = Dev(c)
+    out, lse = d.attend(qd, 0.1)
+    check_attend(c, out, lse, q, 0.1)
+    assert d.status() == si.SI_OK
+
+
 def test_refusals_launch_nothing_on_the_device():
     from test_kv_host import Call, refusals
     plan = si.si_kv_plan(si.make_kv_desc(8, 2, 128, 64))
