@@ -19,12 +19,12 @@
 //  * A warp owns 16 of a unit's 64 tokens (one page: P >= 16) and copies them
 //    into its own ring in shared memory (cp.async, several units ahead): no
 //    barrier between warps inside an item.
-//  * The maximum is lazy: m moves only when a score passes it by more than 8
-//    (a vote a tile instead of shuffles), and p stays below 2^8.
+//  * The maximum is lazy: m moves only when a score passes it by more than 4
+//    (a vote a tile instead of shuffles), and p stays below 2^4.
 //  * p times the page's V scale is rounded to fp16 for the second product.  The
-//    scale is taken relative to a running reference, so that the products stay
-//    inside fp16: p < 2^8, scale/reference <= 4, times 2^4: at most 2^14; a
-//    weight of one keeps its eleven bits down to a relative scale of 2^-18.
+//    scale is taken relative to the largest so far, so that the products stay
+//    inside fp16: p < 2^4, scale/reference <= 1, times 2^11: at most 2^15; a
+//    weight of one keeps its eleven bits down to a relative scale of 2^-25.
 //    (bf16 weights, without the reference, have eight: half a step of the
 //    output's own rounding, or eight steps for an fp16 output.)
 #pragma once
@@ -36,6 +36,7 @@ namespace kv {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 4.0f, kWeightUnit = 2048.0f;
 constexpr float kNoScore = -1e30f;  // a running maximum before the first score
 
 template <int D, int MT>
@@ -219,13 +220,13 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
             m[mt][0] = m[mt][1] = kNoScore;
             l[mt][0] = l[mt][1] = 0.0f;
         }
-        float v_ref = 1e-30f;  // what o is in units of (times 2^-4)
+        float v_ref = 1e-30f;  // the largest V scale so far: o is in units of v_ref / kWeightUnit
 
         // Scores to weights: s (raw products) times the columns' factors and the rows', masked at the
         // rows' limits; updates m, l, and o's scale; returns the second product's operand.
         auto weights = [&](float (&sc)[MT][2][4], const float (&kf)[4], const float (&vf)[4], float v_top, int t0,
                            bool masked, uint32_t (&pa)[MT][4]) {
-            if (v_top > 4.0f * v_ref) {
+            if (v_top > v_ref) {
                 const float f = v_ref / v_top;
                 v_ref = v_top;
 #pragma unroll
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
             }
-            const float inv = 16.0f / v_ref;
+            const float inv = kWeightUnit / v_ref;
             bool over = false;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
                 for (int e = 0; e < 2; ++e) {
                     const float top = fmaxf(fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]),
                                             fmaxf(sc[mt][1][2 * e], sc[mt][1][2 * e + 1]));
-                    over |= top > m[mt][e] + 8.0f;
+                    over |= top > m[mt][e] + kLazy;
                 }
             }
             if (__any_sync(0xffffffffu, over)) {
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
                 float top = s_ml[0][r][0];
 #pragma unroll
                 for (int k = 1; k < kDecWarps; ++k) top = fmaxf(top, s_ml[k][r][0]);
-                const float f = ex2(m[mt][e] - top) * v_ref * 0.0625f;
+                const float f = ex2(m[mt][e] - top) * (v_ref / kWeightUnit);
                 float *to = merge + (w * R + r) * D;
                 // column 2j (and 2j + 1) of tile nt is d = n * run + nt within its 128 (or 64)
                 constexpr int run = D == 64 ? 8 : 16;

@@ -18,12 +18,12 @@
 // the two have to overlap; at D = 64 the exponential alone bounds it.
 #pragma once
 #include "si_kv_decode.cuh"
-#include "si_tc.cuh"
+#include "si_kv_tc.cuh"
 
 namespace si {
 namespace kv {
 
-constexpr int kPrRows = 256, kPrKeys = 128;
+constexpr int kPrRows = 256, kPrKeys = kTileRows;
 constexpr int kPrThreads = 13 * 32;
 constexpr int kPrFactorSlots = 4;
 
@@ -51,73 +51,6 @@ struct PromptArgs {
     long long budget;
     float *partial;  // [splits][T][H][D], then [splits][T][H][2]
 };
-
-// Tensor-memory stores and the product with its first operand in tensor memory.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
-}
-// Descriptor of an operand whose 64 innermost values (128 swizzled bytes) run
-// along M or N: 8-row groups of K follow each other at 1024 bytes (stride
-// offset), the next 64 values along M or N lie `next` bytes on (leading offset).
-__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t smem_addr, uint32_t next) {
-    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(next >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-
-// Byte offset of 16-byte unit u (8 values of d) of row r in an fp16 tile of 128
-// rows: 64 values of d (128 bytes) a row and half, halves 16 KB apart.
-__device__ __forceinline__ uint32_t f16_tile_at(int r, int u) {
-    return (uint32_t)((u >> 3) * 16384 + r * 128 + (((u ^ r) & 7) << 4));
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pk2(float a, float b) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void up2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 template <int CODE, int D>
 __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a) {
@@ -264,7 +197,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 }
             }
             top *= qf;
-            const bool grow = top > m + 8.0f, scale = v_top > 4.0f * v_ref;
+            const bool grow = top > m + kLazy, scale = v_top > v_ref;
             if (__any_sync(0xffffffffu, grow || scale)) {
                 float f = 1.0f;
                 if (grow) {
@@ -288,7 +221,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     }
                 }
             }
-            const float inv = 16.0f / v_ref;
+            const float inv = kWeightUnit / v_ref;
             const f32x2 m2 = pk2(-m, -m);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -338,7 +271,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         up2(l2, l, l_odd);
         l += l_odd;
         if (ok) {
-            const float f = v_ref * 0.0625f, inv = l == 0.0f ? 0.0f : f / l;
+            const float f = v_ref / kWeightUnit, inv = l == 0.0f ? 0.0f : f / l;
             if (a.splits == 1) {
                 uint16_t *dst = a.out.p + row * a.out.row + head * a.out.head;
 #pragma unroll
@@ -430,14 +363,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
 #pragma unroll
                     for (int q = 0; q < CC; ++q) {
                         const uint4 y = v ? vx[k * CC + q] : kx[k * CC + q];
-                        uint32_t o[8];
-                        codes_to_half<CODE>(code_bias<CODE>(y.x), o[0], o[1]);
-                        codes_to_half<CODE>(code_bias<CODE>(y.y), o[2], o[3]);
-                        codes_to_half<CODE>(code_bias<CODE>(y.z), o[4], o[5]);
-                        codes_to_half<CODE>(code_bias<CODE>(y.w), o[6], o[7]);
-                        const int row = r0 + 32 * k, u = 2 * (ch + 4 * q);
-                        sts128(tile + f16_tile_at(row, u), o[0], o[1], o[2], o[3]);
-                        sts128(tile + f16_tile_at(row, u + 1), o[4], o[5], o[6], o[7]);
+                        codes_to_tile<CODE>(y, tile, r0 + 32 * k, 2 * (ch + 4 * q));
                     }
                 if (!v) {
                     kf[pt] = kfx;
@@ -445,54 +371,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 }
                 return;
             }
-            // a tile that reaches past the full pages: page rows, the ring's rows, and zeros
-            for (int k = 0; k < 4; ++k) {
-                const int row = r0 + 32 * k, t = key0 + row;
-                if (t < paged) {
-                    const int64_t p = page_of(t);
-                    const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, p < 0 ? 0 : p, h) + (int64_t)(t & (c.P - 1)) * D + ch * 16;
-#pragma unroll
-                    for (int q = 0; q < CC; ++q) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(at + 64 * q);
-                        uint32_t o[8];
-                        codes_to_half<CODE>(code_bias<CODE>(y.x), o[0], o[1]);
-                        codes_to_half<CODE>(code_bias<CODE>(y.y), o[2], o[3]);
-                        codes_to_half<CODE>(code_bias<CODE>(y.z), o[4], o[5]);
-                        codes_to_half<CODE>(code_bias<CODE>(y.w), o[6], o[7]);
-                        const int u = 2 * (ch + 4 * q);
-                        sts128(tile + f16_tile_at(row, u), o[0], o[1], o[2], o[3]);
-                        sts128(tile + f16_tile_at(row, u + 1), o[4], o[5], o[6], o[7]);
-                    }
-                    if (ch == 0) kf[(v ? 128 : 0) + row] = p < 0 ? nan : (v ? c.vs : c.ks)[p * c.Hk + h];
-                } else {
-                    const bool in = t < s.len && s.slot >= 0;
-                    const uint16_t *at = (v ? c.vt : c.kt) + ring_at(c, in ? s.slot : 0, h, t) + ch * 16;
-                    uint4 y[CC][2];
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < CC; ++q)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            y[q][e] = in ? *reinterpret_cast<const uint4 *>(at + 64 * q + 8 * e) : make_uint4(0, 0, 0, 0);
-                            amax = fmaxf(amax, amax8(y[q][e], bf16));
-                        }
-                    // (the four threads of a row are neighbours and take this branch together)
-                    const unsigned quad = 0xfu << (lane & 28);
-                    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
-                    float mul, f;
-                    row_scale(amax, mul, f);
-                    if (t < s.len && s.slot < 0) f = nan;
-                    if (t >= s.len) f = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < CC; ++q)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            sts128(tile + f16_tile_at(row, 2 * (ch + 4 * q) + e), scale2(y[q][e].x, mul, bf16),
-                                   scale2(y[q][e].y, mul, bf16), scale2(y[q][e].z, mul, bf16), scale2(y[q][e].w, mul, bf16));
-                    if (ch == 0) kf[(v ? 128 : 0) + row] = f;
-                }
-            }
+            key_rows<CODE, D>(c, s, b, h, v, key0, a.log_page, bf16, tile, kf + (v ? 128 : 0), pt);
         };
         if (nt > 0) {
             load(0, false);

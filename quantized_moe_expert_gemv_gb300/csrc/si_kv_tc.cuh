@@ -1,0 +1,152 @@
+// si_kv_tc.cuh -- pieces of the cache's tcgen05 kernels: tensor-memory stores,
+// the product with its first operand in tensor memory, fp16 operand tiles in
+// shared memory and their making from codes and 16-bit rows, packed fp32 pairs.
+#pragma once
+#include "si_kv_mma.cuh"
+#include "si_tc.cuh"
+
+namespace si {
+namespace kv {
+
+constexpr int kTileRows = 128;  // rows of an operand tile
+
+// Tensor-memory stores and the product with its first operand in tensor memory.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// Descriptor of an operand whose 64 innermost values (128 swizzled bytes) run
+// along M or N: 8-row groups of K follow each other at 1024 bytes (stride
+// offset), the next 64 values along M or N lie `next` bytes on (leading offset).
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t smem_addr, uint32_t next) {
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(next >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// Byte offset of 16-byte unit u (8 values of d) of row r in an fp16 tile of 128
+// rows: 64 values of d (128 bytes) a row and half, halves 16 KB apart.
+__device__ __forceinline__ uint32_t f16_tile_at(int r, int u) {
+    return (uint32_t)((u >> 3) * 16384 + r * 128 + (((u ^ r) & 7) << 4));
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pk2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void up2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// One row of 16-bit values into an fp16 tile, by the four neighbouring threads
+// ch = 0..3 of its quad (each D/4 values); returns the factor that undoes the scaling.
+template <int D>
+__device__ __forceinline__ float row_to_tile(const uint16_t *src, bool live, uint32_t tile, int row, int ch, bool bf16) {
+    constexpr int CC = D / 64;
+    uint4 y[CC][2];
+    float amax = 0.0f;
+#pragma unroll
+    for (int q = 0; q < CC; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            y[q][e] = live ? *reinterpret_cast<const uint4 *>(src + ch * 16 + 64 * q + 8 * e) : make_uint4(0, 0, 0, 0);
+            amax = fmaxf(amax, amax8(y[q][e], bf16));
+        }
+    const unsigned quad = 0xfu << (threadIdx.x & 28);  // (the quad may be apart from the rest of its warp)
+    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+    float mul, f;
+    row_scale(amax, mul, f);
+#pragma unroll
+    for (int q = 0; q < CC; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            sts128(tile + f16_tile_at(row, 2 * (ch + 4 * q) + e), scale2(y[q][e].x, mul, bf16), scale2(y[q][e].y, mul, bf16),
+                   scale2(y[q][e].z, mul, bf16), scale2(y[q][e].w, mul, bf16));
+    return f;
+}
+
+// 16 codes (chunk u/2 of a row) into units u and u + 1 of an fp16 tile.
+template <int CODE>
+__device__ __forceinline__ void codes_to_tile(const uint4 &y, uint32_t tile, int row, int u) {
+    uint32_t o[8];
+    codes_to_half<CODE>(code_bias<CODE>(y.x), o[0], o[1]);
+    codes_to_half<CODE>(code_bias<CODE>(y.y), o[2], o[3]);
+    codes_to_half<CODE>(code_bias<CODE>(y.z), o[4], o[5]);
+    codes_to_half<CODE>(code_bias<CODE>(y.w), o[6], o[7]);
+    sts128(tile + f16_tile_at(row, u), o[0], o[1], o[2], o[3]);
+    sts128(tile + f16_tile_at(row, u + 1), o[4], o[5], o[6], o[7]);
+}
+
+// The K (or V) rows of tokens key0 .. key0 + 127 of one kv head into an fp16
+// tile, and a factor for each, by 128 threads (pt): page rows, the unfinished page's
+// rows, zeros past the length.
+template <int CODE, int D>
+__device__ __forceinline__ void key_rows(const Ctx &c, const Seq &s, int b, int h, bool v, int key0, int log_page, bool bf16,
+                                         uint32_t tile, float *factor, int pt) {
+    constexpr int CC = D / 64;
+    const int ch = pt & 3, r0 = pt >> 2, paged = s.len & ~(c.P - 1);
+    const float nan = __int_as_float(0x7fc00000);
+    for (int k = 0; k < 4; ++k) {
+        const int row = r0 + 32 * k, t = key0 + row;
+        float f;
+        if (t < paged) {
+            const int64_t p = load_page(c, b, t >> log_page);
+            const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, p < 0 ? 0 : p, h) + (int64_t)(t & (c.P - 1)) * D + ch * 16;
+            uint4 y[CC];
+#pragma unroll
+            for (int q = 0; q < CC; ++q) y[q] = *reinterpret_cast<const uint4 *>(at + 64 * q);
+#pragma unroll
+            for (int q = 0; q < CC; ++q) codes_to_tile<CODE>(y[q], tile, row, 2 * (ch + 4 * q));
+            f = p < 0 ? nan : (v ? c.vs : c.ks)[p * c.Hk + h];
+        } else {
+            const bool in = t < s.len && s.slot >= 0;
+            f = row_to_tile<D>((v ? c.vt : c.kt) + ring_at(c, in ? s.slot : 0, h, t), in, tile, row, ch, bf16);
+            if (t < s.len && s.slot < 0) f = nan;
+            if (t >= s.len) f = 0.0f;
+        }
+        if (ch == 0) factor[row] = f;
+    }
+}
+
+}  // namespace kv
+}  // namespace si

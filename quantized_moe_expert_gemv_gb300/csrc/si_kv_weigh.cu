@@ -1,62 +1,500 @@
-// si_kv_weigh.cu -- the attention weights of each cached token, added to its running sum.
-#include "si_kv_device.cuh"
+// si_kv_weigh.cu -- the attention weights of each cached token, added to its
+// running sum:
+//   acc_out_t = decay acc_in_t + sum over the rows r that see t of 2^(f S_tr - lse_r log2 e).
+// A token's sum is taken by one thread (or four neighbours) in the rows' order:
+// no atomics, the same bits for the same inputs.
+//
+// Few rows (k_kv_weigh_few): bound by HBM, D bytes of K codes a token.  The
+// warp-level product has the keys as its 16 rows and q's rows as its 8 columns,
+// so that a step of 8 query heads wastes none of it; units of 64 tokens are
+// dealt out evenly over the GPU as in the few-row attention, and nothing has to
+// be joined.
+// Many rows (k_kv_weigh_many, more than 64, head_dim 64 and 128): bound by the
+// exponential (16 a cycle and SM).  One CTA for 128 tokens: S^T = K Q^T on the
+// tcgen05 tensor cores, K's tile staying and q's tiles following each other
+// through two stages; a thread holds one token's sum and walks its row of
+// tensor memory.  Two CTAs fit an SM, so one's loads run under the other's sums.
+#include "si_kv_decode.cuh"
+#include "si_kv_tc.cuh"
 
 namespace si {
 namespace kv {
 
-constexpr int kThreads = 128;
+struct WeighArgs {
+    Ctx c;
+    Rows q;
+    const float *lse, *acc_in;
+    float *acc_out;
+    int64_t acc_stride;
+    float decay, scale2;
+    int bf16, log_page, fault;
+    long long budget;
+};
 
-// One CTA for each (sequence, kv head, 128 tokens), a thread a token, the rows one after the other.
-template <int CODE, int DT>
-__global__ void __launch_bounds__(kThreads) k_kv_weigh(Ctx c, Rows q, const float *lse, const float *acc_in,
-                                                       float *acc_out, int64_t acc_stride, float decay, float sm) {
-    __shared__ float s_q[256];
-    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, D = c.D, P = c.P;
-    const Seq s = load_seq(c, b);
-    const int t = blockIdx.x * kThreads + tid;
-    if (blockIdx.x * kThreads >= s.len) return;
-    const bool live = t < s.len;
-    const int old = s.len - s.n, paged = s.len / P * P;
-    const int64_t page = live && t < paged ? load_page(c, b, t / P) : -1;
-    float sum = 0.0f;
-    for (int i = 0; i < s.n; ++i)
-        for (int g = 0; g < c.G; ++g) {
-            const int head = h * c.G + g, row = s.row0 + i;
-            __syncthreads();
-            for (int d = tid; d < D; d += kThreads) s_q[d] = to_float<DT>(q.p[row * q.row + head * q.head + d]);
-            __syncthreads();
-            if (!live || t > old + i) continue;
-            float dot = 0.0f;
-            if (t < paged) {
-                if (page < 0) dot = NAN;
-                else {
-                    const uint8_t *k = c.kc + page_at(c, page, h) + (int64_t)(t % P) * D;
-                    for (int d = 0; d < D; ++d) dot = fmaf(s_q[d], code_value<CODE>(k[d]), dot);
-                    dot *= c.ks[page * c.Hk + h];
-                }
-            } else if (s.slot < 0) dot = NAN;
-            else {
-                const uint16_t *k = c.kt + ring_at(c, s.slot, h, t);
-                for (int d = 0; d < D; ++d) dot = fmaf(s_q[d], to_float<DT>(k[d]), dot);
-            }
-            sum += expf(dot * sm - lse[(int64_t)row * c.H + head]);
+constexpr int kWeighRows = 64;  // rows whose operand lies in shared memory at a time
+
+template <int D>
+struct WeighCfg {
+    static constexpr int stage = 16 * D;  // a warp's 16 keys
+    static constexpr int stages = D == 256 ? 4 : 8;
+    static constexpr int ring = kDecWarps * stages * stage;
+    static constexpr int q_bytes = kWeighRows / 8 * (D / 16) * 256;
+    static constexpr int smem = ring + q_bytes + kWeighRows * 8;
+    static constexpr int ctas = D == 64 ? 6 : D == 128 ? 4 : 2;
+};
+
+template <int CODE, int D>
+__global__ void __launch_bounds__(kDecThreads, WeighCfg<D>::ctas) k_kv_weigh_few(const WeighArgs a) {
+    using Cfg = WeighCfg<D>;
+    constexpr int KS = D / 16, CH = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_scan[kDecWarps];
+    __shared__ long long s_off;
+    __shared__ int s_b;
+    const Ctx &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
+    const bool bf16 = a.bf16;
+
+    // ---- this CTA's share of the units (64 tokens of a kv head; the unfinished page is one)
+    const int per = (c.B + kDecThreads - 1) / kDecThreads;
+    auto units_of = [&](int b) -> long long { return (long long)seq_tiles(c, load_seq(c, b).len) * c.Hk; };
+    long long mine = 0;
+    for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) mine += units_of(b);
+    long long incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_scan[w] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+    for (int k = 0; k < kDecWarps; ++k) {
+        if (k < w) before += s_scan[k];
+        total += s_scan[k];
+    }
+    const long long N = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+    if (blockIdx.x >= N) return;
+    const long long u_begin = blockIdx.x * total / N, u_end = (blockIdx.x + 1) * total / N;
+    if (before <= u_begin && u_begin < before + mine) {
+        int b = tid * per;
+        long long at = before, n;
+        while (at + (n = units_of(b)) <= u_begin) {
+            at += n;
+            ++b;
         }
-    if (!live) return;
-    const int64_t at = ((int64_t)b * c.Hk + h) * acc_stride + t;
-    acc_out[at] = (acc_in && t < old ? decay * acc_in[at] : 0.0f) + sum;
+        s_b = b;
+        s_off = u_begin - at;
+    }
+    __syncthreads();
+    int b = s_b;
+    long long off = s_off, u = u_begin;
+    const uint32_t ring = smem_addr(smem) + w * (Cfg::stages * Cfg::stage);
+    uint8_t *q_smem = smem + Cfg::ring;
+    float2 *rowf = reinterpret_cast<float2 *>(smem + Cfg::ring + Cfg::q_bytes);  // factor, lse log2 e
+
+    while (u < u_end) {
+        const Seq s = load_seq(c, b);
+        const int tiles = seq_tiles(c, s.len);
+        const long long n_units = (long long)tiles * c.Hk;
+        if (off >= n_units) {
+            off -= n_units;
+            ++b;
+            continue;
+        }
+        const int h = (int)(off / tiles), t_first = (int)(off % tiles);
+        const int t_end = (int)min((long long)tiles, t_first + (u_end - u));
+        const int paged = s.len & ~(c.P - 1), old = s.len - s.n, paged_tiles = (paged + 63) / 64;
+        const int all_rows = s.n * c.G;
+        const int64_t acc_at = ((int64_t)b * c.Hk + h) * a.acc_stride;
+
+        // rows in blocks of 64 (one block, but for many rows of 256 values): the first takes up the earlier sums
+        for (int rb = 0; rb == 0 || rb * kWeighRows < all_rows; ++rb) {
+            const int rows = min(kWeighRows, all_rows - rb * kWeighRows), nts = (rows + 7) / 8;
+            const int lim_min = old + rb * kWeighRows / c.G + 1;
+            __syncthreads();  // the last block's readers are done
+            for (int nt = w; nt < nts; nt += kDecWarps) {
+                const int r = nt * 8 + g, rr = rb * kWeighRows + r;
+                const bool live = r < rows;
+                const int i = live ? rr / c.G : 0, head = live ? h * c.G + rr % c.G : 0;
+                const uint16_t *src = a.q.p + (s.row0 + i) * a.q.row + head * a.q.head;
+                uint4 x[D / 32];
+                float amax = 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
+                        amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
+                    }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                float mul, f;
+                row_scale(amax, mul, f);
+                if (j == 0)  // (a row that pads weighs nothing)
+                    rowf[r] = live ? make_float2(f * a.scale2, a.lse[(int64_t)(s.row0 + i) * c.H + head] * kLog2e)
+                                   : make_float2(0.0f, INFINITY);
+#pragma unroll
+                for (int st = 0; st < KS; ++st) {
+                    const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
+                    *reinterpret_cast<uint2 *>(q_smem + (nt * KS + st) * 256 + lane * 8) =
+                        make_uint2(scale2(st & 1 ? v.z : v.x, mul, bf16), scale2(st & 1 ? v.w : v.y, mul, bf16));
+                }
+            }
+            __syncthreads();
+
+            // the sums of this warp's 16 keys from t0 on; lane < 16 has the earlier sum of key t0 + lane in `was`
+            auto sums = [&](const uint32_t (&ka)[KS][4], float kf0, float kf1, int t0, bool masked, float was) {
+                float sum[2] = {0.0f, 0.0f};
+                for (int nt = 0; nt < nts; ++nt) {
+                    float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int st = 0; st < KS; ++st) {
+                        const uint2 q2 = *reinterpret_cast<const uint2 *>(q_smem + (nt * KS + st) * 256 + lane * 8);
+                        mma16816(sc, ka[st], q2.x, q2.y);
+                    }
+                    const float4 rf = *reinterpret_cast<const float4 *>(rowf + nt * 8 + 2 * j);
+                    float p[4] = {ex2(fmaf(sc[0], kf0 * rf.x, -rf.y)), ex2(fmaf(sc[1], kf0 * rf.z, -rf.w)),
+                                  ex2(fmaf(sc[2], kf1 * rf.x, -rf.y)), ex2(fmaf(sc[3], kf1 * rf.z, -rf.w))};
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = rb * kWeighRows + nt * 8 + 2 * j + (e & 1);
+                            if (t0 + g + 8 * (e >> 1) > old + r / c.G || r >= all_rows) p[e] = 0.0f;
+                        }
+                    }
+                    sum[0] += p[0] + p[1];
+                    sum[1] += p[2] + p[3];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+                    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+                }
+                const float lo = __shfl_sync(0xffffffffu, sum[0], (lane & 7) * 4), hi = __shfl_sync(0xffffffffu, sum[1], (lane & 7) * 4);
+                if (lane < 16 && t0 + lane < s.len) a.acc_out[acc_at + t0 + lane] = was + (lane < 8 ? lo : hi);
+            };
+            auto earlier = [&](int t0) -> float {
+                const int t = t0 + lane;
+                if (lane >= 16 || t >= s.len) return 0.0f;
+                if (rb > 0) return a.acc_out[acc_at + t];
+                return a.acc_in && t < old ? a.decay * a.acc_in[acc_at + t] : 0.0f;
+            };
+
+            const int t_stop = min(t_end, paged_tiles), count = t_stop - t_first;
+            int pid0 = -2, pid1 = -2;
+            float ks0 = 0.0f, ks1 = 0.0f;
+            auto fetch = [&](int set, int first) {
+                const int t = first + lane, token = (t_first + t) * 64 + 16 * w;
+                int p = -2;
+                if (t < count && token < paged) p = (int)load_page(c, b, token >> a.log_page);
+                const float f = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : __int_as_float(0x7fc00000);
+                if (set) {
+                    pid1 = p;
+                    ks1 = f;
+                } else {
+                    pid0 = p;
+                    ks0 = f;
+                }
+            };
+            auto copy = [&](int t) {
+                if (t < count) {
+                    const int p = __shfl_sync(0xffffffffu, (t & 32) ? pid1 : pid0, t & 31);
+                    if (p >= 0) {
+                        const int64_t at = page_at(c, p, h) + (int64_t)(((t_first + t) * 64 + 16 * w) & (c.P - 1)) * D;
+                        const uint32_t to = ring + (t % Cfg::stages) * Cfg::stage;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            const int ci = lane + 32 * k;
+                            cp_async16(to + tile_at<D>(ci / CH, ci % CH), c.kc + at + ci * 16);
+                        }
+                    }
+                }
+                cp_async_commit();
+            };
+            float was = 0.0f, was_next = 0.0f;
+            if (count > 0) {
+                fetch(0, 0);
+                fetch(1, 32);
+#pragma unroll
+                for (int t = 0; t < Cfg::stages - 1; ++t) copy(t);
+                was_next = earlier(t_first * 64 + 16 * w);
+            }
+            for (int t = 0; t < count; ++t) {
+                if ((t & 31) == 0 && t > 0) fetch(((t >> 5) + 1) & 1, (t & ~31) + 32);
+                copy(t + Cfg::stages - 1);
+                was = was_next;
+                if (t + 1 < count) was_next = earlier((t_first + t + 1) * 64 + 16 * w);
+                cp_async_wait<Cfg::stages - 1>();
+                __syncwarp();
+                const int p = __shfl_sync(0xffffffffu, (t & 32) ? pid1 : pid0, t & 31);
+                const float ks = __shfl_sync(0xffffffffu, (t & 32) ? ks1 : ks0, t & 31);
+                const int t0 = (t_first + t) * 64 + 16 * w;
+                if (p == -2) continue;
+                const uint32_t kt = ring + (t % Cfg::stages) * Cfg::stage;
+                uint32_t ka[KS][4];
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        uint4 x = lds128(kt + tile_at<D>(8 * n + g, k_dim<D>(j, i) / 16));
+                        if (p < 0) x = make_uint4(0, 0, 0, 0);  // (a page outside the cache: its factor is NaN)
+                        codes_to_half<CODE>(code_bias<CODE>(x.x), ka[4 * i][n], ka[4 * i][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.y), ka[4 * i + 1][n], ka[4 * i + 1][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.z), ka[4 * i + 2][n], ka[4 * i + 2][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.w), ka[4 * i + 3][n], ka[4 * i + 3][2 + n]);
+                    }
+                sums(ka, ks, ks, t0, t0 + 16 > lim_min, was);
+                __syncwarp();
+            }
+            cp_async_wait<0>();
+
+            // ---- the unfinished page's rows
+            const int tail = s.len - paged, key0 = 16 * w;
+            if (t_end > paged_tiles && key0 < tail) {
+                uint32_t ka[KS][4];
+                float kf[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int key = key0 + 8 * n + g;
+                    const bool live = key < tail && s.slot >= 0;
+                    const uint16_t *src = c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0));
+                    uint4 x[D / 32];
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
+                            amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
+                        }
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                    float mul;
+                    row_scale(amax, mul, kf[n]);
+                    if (s.slot < 0) kf[n] = __int_as_float(0x7fc00000);
+#pragma unroll
+                    for (int st = 0; st < KS; ++st) {
+                        const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
+                        ka[st][n] = scale2(st & 1 ? v.z : v.x, mul, bf16);
+                        ka[st][2 + n] = scale2(st & 1 ? v.w : v.y, mul, bf16);
+                    }
+                }
+                sums(ka, kf[0], kf[1], paged + key0, true, earlier(paged + key0));
+            }
+        }
+        u += t_end - t_first;
+        off += t_end - t_first;
+    }
+}
+
+// ------------------------------------------------------------------ many rows
+constexpr int kWmThreads = 9 * 32;
+template <int D>
+struct WeighManyCfg {
+    static constexpr int tile = kTileRows * D * 2;
+    static constexpr int q = tile;
+    static constexpr int rows = q + 2 * tile;                 // [4][128] (factor, lse)
+    static constexpr int keyf = rows + 4 * 128 * 8;           // [128]
+    static constexpr int bars = keyf + 128 * 4;
+    static constexpr int smem = bars + 16 * 8 + 1024;
+};
+enum WeighBar { kWbK = 0, kWbQFull = 1, kWbQEmpty = 3, kWbSFull = 5, kWbSEmpty = 7, kWbNever = 9 };
+
+template <int CODE, int D>
+__global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs a) {
+    using Cfg = WeighManyCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem;
+    const Ctx &c = a.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.z, h = blockIdx.y, key0 = blockIdx.x * kTileRows;
+    const Seq s = load_seq(c, b);
+    if (key0 >= s.len) return;
+    const int old = s.len - s.n, all_rows = s.n * c.G;
+    // the first row that sees the tile's first key, in tiles of 128 rows
+    const int first = max(0, key0 - old) * c.G / kTileRows;
+    const int nt = max(0, (all_rows + kTileRows - 1) / kTileRows - first);
+
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t *aligned = smem_raw + (base - smem_addr(smem_raw));
+    float2 *rowf = reinterpret_cast<float2 *>(aligned + Cfg::rows);
+    float *keyf = reinterpret_cast<float *>(aligned + Cfg::keyf);
+    auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
+    if (tid == 0) {
+        mbar_init(bar(kWbK), 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kWbQFull + i), 128);
+            mbar_init(bar(kWbQEmpty + i), 1);
+            mbar_init(bar(kWbSFull + i), 1);
+            mbar_init(bar(kWbSEmpty + i), 128);
+        }
+        mbar_init(bar(kWbNever), 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tc::tmem_alloc(smem_addr(&s_tmem), 256);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    auto wait = [&](int i, int parity) {
+        if (ok && !mbar_wait_warp(bar(i), (uint32_t)parity, a.budget)) {
+            ok = false;
+            if (lane == 0) set_status(c.status, SI_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+    auto wait_one = [&](int i, int parity) {
+        if (ok && !mbar_wait_spin(bar(i), (uint32_t)parity, a.budget)) {
+            ok = false;
+            set_status(c.status, SI_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+
+    if (warp < 4) {
+        // ================================================= a thread a key
+        const int t = key0 + tid;
+        const int64_t at = ((int64_t)b * c.Hk + h) * a.acc_stride + t;
+        const float was = t < old && a.acc_in ? a.decay * a.acc_in[at] : 0.0f;
+        const int r_min = max(0, t - old) * c.G;  // the first row that sees the key
+        const uint32_t ts = tmem + ((uint32_t)(32 * warp) << 16);
+        f32x2 sum = pk2(0.0f, 0.0f);
+        float kf = 0.0f;
+        if (wait(kWbK, 0)) kf = keyf[tid];
+        const f32x2 kf2 = pk2(kf, kf);
+        for (int i = 0; i < nt; ++i) {
+            if (!wait(kWbSFull + (i & 1), (i >> 1) & 1)) break;
+            tc::fence_after_sync();
+            const int r0 = (first + i) * kTileRows;
+            const float4 *rf = reinterpret_cast<const float4 *>(rowf + (i & 3) * 128);  // two rows each
+            const bool all = __all_sync(0xffffffffu, r0 >= r_min);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t z[32];
+                tc::tmem_ld32(ts + (i & 1) * 128 + 32 * q, z);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const float4 v = rf[16 * q + k / 2];
+                    const f32x2 f2 = mul2(kf2, pk2(v.x, v.z));
+                    const f32x2 e = fma2(pk2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), f2, pk2(-v.y, -v.w));
+                    float e0, e1;
+                    up2(e, e0, e1);
+                    float p0 = ex2(e0), p1 = ex2(e1);
+                    if (!all) {
+                        if (r0 + 32 * q + k < r_min) p0 = 0.0f;
+                        if (r0 + 32 * q + k + 1 < r_min) p1 = 0.0f;
+                    }
+                    sum = add2(sum, pk2(p0, p1));
+                }
+            }
+            tc::fence_before_sync();
+            mbar_arrive(bar(kWbSEmpty + (i & 1)));
+        }
+        float x, y;
+        up2(sum, x, y);
+        if (ok && t < s.len) a.acc_out[at] = was + (x + y);
+    } else if (warp < 8) {
+        // ================================================= K's tile, then q's
+        const int pt = tid - 128, ch = pt & 3;
+        key_rows<CODE, D>(c, s, b, h, false, key0, a.log_page, a.bf16, base, keyf, pt);
+        tc::fence_proxy_async_smem();
+        mbar_arrive(bar(kWbK));
+        for (int i = 0; i < nt; ++i) {
+            if (i >= 2 && !wait(kWbQEmpty + (i & 1), ((i >> 1) - 1) & 1)) break;
+            for (int k = 0; k < 4; ++k) {
+                const int r = (pt >> 2) + 32 * k, rr = (first + i) * kTileRows + r;
+                const bool live = rr < all_rows;
+                const int row = s.row0 + (live ? rr / c.G : 0), head = h * c.G + (live ? rr % c.G : 0);
+                const float f = row_to_tile<D>(a.q.p + row * a.q.row + head * a.q.head, live, base + Cfg::q + (i & 1) * Cfg::tile,
+                                               r, ch, a.bf16);
+                if (ch == 0)
+                    rowf[(i & 3) * 128 + r] = live ? make_float2(f * a.scale2, a.lse[(int64_t)row * c.H + head] * kLog2e)
+                                                   : make_float2(0.0f, INFINITY);
+            }
+            tc::fence_proxy_async_smem();
+            mbar_arrive(bar(kWbQFull + (i & 1)));
+        }
+    } else if (lane == 0) {
+        // ================================================= the products
+        constexpr uint32_t id = tc::idesc_f16_f32(128, kTileRows);
+        if (a.fault) wait_one(kWbNever, 0);
+        if (wait_one(kWbK, 0))
+            for (int i = 0; i < nt; ++i) {
+                const int st = i & 1;
+                if (!wait_one(kWbQFull + st, (i >> 1) & 1)) break;
+                if (i >= 2 && !wait_one(kWbSEmpty + st, ((i >> 1) - 1) & 1)) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+                    tc::mma_f16kind(tmem + st * 128, tc::sdesc_sw128(base + at),
+                                    tc::sdesc_sw128(base + Cfg::q + st * Cfg::tile + at), id, k > 0);
+                }
+                tc::mma_commit(bar(kWbSFull + st));
+                if (i + 2 < nt) tc::mma_commit(bar(kWbQEmpty + st));
+            }
+        if (!ok) {  // whatever was issued is over before the tensor memory goes back
+            tc::mma_commit(bar(kWbNever));
+            mbar_wait_bounded(bar(kWbNever), 0, 4000000000LL);
+        }
+        tc::fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 8) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 256);
+    }
+}
+
+template <int CODE, int D>
+static cudaError_t few(const Plan &p, const WeighArgs &a, cudaStream_t s) {
+    using Cfg = WeighCfg<D>;
+    cudaError_t e = cudaFuncSetAttribute(k_kv_weigh_few<CODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
+    if (e != cudaSuccess) return e;
+    k_kv_weigh_few<CODE, D><<<p.sm_count * Cfg::ctas, kDecThreads, Cfg::smem, s>>>(a);
+    return cudaGetLastError();
+}
+template <int CODE, int D>
+static cudaError_t many(const WeighArgs &a, cudaStream_t s) {
+    using Cfg = WeighManyCfg<D>;
+    cudaError_t e = cudaFuncSetAttribute(k_kv_weigh_many<CODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((a.c.max_len + kTileRows - 1) / kTileRows, a.c.Hk, a.c.B);
+    k_kv_weigh_many<CODE, D><<<grid, kWmThreads, Cfg::smem, s>>>(a);
+    return cudaGetLastError();
+}
+template <int CODE>
+static cudaError_t weigh(const Plan &p, const WeighArgs &a, cudaStream_t s) {
+    const bool rows = (int64_t)a.c.max_new * a.c.G > kWeighRows;
+    switch (p.desc.head_dim) {
+        case 64: return rows ? many<CODE, 64>(a, s) : few<CODE, 64>(p, a, s);
+        case 128: return rows ? many<CODE, 128>(a, s) : few<CODE, 128>(p, a, s);
+        default: return few<CODE, 256>(p, a, s);
+    }
 }
 
 cudaError_t launch_weigh(const Plan &p, const Ctx &c, Rows q, const float *lse, const float *acc_in, float *acc_out,
                          int64_t acc_stride, float decay, float sm, cudaStream_t s) {
-    const dim3 grid((c.max_len + kThreads - 1) / kThreads, c.Hk, c.B);
-    if (p.desc.code == SI_KV_INT8) {
-        if (p.desc.dtype == SI_KV_BF16) k_kv_weigh<SI_KV_INT8, SI_KV_BF16><<<grid, kThreads, 0, s>>>(c, q, lse, acc_in, acc_out, acc_stride, decay, sm);
-        else k_kv_weigh<SI_KV_INT8, SI_KV_F16><<<grid, kThreads, 0, s>>>(c, q, lse, acc_in, acc_out, acc_stride, decay, sm);
-    } else {
-        if (p.desc.dtype == SI_KV_BF16) k_kv_weigh<SI_KV_E4M3, SI_KV_BF16><<<grid, kThreads, 0, s>>>(c, q, lse, acc_in, acc_out, acc_stride, decay, sm);
-        else k_kv_weigh<SI_KV_E4M3, SI_KV_F16><<<grid, kThreads, 0, s>>>(c, q, lse, acc_in, acc_out, acc_stride, decay, sm);
-    }
-    return cudaGetLastError();
+    WeighArgs a{};
+    a.c = c;
+    a.q = q;
+    a.lse = lse;
+    a.acc_in = acc_in;
+    a.acc_out = acc_out;
+    a.acc_stride = acc_stride;
+    a.decay = decay;
+    a.scale2 = sm * kLog2e;
+    a.bf16 = p.desc.dtype == SI_KV_BF16;
+    a.log_page = p.desc.page_tokens == 16 ? 4 : p.desc.page_tokens == 32 ? 5 : 6;
+    a.fault = p.fault_wait;
+    a.budget = p.wait_budget;
+    return p.desc.code == SI_KV_INT8 ? weigh<SI_KV_INT8>(p, a, s) : weigh<SI_KV_E4M3>(p, a, s);
 }
 
 }  // namespace kv

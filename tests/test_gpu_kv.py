@@ -142,17 +142,19 @@ def test_attend_many_sequences():
 def test_attend_scores_apart(code, n):
     """Scores far apart (one token takes all the weight), scores all equal, and pages of very different scale."""
     shape = Shape(4, 2, 128, 16, code, "bf16")
-    c = ref.make_cache(shape, [300], [n], seed=2)
-    c.t["v_scale"] *= torch.exp2(torch.randint(-12, 4, c.t["v_scale"].shape).float())
-    c.t["k_scale"] *= torch.exp2(torch.randint(-3, 2, c.t["k_scale"].shape).float())
-    d = Dev(c)
-    q, qd = make_q(c, 4)
-    for sm in (0.0, 0.01, 0.1, 0.4):
+    for seed, sm in enumerate((0.0, 0.01, 0.1, 0.4, 0.1, 0.4, 0.2, 0.4)):
+        g = torch.Generator().manual_seed(seed)
+        c = ref.make_cache(shape, [300], [n], seed=2)
+        c.t["v_scale"] *= torch.exp2(torch.randint(-12, 4, c.t["v_scale"].shape, generator=g).float())
+        c.t["k_scale"] *= torch.exp2(torch.randint(-3, 2, c.t["k_scale"].shape, generator=g).float())
+        d = Dev(c)
+        q, qd = make_q(c, 4)
         out, lse = d.attend(qd, sm)
         o, z, S, A = ref.attend(c, q, sm)
         half = torch.finfo(torch.bfloat16).eps / 2
         tol = half * o.abs() + (2.0 ** -11 + 2.0 ** -15 * A[..., None]) * S + 2.0 ** -25
-        assert ((out.double().cpu() - o).abs() <= tol).all(), sm
+        far = float(((out.double().cpu() - o).abs() / tol).max())
+        assert far <= 1, (seed, sm, far)
         assert ((lse.double().cpu() - z).abs() <= 2.0 ** -17 * A + 2.0 ** -21 * (1 + z.abs())).all()
 
 
@@ -246,6 +248,9 @@ def test_attend_reports_a_wait_that_runs_out(monkeypatch, dim):
     monkeypatch.setenv("SI_FAULT_WAIT_BUDGET", "20000")
     d = Dev(c)
     d.attend(qd, 0.1)
+    assert d.status() == si.SI_ERR_TIMEOUT
+    acc = torch.zeros((1, 2, 500), device=DEV)
+    si.si_kv_weigh(d.plan, d.cache, d.batch, qd, torch.zeros((200, 8), device=DEV), None, acc, 1.0, 0.1, d.scratch)
     assert d.status() == si.SI_ERR_TIMEOUT
     monkeypatch.delenv("SI_FAULT_WAIT_BUDGET")
     d = Dev(c)
