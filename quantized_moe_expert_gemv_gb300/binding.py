@@ -467,19 +467,48 @@ def kv_batch(n_seqs, total_new, max_new, max_len, q_start, lens, page_table, slo
 
 def _rows(t) -> si_kv_rows:
     """A [rows, heads, D] tensor (or a view with D contiguous) as si_kv_rows."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    strides = t.stride()
+    if len(strides) != 3 or strides[2] != 1:
         raise ValueError("q, k, v and out are [rows, heads, D] with D contiguous")
-    return si_kv_rows(_ptr(t), t.stride(0), t.stride(1))
+    return si_kv_rows(t.data_ptr(), strides[0], strides[1])
 
 
 def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-def _kv_call(name, plan, args, scratch, stream, raw_status):
-    st = getattr(load_library(), name)(plan.handle, *args, _ptr(scratch), _nbytes(scratch), _stream(stream))
-    if not raw_status:
-        _check(st, name)
+def _opt(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+# A decode step makes a few of these calls for each layer, and on the host each should cost little more than
+# its launch: the functions are looked up once, and the current stream is read without making a Stream object.
+_kv_fns: dict = {}
+_raw_stream = None
+
+
+def _kv_fn(name):
+    f = _kv_fns.get(name)
+    if f is None:
+        f = _kv_fns[name] = getattr(load_library(), name)
+    return f
+
+
+def _kv_stream(stream) -> Optional[int]:
+    global _raw_stream
+    if stream is not None:
+        return _stream(stream)
+    if _raw_stream is None:
+        import torch
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        torch.cuda.current_stream()  # (brings CUDA up)
+        _raw_stream = (lambda: raw(device())) if raw else lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
+
+
+def _kv_done(st, name, raw_status):
+    if st != SI_OK and not raw_status:
+        raise SiError(st, name)
     return st
 
 
@@ -497,36 +526,42 @@ def si_kv_scratch_init(plan: KvPlan, scratch, stream=None):
 
 def si_kv_append(plan, cache: si_kv_cache, batch: si_kv_batch, k, v, lens_out, scratch, stream=None,
                  raw_status=False):
-    return _kv_call("si_kv_append", plan, (ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(_rows(k)),
-                                           ctypes.byref(_rows(v)), _ptr(lens_out)), scratch, stream, raw_status)
+    st = _kv_fn("si_kv_append")(plan.handle, cache, batch, _rows(k), _rows(v), lens_out.data_ptr(), scratch.data_ptr(),
+                                _nbytes(scratch), _kv_stream(stream))
+    return _kv_done(st, "si_kv_append", raw_status)
 
 
 def si_kv_read(plan, cache: si_kv_cache, pages, n, k_out, v_out, scratch, stream=None, raw_status=False):
-    return _kv_call("si_kv_read", plan, (ctypes.byref(cache), _ptr(pages), int(n), _ptr(k_out), _ptr(v_out)),
-                    scratch, stream, raw_status)
+    st = _kv_fn("si_kv_read")(plan.handle, cache, pages.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                              scratch.data_ptr(), _nbytes(scratch), _kv_stream(stream))
+    return _kv_done(st, "si_kv_read", raw_status)
 
 
 def si_kv_attend(plan, cache: si_kv_cache, batch: si_kv_batch, q, out, lse, sm_scale, scratch, stream=None,
                  raw_status=False):
-    return _kv_call("si_kv_attend", plan, (ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(_rows(q)),
-                                           ctypes.byref(_rows(out)), _ptr(lse), float(sm_scale)), scratch, stream,
-                    raw_status)
+    """lse: [rows, n_heads] float32, or None."""
+    st = _kv_fn("si_kv_attend")(plan.handle, cache, batch, _rows(q), _rows(out), _opt(lse), sm_scale,
+                                scratch.data_ptr(), _nbytes(scratch), _kv_stream(stream))
+    return _kv_done(st, "si_kv_attend", raw_status)
 
 
 def si_kv_weigh(plan, cache: si_kv_cache, batch: si_kv_batch, q, lse, acc_in, acc_out, decay, sm_scale, scratch,
                 stream=None, raw_status=False):
     """acc_in (or None) and acc_out: [n_seqs, Hkv, acc_stride] float32, contiguous."""
-    return _kv_call("si_kv_weigh", plan, (ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(_rows(q)), _ptr(lse),
-                                          _ptr(acc_in), _ptr(acc_out), acc_out.shape[2], float(decay),
-                                          float(sm_scale)), scratch, stream, raw_status)
+    st = _kv_fn("si_kv_weigh")(plan.handle, cache, batch, _rows(q), lse.data_ptr(), _opt(acc_in), acc_out.data_ptr(),
+                               acc_out.shape[2], decay, sm_scale, scratch.data_ptr(), _nbytes(scratch),
+                               _kv_stream(stream))
+    return _kv_done(st, "si_kv_weigh", raw_status)
 
 
 def si_kv_evict(plan, cache: si_kv_cache, batch: si_kv_batch, acc_in, acc_out, budget, sink, recent, new_table,
                 new_slots, keep, lens_out, scratch, stream=None, raw_status=False):
-    """new_table [n_seqs, budget], keep [n_seqs, Hkv, budget] int32; acc_in, acc_out [n_seqs, Hkv, acc_stride]."""
-    return _kv_call("si_kv_evict", plan, (ctypes.byref(cache), ctypes.byref(batch), _ptr(acc_in), _ptr(acc_out),
-                                          acc_in.shape[2], int(budget), int(sink), int(recent), _ptr(new_table),
-                                          _ptr(new_slots), _ptr(keep), _ptr(lens_out)), scratch, stream, raw_status)
+    """new_table [n_seqs, budget], keep [n_seqs, Hkv, budget] int32; acc_in, acc_out [n_seqs, Hkv, acc_stride];
+    new_slots [n_seqs] int32 or None (the batch's own)."""
+    st = _kv_fn("si_kv_evict")(plan.handle, cache, batch, acc_in.data_ptr(), acc_out.data_ptr(), acc_in.shape[2], budget,
+                               sink, recent, new_table.data_ptr(), _opt(new_slots), keep.data_ptr(),
+                               lens_out.data_ptr(), scratch.data_ptr(), _nbytes(scratch), _kv_stream(stream))
+    return _kv_done(st, "si_kv_evict", raw_status)
 
 
 def si_kv_read_status(plan: KvPlan, scratch, stream=None) -> int:

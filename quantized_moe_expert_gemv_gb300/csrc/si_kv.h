@@ -1,6 +1,7 @@
 // si_kv.h -- the attention block's internals: the plan, the scratch layout,
 // the arguments every kernel gets, and the launchers.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -43,6 +44,18 @@ struct Rows {
     uint16_t *p;
     int64_t row, head;  // strides in elements
 };
+
+// Allow kernel F `smem` bytes of dynamic shared memory, once a device (F and smem
+// are the caller's constants; the attribute stays with the function).
+template <auto F>
+cudaError_t allow_smem(const Plan &p, int smem) {
+    static std::atomic<unsigned long long> done{0};
+    const unsigned long long bit = 1ull << (p.device & 63);
+    if (p.device < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && p.device < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int max_len);
 

@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
 template <int CODE, int D, int MT>
 cudaError_t decode_launch(const Plan &p, const DecodeArgs &a, cudaStream_t s) {
     using Cfg = DecodeCfg<D, MT>;
-    cudaError_t e = cudaFuncSetAttribute(k_kv_decode<CODE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_decode<CODE, D, MT>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
     k_kv_decode<CODE, D, MT><<<p.sm_count * Cfg::ctas, kDecThreads, Cfg::smem, s>>>(a);
     return cudaGetLastError();

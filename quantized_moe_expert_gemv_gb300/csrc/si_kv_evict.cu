@@ -177,12 +177,11 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(Ctx c, const float *ac
     }
 }
 
-cudaError_t launch_evict(const Plan &, const Ctx &c, const float *acc_in, float *acc_out, int64_t acc_stride, int budget,
+cudaError_t launch_evict(const Plan &p, const Ctx &c, const float *acc_in, float *acc_out, int64_t acc_stride, int budget,
                          int sink, int recent, const int32_t *new_table, const int32_t *new_slots, int32_t *keep,
                          int32_t *lens_out, cudaStream_t s) {
     const size_t smem = (size_t)(c.max_len / c.P) * sizeof(unsigned long long);
-    cudaError_t e = cudaFuncSetAttribute(k_kv_choose, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SI_KV_MAX_EVICT_PAGES * (int)sizeof(unsigned long long));
+    cudaError_t e = allow_smem<k_kv_choose>(p, SI_KV_MAX_EVICT_PAGES * (int)sizeof(unsigned long long));
     if (e != cudaSuccess) return e;
     k_kv_choose<<<dim3(c.Hk, c.B), kChooseThreads, smem, s>>>(c, acc_in, acc_stride, budget, sink, recent, keep,
                                                               lens_out);

@@ -455,15 +455,15 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
 template <int CODE, int D>
 static cudaError_t few(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighCfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(k_kv_weigh_few<CODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_weigh_few<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
     k_kv_weigh_few<CODE, D><<<p.sm_count * Cfg::ctas, kDecThreads, Cfg::smem, s>>>(a);
     return cudaGetLastError();
 }
 template <int CODE, int D>
-static cudaError_t many(const WeighArgs &a, cudaStream_t s) {
+static cudaError_t many(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighManyCfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(k_kv_weigh_many<CODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_weigh_many<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((a.c.max_len + kTileRows - 1) / kTileRows, a.c.Hk, a.c.B);
     k_kv_weigh_many<CODE, D><<<grid, kWmThreads, Cfg::smem, s>>>(a);
@@ -473,8 +473,8 @@ template <int CODE>
 static cudaError_t weigh(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     const bool rows = (int64_t)a.c.max_new * a.c.G > kWeighRows;
     switch (p.desc.head_dim) {
-        case 64: return rows ? many<CODE, 64>(a, s) : few<CODE, 64>(p, a, s);
-        case 128: return rows ? many<CODE, 128>(a, s) : few<CODE, 128>(p, a, s);
+        case 64: return rows ? many<CODE, 64>(p, a, s) : few<CODE, 64>(p, a, s);
+        case 128: return rows ? many<CODE, 128>(p, a, s) : few<CODE, 128>(p, a, s);
         default: return few<CODE, 256>(p, a, s);
     }
 }
