@@ -4,8 +4,8 @@
 namespace si {
 namespace kv {
 
-cudaError_t launch_decode_int8(const Plan &p, const DecodeArgs &a, int mt, cudaStream_t s);
-cudaError_t launch_decode_e4m3(const Plan &p, const DecodeArgs &a, int mt, cudaStream_t s);
+cudaError_t launch_decode_int8(const Plan &p, const DecodeArgs &a, int r8, cudaStream_t s);
+cudaError_t launch_decode_e4m3(const Plan &p, const DecodeArgs &a, int r8, cudaStream_t s);
 cudaError_t launch_prompt_int8(const Plan &p, const PromptArgs &a, cudaStream_t s);
 cudaError_t launch_prompt_e4m3(const Plan &p, const PromptArgs &a, cudaStream_t s);
 
@@ -23,27 +23,18 @@ static int prompt_splits(const Plan &p, int n_seqs, int max_new, int max_len) {
     return n < 1 ? 1 : n > 32 ? 32 : (int)n;
 }
 
-// Row groups of 16 (one group for a decode step) or 32 rows.
+// Column tiles of 8 rows in a row group of the few-row kernel: the fewest that hold a sequence's rows,
+// as far as the registers go.
 static int row_tiles(const Plan &p, int max_new) {
     const int64_t rows = (int64_t)max_new * (p.desc.n_heads / p.desc.n_kv_heads);
-    return rows > 16 && p.desc.head_dim <= 128 ? 2 : 1;
-}
-static int decode_ctas(const Plan &p, int mt) {
-    const int D = p.desc.head_dim;
-    return p.sm_count * (D == 256 ? DecodeCfg<256, 1>::ctas
-                                  : D == 128 ? (mt == 1 ? DecodeCfg<128, 1>::ctas : DecodeCfg<128, 2>::ctas)
-                                             : (mt == 1 ? DecodeCfg<64, 1>::ctas : DecodeCfg<64, 2>::ctas));
+    return rows <= 8 ? 1 : rows <= 16 || p.desc.head_dim == 256 ? 2 : 4;
 }
 
 size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int max_len) {
     // A buffer for larger bounds serves smaller ones, so this takes the most that any call within the bounds needs:
     // a call with fewer sequences or rows may be split more (at most sm_count CTAs of 256 rows together).
     const size_t D = p.desc.head_dim;
-    size_t most = 0;
-    for (int mt = 1; mt <= 2; ++mt) {
-        const size_t n = (size_t)decode_ctas(p, mt) * 2 * (size_t)partial_floats(16 * mt, p.desc.head_dim) * sizeof(float);
-        most = n > most ? n : most;
-    }
+    size_t most = (size_t)p.sm_count * 2 * (size_t)partial_floats(8 * row_tiles(p, max_new), p.desc.head_dim) * sizeof(float);
     if (many_rows(p, max_new)) {
         const size_t row_heads = (size_t)total_new * p.desc.n_heads;
         size_t n = row_heads * 32;                                         // 32 splits at most, and
@@ -85,8 +76,8 @@ cudaError_t launch_attend(const Plan &p, const Ctx &c, Rows q, Rows out, float *
     a.log_page = log_page;
     a.counters = static_cast<int32_t *>(scratch) + kCtrlWords;
     a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + kCtrlBytes);
-    const int mt = row_tiles(p, c.max_new);
-    return p.desc.code == SI_KV_INT8 ? launch_decode_int8(p, a, mt, s) : launch_decode_e4m3(p, a, mt, s);
+    const int r8 = row_tiles(p, c.max_new);
+    return p.desc.code == SI_KV_INT8 ? launch_decode_int8(p, a, r8, s) : launch_decode_e4m3(p, a, r8, s);
 }
 
 }  // namespace kv

@@ -7,20 +7,26 @@
 // sm_scale * log2 e, and m_r is a running maximum.
 //
 // Bound: HBM.  Every cached token is read once for all the rows of its kv
-// head, 2D bytes of codes; the arithmetic per byte is 2 x 16 rows of matrix
-// work and the codes' conversion to fp16 (about 1.4 half-rate instructions a
-// byte), which has to stay below the time that the byte takes to arrive: 23
+// head, 2D bytes of codes; the arithmetic per byte is the matrix work for 8
+// rows and the codes' conversion to fp16 (1.4 instructions a byte, at half
+// rate), which has to stay below the time that the byte takes to arrive: 23
 // bytes a cycle and SM at the measured copy rate.
+//  * Products: keys are the 16 rows of the warp-level product and q's rows its 8
+//    columns (S^T = K Q^T, then O^T = V^T P^T), so a step of 8 query heads for
+//    a kv head wastes none of it; with q's rows as the 16 rows, 4 heads used a
+//    quarter of the matrix and softmax work, and a batch of 64 sequences took
+//    273 us.  Between the two products P^T is transposed in registers.
 //  * Work: units of 64 tokens of one (sequence, kv head, row group), numbered in
-//    order; each CTA takes an equal share of consecutive units, whatever the
-//    sequences' lengths.  A CTA joins its warps' results for each item it
-//    touches; an item that lies in several CTAs is joined by the last of them
-//    to arrive, in the CTAs' order (the same inputs give the same bits).
-//  * A warp owns 16 of a unit's 64 tokens (one page: P >= 16) and copies them
-//    into its own ring in shared memory (cp.async, several units ahead): no
+//    order; each CTA (one an SM) takes an equal share of consecutive units,
+//    whatever the sequences' lengths.  A CTA joins its warps' results for each
+//    item it touches; an item that lies in several CTAs is joined by the last of
+//    them to arrive (in groups of 16 where there are many), in the CTAs' order:
+//    the same inputs give the same bits.
+//  * A warp takes pieces of 16 tokens (one page: P >= 16), every W-th, and copies
+//    them into its own ring in shared memory (cp.async, some pieces ahead): no
 //    barrier between warps inside an item.
 //  * The maximum is lazy: m moves only when a score passes it by more than 4
-//    (a vote a tile instead of shuffles), and p stays below 2^4.
+//    (a vote a piece instead of shuffles), and p stays below 2^4.
 //  * p times the page's V scale is rounded to fp16 for the second product.  The
 //    scale is taken relative to the largest so far, so that the products stay
 //    inside fp16: p < 2^4, scale/reference <= 1, times 2^11: at most 2^15; a
@@ -33,28 +39,31 @@
 namespace si {
 namespace kv {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = kDecWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 4.0f, kWeightUnit = 2048.0f;
 constexpr float kNoScore = -1e30f;  // a running maximum before the first score
 
-template <int D, int MT>
+// R8: column tiles of 8 rows.  As many warps as the registers allow (the second product's sums are
+// D R8 / 4 a lane), then as many stages as fit 192 KB.
+template <int D, int R8>
 struct DecodeCfg {
-    static constexpr int stage = 32 * D;  // bytes of one warp's 16 keys, K and V
-    static constexpr int stages = D == 64 ? 6 : D == 128 ? 4 : 3;
-    static constexpr int ring = kDecWarps * stages * stage;
-    static constexpr int merge = kDecWarps * 16 * MT * D * 4;
-    static constexpr bool q_in_regs = D * MT <= 128;
-    static constexpr int q_bytes = q_in_regs ? 0 : MT * (D / 16) * 512;
-    static constexpr int ctas = D == 256 ? 2 : MT == 2 ? 2 : D == 64 ? 4 : 3;  // a SM
-    static constexpr int smem = (ring > merge ? ring : merge) + q_bytes;
+    static constexpr int warps = D * R8 <= 128 ? 16 : D * R8 <= 256 ? 12 : 8;
+    static constexpr int stage = 32 * D;  // bytes of one piece, K and V
+    static constexpr int stages = 192 * 1024 / (warps * stage);
+    static constexpr int ring = warps * stages * stage;
+    static constexpr bool q_in_regs = D * R8 <= 256;
+    static constexpr int q_bytes = q_in_regs ? 0 : R8 * (D / 16) * 256;
+    static constexpr int smem = ring + q_bytes;
+    static_assert(warps * 8 * R8 * D * 4 <= ring, "the warps' results are joined in the ring's place");
 };
 
 // Partial results in the scratch: two slots a CTA (an item that began in an
 // earlier CTA, one that goes on in a later one), each [rows][D] sums, then [rows][2]
 // maximum and sum.
 __host__ __device__ constexpr int64_t partial_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
+constexpr int kMaxDecodeCtas = 1024;  // arrival counters: one an item's first CTA, then two a CTA for groups
+constexpr int kJoinGroup = 16;
+static_assert(3 * kMaxDecodeCtas <= kCounters, "");
 
 struct DecodeArgs {
     Ctx c;
@@ -67,38 +76,29 @@ struct DecodeArgs {
     float *partial;
 };
 
-// Units of sequence b: (pages in tiles of 64 tokens, then the unfinished page) x kv heads x row groups.
+// Units of 64 tokens of a sequence: its full pages, then the unfinished page.
 __device__ __forceinline__ int seq_tiles(const Ctx &c, int len) {
     const int paged = len & ~(c.P - 1);
     return (paged + 63) / 64 + (paged < len ? 1 : 0);
 }
 
-template <int CODE, int D, int MT>
-__global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_decode(const DecodeArgs a) {
-    using Cfg = DecodeCfg<D, MT>;
-    constexpr int R = 16 * MT;      // rows of an item
-    constexpr int NT = D / 8;       // column tiles of the second product
-    constexpr int KS = D / 16;      // steps of the first
-    constexpr int CH = D / 16;      // 16-byte chunks of a key
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_scan[kDecWarps];
+// A CTA's equal share [begin, end) of all units, and the sequence that `begin` lies in.  `units_of(b)`:
+// units of sequence b.  All threads call this; `some_empty`: whether a sequence has none.
+struct Share {
+    long long total, ctas, begin, end, off;  // off: begin's place within sequence b
+    int b;
+    bool some_empty;
+};
+template <int WARPS, typename F>
+__device__ __forceinline__ Share take_share(int B, F units_of) {
+    __shared__ long long s_scan[WARPS];
     __shared__ long long s_off;
-    __shared__ int s_b, s_last;
-    __shared__ float s_ml[kDecWarps][R][2];
-    __shared__ float s_part[R][2];
-    const Ctx &c = a.c;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
-    const bool bf16 = a.bf16;
-
-    // ---- this CTA's share of the units
-    const int per = (c.B + kDecThreads - 1) / kDecThreads;
-    auto units_of = [&](int b) -> long long {
-        const Seq s = load_seq(c, b);
-        return (long long)seq_tiles(c, s.len) * c.Hk * ((s.n * c.G + R - 1) / R);
-    };
+    __shared__ int s_b;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
     long long mine = 0;
     bool empty = false;
-    for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) {
+    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
         const long long n = units_of(b);
         mine += n;
         empty |= n == 0;
@@ -109,43 +109,78 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
         if (lane >= o) incl += up;
     }
     if (lane == 31) s_scan[w] = incl;
-    const bool some_empty = __syncthreads_or(empty);
-    long long before = incl - mine, total = 0;
-    for (int k = 0; k < kDecWarps; ++k) {
+    Share s;
+    s.some_empty = __syncthreads_or(empty);
+    long long before = incl - mine;
+    s.total = 0;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
         if (k < w) before += s_scan[k];
-        total += s_scan[k];
+        s.total += s_scan[k];
     }
+    s.ctas = s.total < (long long)gridDim.x ? s.total : (long long)gridDim.x;
+    s.begin = s.end = 0;
+    if (blockIdx.x < s.ctas) {
+        s.begin = blockIdx.x * s.total / s.ctas;
+        s.end = (blockIdx.x + 1) * s.total / s.ctas;
+        if (before <= s.begin && s.begin < before + mine) {
+            int b = tid * per;
+            long long at = before, n;
+            while (at + (n = units_of(b)) <= s.begin) {
+                at += n;
+                ++b;
+            }
+            s_b = b;
+            s_off = s.begin - at;
+        }
+    }
+    __syncthreads();
+    s.b = s_b;
+    s.off = s_off;
+    return s;
+}
+
+template <int CODE, int D, int R8>
+__global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(const DecodeArgs a) {
+    using Cfg = DecodeCfg<D, R8>;
+    constexpr int W = Cfg::warps, THREADS = W * 32;
+    constexpr int R = 8 * R8;       // rows of an item
+    constexpr int MT = D / 16;      // row tiles of the second product
+    constexpr int KS = D / 16;      // steps of the first
+    constexpr int CH = D / 16;      // 16-byte chunks of a key
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_last;
+    __shared__ __align__(8) float s_ml[W][R][2];
+    __shared__ __align__(8) float s_part[R][2];
+    const Ctx &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
+    const bool bf16 = a.bf16;
+
+    const Share share = take_share<W>(c.B, [&](int b) -> long long {
+        const Seq s = load_seq(c, b);
+        return (long long)seq_tiles(c, s.len) * c.Hk * ((s.n * c.G + R - 1) / R);
+    });
     // rows whose sequence has no token at all are in no unit: zeros
-    if (some_empty)
+    if (share.some_empty)
         for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
             const Seq s = load_seq(c, b);
             if (s.len > 0) continue;
-            for (int k = tid; k < s.n * c.H * (D / 8); k += kDecThreads) {
+            for (int k = tid; k < s.n * c.H * (D / 8); k += THREADS) {
                 const int row = s.row0 + k / (c.H * (D / 8)), head = k / (D / 8) % c.H, d = k % (D / 8) * 8;
                 *reinterpret_cast<uint4 *>(a.out.p + row * a.out.row + head * a.out.head + d) = make_uint4(0, 0, 0, 0);
                 if (a.lse && d == 0) a.lse[(int64_t)row * c.H + head] = -INFINITY;
             }
         }
-    const long long N = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-    if (blockIdx.x >= N) return;
-    const long long u_begin = blockIdx.x * total / N, u_end = (blockIdx.x + 1) * total / N;
-    if (before <= u_begin && u_begin < before + mine) {
-        int b = tid * per;
-        long long at = before, n;
-        while (at + (n = units_of(b)) <= u_begin) {
-            at += n;
-            ++b;
-        }
-        s_b = b;
-        s_off = u_begin - at;
-    }
-    __syncthreads();
-    int b = s_b;
-    long long off = s_off;  // within sequence b
-    long long u = u_begin;
+    if (blockIdx.x >= share.ctas) return;
+    int b = share.b;
+    long long off = share.off, u = share.begin;
+    const long long u_end = share.end;
 
     const uint32_t ring = smem_addr(smem) + w * (Cfg::stages * Cfg::stage);
-    uint8_t *q_smem = smem + (Cfg::smem - Cfg::q_bytes);
+    uint8_t *q_smem = smem + Cfg::ring;
+    uint32_t chunk_at[D / 32];  // where this lane's chunks of a piece go
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) chunk_at[k] = tile_at<D>((lane + 32 * k) / CH, (lane + 32 * k) % CH);
 
     while (u < u_end) {
         const Seq s = load_seq(c, b);
@@ -165,169 +200,39 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
         const int lim_min = old + rb * R / c.G + 1, lim_max = old + (rb * R + rows - 1) / c.G + 1;
         const int paged_tiles = (paged + 63) / 64;
 
-        // ---- q
-        uint32_t qa[Cfg::q_in_regs ? MT * KS : 1][4];
-        float qf[MT][2];
-        int lim[MT][2];
-        if (!Cfg::q_in_regs) __syncthreads();  // the last item's readers are done
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = rb * R + mt * 16 + g + 8 * e;
-                const bool live = mt * 16 + g + 8 * e < rows;
-                const int i = live ? r / c.G : 0, head = live ? h * c.G + r % c.G : 0;
-                const uint16_t *src = a.q.p + (s.row0 + i) * a.q.row + head * a.q.head;
-                uint4 x[D / 32];
-                float amax = 0.0f;
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
-                        amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
-                    }
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                float mul;
-                row_scale(amax, mul, qf[mt][e]);
-                qf[mt][e] *= a.scale2;
-                lim[mt][e] = live ? old + i + 1 : INT32_MAX;
-#pragma unroll
-                for (int st = 0; st < KS; ++st) {  // chunk st / 4, four values at 4 * (st % 4)
-                    const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
-                    const uint32_t lo = scale2(st & 1 ? v.z : v.x, mul, bf16), hi = scale2(st & 1 ? v.w : v.y, mul, bf16);
-                    if constexpr (Cfg::q_in_regs) {
-                        qa[mt * KS + st][e] = lo;
-                        qa[mt * KS + st][2 + e] = hi;
-                    } else if ((st & 3) == w) {
-                        uint32_t *to = reinterpret_cast<uint32_t *>(q_smem + (mt * KS + st) * 512 + lane * 16);
-                        to[e] = lo;
-                        to[2 + e] = hi;
-                    }
-                }
-            }
-        }
-        if (!Cfg::q_in_regs) __syncthreads();
-
-        float o[MT][NT][4];
-        float m[MT][2], l[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
-            m[mt][0] = m[mt][1] = kNoScore;
-            l[mt][0] = l[mt][1] = 0.0f;
-        }
-        float v_ref = 1e-30f;  // the largest V scale so far: o is in units of v_ref / kWeightUnit
-
-        // Scores to weights: s (raw products) times the columns' factors and the rows', masked at the
-        // rows' limits; updates m, l, and o's scale; returns the second product's operand.
-        auto weights = [&](float (&sc)[MT][2][4], const float (&kf)[4], const float (&vf)[4], float v_top, int t0,
-                           bool masked, uint32_t (&pa)[MT][4]) {
-            if (v_top > v_ref) {
-                const float f = v_ref / v_top;
-                v_ref = v_top;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
-            }
-            const float inv = kWeightUnit / v_ref;
-            bool over = false;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float z = sc[mt][n][e] * (kf[2 * n + (e & 1)] * qf[mt][e >> 1]);
-                        if (masked && t0 + 8 * n + 2 * j + (e & 1) >= lim[mt][e >> 1]) z = -INFINITY;
-                        sc[mt][n][e] = z;
-                    }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float top = fmaxf(fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]),
-                                            fmaxf(sc[mt][1][2 * e], sc[mt][1][2 * e + 1]));
-                    over |= top > m[mt][e] + kLazy;
-                }
-            }
-            if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float f[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]),
-                                          fmaxf(sc[mt][1][2 * e], sc[mt][1][2 * e + 1]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        top = fmaxf(top, m[mt][e]);
-                        f[e] = ex2(m[mt][e] - top);
-                        m[mt][e] = top;
-                        l[mt][e] *= f[e];
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[mt][n][0] *= f[0];
-                        o[mt][n][1] *= f[0];
-                        o[mt][n][2] *= f[1];
-                        o[mt][n][3] *= f[1];
-                    }
-                }
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float p0 = ex2(sc[mt][n][2 * e] - m[mt][e]), p1 = ex2(sc[mt][n][2 * e + 1] - m[mt][e]);
-                        l[mt][e] += p0 + p1;
-                        // (a page without a scale makes NaN of the weights that see it, and of no other)
-                        const float w0 = p0 == 0.0f ? 0.0f : p0 * (vf[2 * n] * inv);
-                        const float w1 = p1 == 0.0f ? 0.0f : p1 * (vf[2 * n + 1] * inv);
-                        pa[mt][2 * n + e] = half2_bits(w0, w1);
-                    }
-        };
-
-        // ---- full pages
-        const int t_stop = min(min(t_end, paged_tiles), (lim_max + 63) / 64);  // no row sees a later tile
-        const int count = t_stop - t_first;
-        // page, K scale and V scale of this warp's 16 tokens, for 32 tiles at a time (a lane a tile), two sets
-        int pid[2] = {-2, -2};
-        float ksc[2] = {0.0f, 0.0f}, vsc[2] = {0.0f, 0.0f};
+        // this warp's pieces of full pages: page and scales of 32 pieces at a time (a lane a piece), two sets
+        const int p_first = 4 * t_first + w;
+        const int p_stop = min(min(4 * t_end, paged >> 4), (lim_max + 15) >> 4);  // no row sees a later piece
+        const int count = p_stop > p_first ? (p_stop - p_first + W - 1) / W : 0;
+        int pid0 = -1, pid1 = -1;
+        float ks0 = 0.0f, ks1 = 0.0f, vs0 = 0.0f, vs1 = 0.0f;
         auto fetch = [&](int set, int first) {
-            const int t = first + lane, token = (t_first + t) * 64 + 16 * w;
-            int p = -2;  // no tokens
-            if (t < count && token < paged) p = (int)load_page(c, b, token >> a.log_page);
+            const int i = first + lane;
+            int p = -1;
+            if (i < count) p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
             const float ks = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : 0.0f;
             const float vs = p >= 0 ? __ldg(c.vs + (int64_t)p * c.Hk + h) : 0.0f;
             if (set) {
-                pid[1] = p;
-                ksc[1] = ks;
-                vsc[1] = vs;
+                pid1 = p;
+                ks1 = ks;
+                vs1 = vs;
             } else {
-                pid[0] = p;
-                ksc[0] = ks;
-                vsc[0] = vs;
+                pid0 = p;
+                ks0 = ks;
+                vs0 = vs;
             }
         };
-        auto copy = [&](int t) {  // tile t of this item, relative to t_first
-            if (t < count) {
-                const int p = __shfl_sync(0xffffffffu, (t & 32) ? pid[1] : pid[0], t & 31);
+        auto copy = [&](int i, int stage) {
+            if (i < count) {
+                const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
                 if (p >= 0) {
-                    const int64_t at = page_at(c, p, h) + (int64_t)(((t_first + t) * 64 + 16 * w) & (c.P - 1)) * D;
-                    const uint32_t to = ring + (t % Cfg::stages) * Cfg::stage;
+                    const int64_t at = page_at(c, p, h) + (uint32_t)((((p_first + W * i) << 4) & (c.P - 1)) * D + lane * 16);
+                    const uint8_t *kc = c.kc + at, *vc = c.vc + at;
+                    const uint32_t to = ring + stage * Cfg::stage;
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
-                        const int ci = lane + 32 * k;
-                        const uint32_t x = to + tile_at<D>(ci / CH, ci % CH);
-                        cp_async16(x, c.kc + at + ci * 16);
-                        cp_async16(x + 16 * D, c.vc + at + ci * 16);
+                        cp_async16(to + chunk_at[k], kc + 512 * k);
+                        cp_async16(to + chunk_at[k] + 16 * D, vc + 512 * k);
                     }
                 }
             }
@@ -335,70 +240,178 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
         };
         if (count > 0) {
             fetch(0, 0);
-            fetch(1, 32);
 #pragma unroll
-            for (int t = 0; t < Cfg::stages - 1; ++t) copy(t);
+            for (int i = 0; i < Cfg::stages - 1; ++i) copy(i, i);
+            if (count > 32) fetch(1, 32);
         }
-        for (int t = 0; t < count; ++t) {
-            if ((t & 31) == 0 && t > 0) fetch(((t >> 5) + 1) & 1, (t & ~31) + 32);
-            copy(t + Cfg::stages - 1);
-            cp_async_wait<Cfg::stages - 1>();
-            __syncwarp();
-            const int p = __shfl_sync(0xffffffffu, (t & 32) ? pid[1] : pid[0], t & 31);
-            const float ks = __shfl_sync(0xffffffffu, (t & 32) ? ksc[1] : ksc[0], t & 31);
-            const float vs = __shfl_sync(0xffffffffu, (t & 32) ? vsc[1] : vsc[0], t & 31);
-            const int t0 = (t_first + t) * 64 + 16 * w;
-            if (p == -2 || t0 >= lim_max) continue;
-            if (p < 0) {  // not one of the cache's pages: NaN for the rows that see it
+
+        // ---- q (while the first copies are under way)
+        uint2 qb[Cfg::q_in_regs ? R8 : 1][KS];
+        float qf[R8][2];   // of rows 2j, 2j + 1 of each column tile
+        int lim[R8][2];    // the tokens that they see
+        if (!Cfg::q_in_regs) __syncthreads();  // the last item's readers are done
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < R8; ++n) {
+            const int r = rb * R + n * 8 + g;
+            const bool live = n * 8 + g < rows;
+            const int i = live ? r / c.G : 0, head = h * c.G + (live ? r % c.G : 0);
+            uint2 op[KS];
+            const float f = row_operand<D>(a.q.p + (s.row0 + i) * a.q.row + head * a.q.head, live, j, bf16, op) * a.scale2;
+            if constexpr (Cfg::q_in_regs) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (t0 < lim[mt][e]) l[mt][e] = __int_as_float(0x7fc00000);
-                continue;
+                for (int st = 0; st < KS; ++st) qb[n][st] = op[st];
+            } else {
+#pragma unroll
+                for (int st = 0; st < KS; ++st)
+                    if (st % W == w) *reinterpret_cast<uint2 *>(q_smem + (n * KS + st) * 256 + lane * 8) = op[st];
             }
-            const uint32_t kt = ring + (t % Cfg::stages) * Cfg::stage, vt = kt + 16 * D;
-            float sc[MT][2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int e = 0; e < 2; ++e) {
+                qf[n][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * j + e));
+                const int rr = n * 8 + 2 * j + e;
+                lim[n][e] = rr < rows ? old + (rb * R + rr) / c.G + 1 : INT32_MAX;
+            }
+        }
+        if (!Cfg::q_in_regs) __syncthreads();
+
+        float o[R8][MT][4];  // (d, row): d of rows g and g + 8 of row tile mt, rows 2j and 2j + 1 of the column tile
+        float m[R8][2], l[R8][2];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) sc[mt][n][0] = sc[mt][n][1] = sc[mt][n][2] = sc[mt][n][3] = 0.0f;
+        for (int n = 0; n < R8; ++n) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                uint4 x[2];
+            for (int mt = 0; mt < MT; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0.0f;
+            m[n][0] = m[n][1] = kNoScore;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+        // the largest V scale so far, and its inverse: o is in units of v_ref / kWeightUnit
+        float v_ref = 1e-30f, v_inv = kWeightUnit / 1e-30f;
+
+        // S^T of one step (k = 16) of 16 keys: ka is the keys' operand
+        auto scores = [&](float (&sc)[R8][4], const uint32_t (&ka)[4], int st) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) x[n] = lds128(kt + tile_at<D>(8 * n + g, k_dim<D>(j, i) / 16));
+            for (int n = 0; n < R8; ++n) {
+                if constexpr (Cfg::q_in_regs) {
+                    mma16816(sc[n], ka, qb[n][st].x, qb[n][st].y);
+                } else {
+                    const uint2 q2 = *reinterpret_cast<const uint2 *>(q_smem + (n * KS + st) * 256 + lane * 8);
+                    mma16816(sc[n], ka, q2.x, q2.y);
+                }
+            }
+        };
+        // Raw scores of keys t0 + g, t0 + g + 8 to the second product's operand: factors kf of the two
+        // keys, vf of their V; updates m, l and o's units.
+        auto weights = [&](float (&sc)[R8][4], float kf0, float kf1, float vf0, float vf1, float v_top, int t0, bool masked,
+                           uint32_t (&pb)[R8][2]) {
+            if (v_top > v_ref) {
+                const float f = v_ref / v_top;
+                v_ref = v_top;
+                v_inv = kWeightUnit / v_top;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int st = 4 * i + q;
-                    uint32_t lo[2], hi[2];
+                for (int n = 0; n < R8; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t word = q == 0 ? x[n].x : q == 1 ? x[n].y : q == 2 ? x[n].z : x[n].w;
-                        codes_to_half<CODE>(code_bias<CODE>(word), lo[n], hi[n]);
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][mt][e] *= f;
+            }
+            bool over = false;
+#pragma unroll
+            for (int n = 0; n < R8; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sc[n][e] *= kf0 * qf[n][e];
+                    sc[n][2 + e] *= kf1 * qf[n][e];
+                    if (masked) {
+                        if (t0 + g >= lim[n][e]) sc[n][e] = -INFINITY;
+                        if (t0 + g + 8 >= lim[n][e]) sc[n][2 + e] = -INFINITY;
+                    }
+                    over |= fmaxf(sc[n][e], sc[n][2 + e]) > m[n][e] + kLazy;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int n = 0; n < R8; ++n) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(sc[n][e], sc[n][2 + e]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        top = fmaxf(top, m[n][e]);
+                        f[e] = ex2(m[n][e] - top);
+                        m[n][e] = top;
+                        l[n][e] *= f[e];
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        if constexpr (Cfg::q_in_regs) {
-                            mma16816(sc[mt][0], qa[mt * KS + st], lo[0], hi[0]);
-                            mma16816(sc[mt][1], qa[mt * KS + st], lo[1], hi[1]);
-                        } else {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(q_smem + (mt * KS + st) * 512 + lane * 16);
-                            const uint32_t f[4] = {v.x, v.y, v.z, v.w};
-                            mma16816(sc[mt][0], f, lo[0], hi[0]);
-                            mma16816(sc[mt][1], f, lo[1], hi[1]);
-                        }
+                        o[n][mt][0] *= f[0];
+                        o[n][mt][1] *= f[1];
+                        o[n][mt][2] *= f[0];
+                        o[n][mt][3] *= f[1];
                     }
                 }
             }
-            uint32_t pa[MT][4];
-            const float kf[4] = {ks, ks, ks, ks}, vf[4] = {vs, vs, vs, vs};
+            const float w0 = vf0 * v_inv, w1 = vf1 * v_inv;
+#pragma unroll
+            for (int n = 0; n < R8; ++n) {
+                float p[4], y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2(sc[n][e] - m[n][e & 1]);
+                    y[e] = p[e] * (e < 2 ? w0 : w1);
+                    // (a page without a scale makes NaN of the weights that see it, and of no other)
+                    if (masked && p[e] == 0.0f) y[e] = 0.0f;
+                }
+                l[n][0] += p[0] + p[2];
+                l[n][1] += p[1] + p[3];
+                pb[n][0] = transpose8x8(half2_bits(y[0], y[1]));
+                pb[n][1] = transpose8x8(half2_bits(y[2], y[3]));
+            }
+        };
+
+        // ---- full pages
+        int stage = 0;
+        for (int i = 0; i < count; ++i) {
+            if ((i & 31) == 0 && i > 0 && i + 32 < count) fetch(((i >> 5) + 1) & 1, i + 32);
+            copy(i + Cfg::stages - 1, stage == 0 ? Cfg::stages - 1 : stage - 1);
+            cp_async_wait<Cfg::stages - 1>();
+            __syncwarp();
+            const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
+            const float ks = __shfl_sync(0xffffffffu, (i & 32) ? ks1 : ks0, i & 31);
+            const float vs = __shfl_sync(0xffffffffu, (i & 32) ? vs1 : vs0, i & 31);
+            const int t0 = (p_first + W * i) << 4;
+            const uint32_t kt = ring + stage * Cfg::stage, vt = kt + 16 * D;
+            stage = stage + 1 == Cfg::stages ? 0 : stage + 1;
+            if (p < 0) {  // not one of the cache's pages: NaN for the rows that see it
+#pragma unroll
+                for (int n = 0; n < R8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (t0 < lim[n][e]) l[n][e] = __int_as_float(0x7fc00000);
+                continue;
+            }
+            float sc[R8][4];
+#pragma unroll
+            for (int n = 0; n < R8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q) {
+                const uint4 x = lds128(kt + tile_at<D>(g, k_dim<D>(j, q) / 16));
+                const uint4 y = lds128(kt + tile_at<D>(8 + g, k_dim<D>(j, q) / 16));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t ka[4];
+                    codes_to_half<CODE>(code_bias<CODE>(xs[e]), ka[0], ka[2]);
+                    codes_to_half<CODE>(code_bias<CODE>(ys[e]), ka[1], ka[3]);
+                    scores(sc, ka, 4 * q + e);
+                }
+            }
+            uint32_t pb[R8][2];
             if (t0 + 16 <= lim_min)
-                weights(sc, kf, vf, vs, t0, false, pa);
+                weights(sc, ks, ks, vs, vs, vs, t0, false, pb);
             else
-                weights(sc, kf, vf, vs, t0, true, pa);
-            // V: keys 2j, 2j+1, 2j+8, 2j+9, and for column n of tile nt the value d = n * (16 or 8) + nt
-            constexpr int HW = D == 64 ? 2 : 4;  // words of a lane's run of d's
+                weights(sc, ks, ks, vs, vs, vs, t0, true, pb);
+            // V^T: keys 2j, 2j+1 and 2j+8, 2j+9; rows g and g + 8 of a row tile are two of this lane's run of d's
+            constexpr int HW = D == 64 ? 2 : 4;  // words of a lane's run of d's (8 or 16 of each 64 or 128)
 #pragma unroll
             for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
                 uint32_t x[4][HW];
@@ -418,68 +431,49 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < HW; ++q) {
+                for (int q = 0; q < HW; ++q) {  // d = 4 q + e of the run: row tile (4 q + e) / 2, its rows g or g + 8
                     uint32_t b0[4], b1[4];
                     codes_to_half<CODE>(__byte_perm(x[0][q], x[1][q], 0x5140), b0[0], b0[1]);
                     codes_to_half<CODE>(__byte_perm(x[0][q], x[1][q], 0x7362), b0[2], b0[3]);
                     codes_to_half<CODE>(__byte_perm(x[2][q], x[3][q], 0x5140), b1[0], b1[1]);
                     codes_to_half<CODE>(__byte_perm(x[2][q], x[3][q], 0x7362), b1[2], b1[3]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t va[4] = {b0[2 * e], b0[2 * e + 1], b1[2 * e], b1[2 * e + 1]};
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][16 * half + 4 * q + e], pa[mt], b0[e], b1[e]);
+                        for (int n = 0; n < R8; ++n) mma16816(o[n][8 * half + 2 * q + e], va, pb[n][0], pb[n][1]);
+                    }
                 }
             }
             __syncwarp();
         }
         cp_async_wait<0>();
 
-        // ---- the unfinished page's rows, in 16 bits
-        const int tail = s.len - paged, key0 = 16 * w;  // this warp's first row of it
-        if (t_end > paged_tiles && paged + key0 < min(s.len, lim_max)) {
-            float sc[MT][2][4];
-            float kf[4], vf[4];
+        // ---- the unfinished page's rows, in 16 bits: 16 of them for each of the last four warps
+        const int tail = s.len - paged, key0 = 16 * (w - (W - 4));
+        if (t_end > paged_tiles && key0 >= 0 && paged + key0 < min(s.len, lim_max)) {
+            float sc[R8][4];
+            uint32_t ka[KS][4];
+            float kf[2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int key = key0 + 8 * n + g;
+            for (int e = 0; e < 2; ++e) {
+                const int key = key0 + 8 * e + g;
                 const bool live = key < tail && s.slot >= 0;
-                const uint16_t *src = c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0));
-                uint4 x[D / 32];
-                float amax = 0.0f;
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
-                        amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
-                    }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                float mul, f;
-                row_scale(amax, mul, f);
-                if (s.slot < 0) f = __int_as_float(0x7fc00000);
-                kf[2 * n] = __shfl_sync(0xffffffffu, f, 8 * j);          // keys 2j and 2j + 1 of the tile
-                kf[2 * n + 1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) sc[mt][n][0] = sc[mt][n][1] = sc[mt][n][2] = sc[mt][n][3] = 0.0f;
+                uint2 op[KS];
+                kf[e] = row_operand<D>(c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)), live, j, bf16, op);
+                if (s.slot < 0) kf[e] = __int_as_float(0x7fc00000);
 #pragma unroll
                 for (int st = 0; st < KS; ++st) {
-                    const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
-                    const uint32_t lo = scale2(st & 1 ? v.z : v.x, mul, bf16), hi = scale2(st & 1 ? v.w : v.y, mul, bf16);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if constexpr (Cfg::q_in_regs) {
-                            mma16816(sc[mt][n], qa[mt * KS + st], lo, hi);
-                        } else {
-                            const uint4 q4 = *reinterpret_cast<const uint4 *>(q_smem + (mt * KS + st) * 512 + lane * 16);
-                            const uint32_t f4[4] = {q4.x, q4.y, q4.z, q4.w};
-                            mma16816(sc[mt][n], f4, lo, hi);
-                        }
-                    }
+                    ka[st][e] = op[st].x;
+                    ka[st][2 + e] = op[st].y;
                 }
             }
+#pragma unroll
+            for (int n = 0; n < R8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < KS; ++st) scores(sc, ka[st], st);
             // V rows: a first pass for the keys' scales, a second for the products
-            float vmul[4];
+            float vmul[4], vf[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int key = key0 + 2 * j + (k & 1) + 8 * (k >> 1);
@@ -498,81 +492,80 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
             float v_top = fmaxf(fmaxf(vf[0], vf[1]), fmaxf(vf[2], vf[3]));  // (NaN leaves it)
             v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, 1));
             v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, 2));
-            uint32_t pa[MT][4];
+            // those of this lane's scores' keys, g and g + 8, are with the lanes of j = g / 2
+            float of[4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)  // rows that pad see no more than the tail's own tokens
-                for (int e = 0; e < 2; ++e) lim[mt][e] = min(lim[mt][e], s.len);
-            weights(sc, kf, vf, v_top, paged + key0, true, pa);
+            for (int k = 0; k < 4; ++k) of[k] = __shfl_sync(0xffffffffu, vf[k], g >> 1);
+#pragma unroll
+            for (int n = 0; n < R8; ++n)  // rows that pad see no more than the tail's own tokens
+#pragma unroll
+                for (int e = 0; e < 2; ++e) lim[n][e] = min(lim[n][e], s.len);
+            uint32_t pb[R8][2];
+            weights(sc, kf[0], kf[1], g & 1 ? of[1] : of[0], g & 1 ? of[3] : of[2], v_top, paged + key0, true, pb);
 #pragma unroll
             for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
                 constexpr int HV = D == 64 ? 1 : 2;  // loads of 8 values of a lane's run of d's
 #pragma unroll
                 for (int z = 0; z < HV; ++z) {
-                    uint4 x[4];
+                    uint32_t x[4][4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int key = key0 + 2 * j + (k & 1) + 8 * (k >> 1);
                         const bool live = key < tail && s.slot >= 0;
                         const uint16_t *src = c.vt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)) + 128 * half +
                                               g * (D == 64 ? 8 : 16) + 8 * z;
-                        x[k] = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                        x[k].x = scale2(x[k].x, vmul[k], bf16);
-                        x[k].y = scale2(x[k].y, vmul[k], bf16);
-                        x[k].z = scale2(x[k].z, vmul[k], bf16);
-                        x[k].w = scale2(x[k].w, vmul[k], bf16);
+                        const uint4 v = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                        x[k][0] = scale2(v.x, vmul[k], bf16);
+                        x[k][1] = scale2(v.y, vmul[k], bf16);
+                        x[k][2] = scale2(v.z, vmul[k], bf16);
+                        x[k][3] = scale2(v.w, vmul[k], bf16);
                     }
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint32_t sel = q & 1 ? 0x7632 : 0x5410;
-                        auto word = [&](int k) { return (q >> 1) == 0 ? x[k].x : (q >> 1) == 1 ? x[k].y : (q >> 1) == 2 ? x[k].z : x[k].w; };
-                        const uint32_t b0 = __byte_perm(word(0), word(1), sel), b1 = __byte_perm(word(2), word(3), sel);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t va[4] = {__byte_perm(x[0][q], x[1][q], 0x5410), __byte_perm(x[0][q], x[1][q], 0x7632),
+                                                __byte_perm(x[2][q], x[3][q], 0x5410), __byte_perm(x[2][q], x[3][q], 0x7632)};
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][16 * half + 8 * z + q], pa[mt], b0, b1);
+                        for (int n = 0; n < R8; ++n) mma16816(o[n][8 * half + 4 * z + q], va, pb[n][0], pb[n][1]);
                     }
                 }
             }
         }
 
-        // ---- join the four warps: into shared memory, each in units of its own maximum's share
+        // ---- join the warps: into shared memory, each in units of the common maximum
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < R8; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[mt][e];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (j == 0) {
-                    s_ml[w][mt * 16 + g + 8 * e][0] = m[mt][e];
-                    s_ml[w][mt * 16 + g + 8 * e][1] = sum;
-                }
+                float sum = l[n][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (g == 0) *reinterpret_cast<float2 *>(s_ml[w][n * 8 + 2 * j + e]) = make_float2(m[n][e], sum);
             }
         __syncthreads();  // every warp's ring is idle, and the maxima are there
         float *merge = reinterpret_cast<float *>(smem);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < R8; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + g + 8 * e;
+                const int r = n * 8 + 2 * j + e;
                 float top = s_ml[0][r][0];
 #pragma unroll
-                for (int k = 1; k < kDecWarps; ++k) top = fmaxf(top, s_ml[k][r][0]);
-                const float f = ex2(m[mt][e] - top) * (v_ref / kWeightUnit);
+                for (int k = 1; k < W; ++k) top = fmaxf(top, s_ml[k][r][0]);
+                const float f = ex2(m[n][e] - top) * (v_ref / kWeightUnit);
                 float *to = merge + (w * R + r) * D;
-                // column 2j (and 2j + 1) of tile nt is d = n * run + nt within its 128 (or 64)
-                constexpr int run = D == 64 ? 8 : 16;
+                constexpr int run = D == 64 ? 8 : 16;  // a lane's d's: g * run + 2 mt (row g), + 1 (row g + 8)
+                if (r < rows) {
 #pragma unroll
-                for (int n = 0; n < NT; n += 4)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int d = (n / 16) * 128 * (D != 64) + (2 * j + q) * run + (D == 64 ? n : n % 16);
-                        *reinterpret_cast<float4 *>(to + d) = make_float4(o[mt][n][2 * e + q] * f, o[mt][n + 1][2 * e + q] * f,
-                                                                          o[mt][n + 2][2 * e + q] * f, o[mt][n + 3][2 * e + q] * f);
-                    }
+                    for (int mt = 0; mt < MT; mt += 2)
+                        *reinterpret_cast<float4 *>(to + (mt / 8) * 128 + g * run + 2 * (mt % 8)) =
+                            make_float4(o[n][mt][e] * f, o[n][mt][2 + e] * f, o[n][mt + 1][e] * f, o[n][mt + 1][2 + e] * f);
+                }
             }
         if (tid < R) {
             float top = s_ml[0][tid][0], sum = 0.0f;
-            for (int k = 1; k < kDecWarps; ++k) top = fmaxf(top, s_ml[k][tid][0]);
-            for (int k = 0; k < kDecWarps; ++k) sum += s_ml[k][tid][1] * ex2(s_ml[k][tid][0] - top);
+            for (int k = 1; k < W; ++k) top = fmaxf(top, s_ml[k][tid][0]);
+            for (int k = 0; k < W; ++k) sum += s_ml[k][tid][1] * ex2(s_ml[k][tid][0] - top);
             s_part[tid][0] = top;
             s_part[tid][1] = sum;
         }
@@ -580,7 +573,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
         auto merged = [&](int r, int d) {
             float4 x = *reinterpret_cast<const float4 *>(merge + r * D + d);
 #pragma unroll
-            for (int k = 1; k < kDecWarps; ++k) {
+            for (int k = 1; k < W; ++k) {
                 const float4 y = *reinterpret_cast<const float4 *>(merge + (k * R + r) * D + d);
                 x.x += y.x;
                 x.y += y.y;
@@ -604,52 +597,91 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
             if (a.lse) a.lse[(int64_t)row * c.H + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
         };
         if (t_first == 0 && t_end == tiles) {
-            for (int k = tid; k < rows * (D / 4); k += kDecThreads) {
+            for (int k = tid; k < rows * (D / 4); k += THREADS) {
                 const int r = k / (D / 4), d = k % (D / 4) * 4;
                 store(r, d, merged(r, d), s_part[r][1]);
             }
             if (tid < rows) store_lse(tid, s_part[tid][0], s_part[tid][1]);
             __syncthreads();
         } else {
+            // The CTAs that share the item: those of its first and of its last unit.  Each leaves its part in
+            // the scratch and counts itself; the last of a group joins the group's parts (in the place of the
+            // group's first), the last group's the groups'.
+            const long long N = share.ctas, total = share.total, i0 = u - t_first, i1 = i0 + tiles - 1;
+            const int c0 = (int)(((i0 + 1) * N - 1) / total), c1 = (int)(((i1 + 1) * N - 1) / total);
+            const int nc = c1 - c0 + 1, me = (int)blockIdx.x - c0;
             const int64_t pf = partial_floats(R, D);
-            float *slot = a.partial + (2 * (int64_t)blockIdx.x + (t_first == 0 ? 1 : 0)) * pf;
-            for (int k = tid; k < rows * (D / 4); k += kDecThreads) {
+            auto slot_of = [&](int k) { return a.partial + (2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * pf; };
+            float *slot = slot_of(me);
+            for (int k = tid; k < rows * (D / 4); k += THREADS) {
                 const int r = k / (D / 4), d = k % (D / 4) * 4;
                 __stcg(reinterpret_cast<float4 *>(slot + r * D + d), merged(r, d));
             }
             if (tid < rows) __stcg(reinterpret_cast<float2 *>(slot + R * D + 2 * tid), make_float2(s_part[tid][0], s_part[tid][1]));
-            // the CTAs that share the item: those of its first and of its last unit
-            const long long i0 = u - t_first, i1 = i0 + tiles - 1;
-            const long long c0 = ((i0 + 1) * N - 1) / total, c1 = ((i1 + 1) * N - 1) / total;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int n = atomicAdd(a.counters + c0, 1);
-                s_last = n == (int)(c1 - c0);
-                if (s_last) a.counters[c0] = 0;
-                __threadfence();
-            }
-            __syncthreads();
-            if (s_last) {
-                const int nc = (int)(c1 - c0) + 1;
-                auto slot_of = [&](int k) { return a.partial + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * pf; };
-                for (int k = tid; k < rows * (D / 4); k += kDecThreads) {
-                    const int r = k / (D / 4), d = k % (D / 4) * 4;
+            const bool two = nc > 2 * kJoinGroup;
+            // `n` parts from part `first`, `step` apart, joined: onto part `first`, or into the result
+            auto join = [&](int first, int n, int step, bool last) {
+                float2 *ml = reinterpret_cast<float2 *>(smem);  // [n][rows] maximum, sum; then the part's factor
+                float *top_sum = s_part[0];
+                for (int k = tid; k < n * rows; k += THREADS)
+                    ml[k] = __ldcg(reinterpret_cast<const float2 *>(slot_of(first + k / rows * step) + R * D) + k % rows);
+                __syncthreads();
+                if (tid < rows) {
                     float top = kNoScore, sum = 0.0f;
-                    for (int q = 0; q < nc; ++q) top = fmaxf(top, __ldcg(slot_of(q) + R * D + 2 * r));
+                    for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k * rows + tid].x);
+                    for (int k = 0; k < n; ++k) {
+                        const float f = ex2(ml[k * rows + tid].x - top);
+                        sum = fmaf(ml[k * rows + tid].y, f, sum);
+                        ml[k * rows + tid].x = f;
+                    }
+                    top_sum[2 * tid] = top;
+                    top_sum[2 * tid + 1] = sum;
+                }
+                __syncthreads();
+                for (int k = tid; k < rows * (D / 4); k += THREADS) {
+                    const int r = k / (D / 4), d = k % (D / 4) * 4;
                     float4 x = make_float4(0, 0, 0, 0);
-                    for (int q = 0; q < nc; ++q) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(q) + R * D + 2 * r));
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(slot_of(q) + r * D + d));
-                        const float f = ex2(ml.x - top);
-                        sum += ml.y * f;
+#pragma unroll 8
+                    for (int q = 0; q < n; ++q) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + r * D + d));
+                        const float f = ml[q * rows + r].x;
                         x.x = fmaf(y.x, f, x.x);
                         x.y = fmaf(y.y, f, x.y);
                         x.z = fmaf(y.z, f, x.z);
                         x.w = fmaf(y.w, f, x.w);
                     }
-                    store(r, d, x, sum);
-                    if (d == 0) store_lse(r, top, sum);
+                    if (last)
+                        store(r, d, x, top_sum[2 * r + 1]);
+                    else
+                        __stcg(reinterpret_cast<float4 *>(slot_of(first) + r * D + d), x);
+                }
+                if (tid < rows) {
+                    if (last)
+                        store_lse(tid, top_sum[2 * tid], top_sum[2 * tid + 1]);
+                    else
+                        __stcg(reinterpret_cast<float2 *>(slot_of(first) + R * D) + tid, make_float2(top_sum[2 * tid], top_sum[2 * tid + 1]));
+                }
+            };
+            auto arrive = [&](int32_t *counter, int n) {  // whether this CTA is the last of n
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const int k = atomicAdd(counter, 1);
+                    s_last = k == n - 1;
+                    if (s_last) *counter = 0;
+                    __threadfence();
+                }
+                __syncthreads();
+                return s_last != 0;
+            };
+            if (!two) {
+                if (arrive(a.counters + c0, nc)) join(0, nc, 1, true);
+            } else {
+                const int first = me / kJoinGroup * kJoinGroup, n = min(kJoinGroup, nc - first);
+                if (arrive(a.counters + kMaxDecodeCtas + 2 * (c0 + first) + (first == 0), n)) {
+                    join(first, n, 1, false);
+                    const int parts = (nc + kJoinGroup - 1) / kJoinGroup;
+                    if (arrive(a.counters + c0, parts)) join(0, parts, kJoinGroup, true);
                 }
             }
             __syncthreads();
@@ -659,12 +691,12 @@ __global__ void __launch_bounds__(kDecThreads, DecodeCfg<D, MT>::ctas) k_kv_deco
     }
 }
 
-template <int CODE, int D, int MT>
+template <int CODE, int D, int R8>
 cudaError_t decode_launch(const Plan &p, const DecodeArgs &a, cudaStream_t s) {
-    using Cfg = DecodeCfg<D, MT>;
-    cudaError_t e = allow_smem<k_kv_decode<CODE, D, MT>>(p, Cfg::smem);
+    using Cfg = DecodeCfg<D, R8>;
+    const cudaError_t e = allow_smem<k_kv_decode<CODE, D, R8>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_decode<CODE, D, MT><<<p.sm_count * Cfg::ctas, kDecThreads, Cfg::smem, s>>>(a);
+    k_kv_decode<CODE, D, R8><<<p.sm_count, Cfg::warps * 32, Cfg::smem, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -29,6 +29,13 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {  // a in the 
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// An 8 x 8 tile of 16-bit values, in the layout of a product's result, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // Codes of a word to fp16 pairs: (byte 0, byte 1) and (byte 2, byte 3).  int8: the
 // byte with its sign bit flipped is code + 128; as the low byte of 0x6400 it reads 1024 + code + 128.
 // bias() is done once for a word before its bytes may be interleaved.
@@ -121,16 +128,41 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
-// Which d's a lane's operand bytes hold.  Lane (g, j) = (lane / 4, lane % 4).  In
+// Which d's a lane's bytes of a key hold.  Lane (g, j) = (lane / 4, lane % 4).  In
 // the first product its bytes of a key are D/4 values in D/64 chunks of 16: chunk
 // i starts at d = k_dim(j, i), and step s of the product (k = 16) takes 4 of
-// them.  (The order of d is free as long as q has the same one.)
+// them, two for k = 2j, 2j+1 and two for k = 2j+8, 2j+9.  (The order of d is free
+// as long as q has the same one.)
 template <int D>
 __device__ __forceinline__ constexpr int k_dim(int j, int i) {
     return D == 64 ? j * 16 : 128 * (i >> 1) + j * 32 + 16 * (i & 1);
 }
-// The 16 rows' q operand of step s: rows g and g + 8, four d's each, the row's
-// first two d's for k = 2j, 2j+1 and the others for k = 2j+8, 2j+9.
+
+// The first product's operand of one 16-bit row, this lane's D/4 values of it: op[s] of step s is
+// (two values for k = 2j, 2j+1; two for k = 2j+8, 2j+9).  The four lanes of a g hold a row
+// together; all 32 lanes call this.  Returns the factor that undoes the scaling.
+template <int D>
+__device__ __forceinline__ float row_operand(const uint16_t *src, bool live, int j, bool bf16, uint2 (&op)[D / 16]) {
+    uint4 x[D / 32];
+    float amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
+            amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
+        }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    float mul, f;
+    row_scale(amax, mul, f);
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {  // chunk st / 4, four values at 4 * (st % 4)
+        const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
+        op[st] = make_uint2(scale2(st & 1 ? v.z : v.x, mul, bf16), scale2(st & 1 ? v.w : v.y, mul, bf16));
+    }
+    return f;
+}
 
 }  // namespace kv
 }  // namespace si

@@ -35,64 +35,37 @@ constexpr int kWeighRows = 64;  // rows whose operand lies in shared memory at a
 
 template <int D>
 struct WeighCfg {
-    static constexpr int stage = 16 * D;  // a warp's 16 keys
-    static constexpr int stages = D == 256 ? 4 : 8;
-    static constexpr int ring = kDecWarps * stages * stage;
+    static constexpr int warps = D == 256 ? 8 : 16;
+    static constexpr int stage = 16 * D;  // a piece of 16 keys
+    static constexpr int stages = 128 * 1024 / (warps * stage);
+    static constexpr int ring = warps * stages * stage;
     static constexpr int q_bytes = kWeighRows / 8 * (D / 16) * 256;
-    static constexpr int smem = ring + q_bytes + kWeighRows * 8;
-    static constexpr int ctas = D == 64 ? 6 : D == 128 ? 4 : 2;
+    static constexpr int sums = warps * 32 * 16 * 4;  // the sums of a warp's last 32 pieces
+    static constexpr int smem = ring + q_bytes + sums + kWeighRows * 8;
 };
 
 template <int CODE, int D>
-__global__ void __launch_bounds__(kDecThreads, WeighCfg<D>::ctas) k_kv_weigh_few(const WeighArgs a) {
+__global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(const WeighArgs a) {
     using Cfg = WeighCfg<D>;
-    constexpr int KS = D / 16, CH = D / 16;
+    constexpr int W = Cfg::warps, KS = D / 16, CH = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_scan[kDecWarps];
-    __shared__ long long s_off;
-    __shared__ int s_b;
     const Ctx &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
     const bool bf16 = a.bf16;
 
-    // ---- this CTA's share of the units (64 tokens of a kv head; the unfinished page is one)
-    const int per = (c.B + kDecThreads - 1) / kDecThreads;
-    auto units_of = [&](int b) -> long long { return (long long)seq_tiles(c, load_seq(c, b).len) * c.Hk; };
-    long long mine = 0;
-    for (int b = tid * per; b < min(c.B, (tid + 1) * per); ++b) mine += units_of(b);
-    long long incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-    }
-    if (lane == 31) s_scan[w] = incl;
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-    for (int k = 0; k < kDecWarps; ++k) {
-        if (k < w) before += s_scan[k];
-        total += s_scan[k];
-    }
-    const long long N = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-    if (blockIdx.x >= N) return;
-    const long long u_begin = blockIdx.x * total / N, u_end = (blockIdx.x + 1) * total / N;
-    if (before <= u_begin && u_begin < before + mine) {
-        int b = tid * per;
-        long long at = before, n;
-        while (at + (n = units_of(b)) <= u_begin) {
-            at += n;
-            ++b;
-        }
-        s_b = b;
-        s_off = u_begin - at;
-    }
-    __syncthreads();
-    int b = s_b;
-    long long off = s_off, u = u_begin;
+    const Share share = take_share<W>(c.B, [&](int b) -> long long { return (long long)seq_tiles(c, load_seq(c, b).len) * c.Hk; });
+    if (blockIdx.x >= share.ctas) return;
+    int b = share.b;
+    long long off = share.off, u = share.begin;
     const uint32_t ring = smem_addr(smem) + w * (Cfg::stages * Cfg::stage);
     uint8_t *q_smem = smem + Cfg::ring;
-    float2 *rowf = reinterpret_cast<float2 *>(smem + Cfg::ring + Cfg::q_bytes);  // factor, lse log2 e
+    float *sums = reinterpret_cast<float *>(smem + Cfg::ring + Cfg::q_bytes) + w * 512;
+    float2 *rowf = reinterpret_cast<float2 *>(smem + Cfg::ring + Cfg::q_bytes + Cfg::sums);  // factor, lse log2 e
+    uint32_t chunk_at[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) chunk_at[k] = tile_at<D>((lane + 32 * k) / CH, (lane + 32 * k) % CH);
 
-    while (u < u_end) {
+    while (u < share.end) {
         const Seq s = load_seq(c, b);
         const int tiles = seq_tiles(c, s.len);
         const long long n_units = (long long)tiles * c.Hk;
@@ -102,48 +75,68 @@ __global__ void __launch_bounds__(kDecThreads, WeighCfg<D>::ctas) k_kv_weigh_few
             continue;
         }
         const int h = (int)(off / tiles), t_first = (int)(off % tiles);
-        const int t_end = (int)min((long long)tiles, t_first + (u_end - u));
+        const int t_end = (int)min((long long)tiles, t_first + (share.end - u));
         const int paged = s.len & ~(c.P - 1), old = s.len - s.n, paged_tiles = (paged + 63) / 64;
         const int all_rows = s.n * c.G;
         const int64_t acc_at = ((int64_t)b * c.Hk + h) * a.acc_stride;
+        // this warp's pieces: every W-th of those of the units' full pages
+        const int p_first = 4 * t_first + w, p_stop = min(4 * t_end, paged >> 4);
+        const int count = p_stop > p_first ? (p_stop - p_first + W - 1) / W : 0;
 
         // rows in blocks of 64 (one block, but for many rows of 256 values): the first takes up the earlier sums
         for (int rb = 0; rb == 0 || rb * kWeighRows < all_rows; ++rb) {
             const int rows = min(kWeighRows, all_rows - rb * kWeighRows), nts = (rows + 7) / 8;
             const int lim_min = old + rb * kWeighRows / c.G + 1;
-            __syncthreads();  // the last block's readers are done
-            for (int nt = w; nt < nts; nt += kDecWarps) {
+            int pid0 = -1, pid1 = -1;
+            float ks0 = 0.0f, ks1 = 0.0f;
+            auto fetch = [&](int set, int first) {
+                const int i = first + lane;
+                int p = -1;
+                if (i < count) p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
+                const float f = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : __int_as_float(0x7fc00000);
+                if (set) {
+                    pid1 = p;
+                    ks1 = f;
+                } else {
+                    pid0 = p;
+                    ks0 = f;
+                }
+            };
+            auto copy = [&](int i, int stage) {
+                if (i < count) {
+                    const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
+                    if (p >= 0) {
+                        const uint8_t *kc = c.kc + page_at(c, p, h) + (uint32_t)((((p_first + W * i) << 4) & (c.P - 1)) * D + lane * 16);
+                        const uint32_t to = ring + stage * Cfg::stage;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) cp_async16(to + chunk_at[k], kc + 512 * k);
+                    }
+                }
+                cp_async_commit();
+            };
+            if (count > 0) {
+                fetch(0, 0);
+#pragma unroll
+                for (int i = 0; i < Cfg::stages - 1; ++i) copy(i, i);
+                if (count > 32) fetch(1, 32);
+            }
+            __syncthreads();  // the last block's readers of q are done
+            for (int nt = w; nt < nts; nt += W) {
                 const int r = nt * 8 + g, rr = rb * kWeighRows + r;
                 const bool live = r < rows;
-                const int i = live ? rr / c.G : 0, head = live ? h * c.G + rr % c.G : 0;
-                const uint16_t *src = a.q.p + (s.row0 + i) * a.q.row + head * a.q.head;
-                uint4 x[D / 32];
-                float amax = 0.0f;
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
-                        amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
-                    }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                float mul, f;
-                row_scale(amax, mul, f);
+                const int i = live ? rr / c.G : 0, head = h * c.G + (live ? rr % c.G : 0);
+                uint2 op[KS];
+                const float f = row_operand<D>(a.q.p + (s.row0 + i) * a.q.row + head * a.q.head, live, j, bf16, op);
                 if (j == 0)  // (a row that pads weighs nothing)
                     rowf[r] = live ? make_float2(f * a.scale2, a.lse[(int64_t)(s.row0 + i) * c.H + head] * kLog2e)
                                    : make_float2(0.0f, INFINITY);
 #pragma unroll
-                for (int st = 0; st < KS; ++st) {
-                    const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
-                    *reinterpret_cast<uint2 *>(q_smem + (nt * KS + st) * 256 + lane * 8) =
-                        make_uint2(scale2(st & 1 ? v.z : v.x, mul, bf16), scale2(st & 1 ? v.w : v.y, mul, bf16));
-                }
+                for (int st = 0; st < KS; ++st) *reinterpret_cast<uint2 *>(q_smem + (nt * KS + st) * 256 + lane * 8) = op[st];
             }
             __syncthreads();
 
-            // the sums of this warp's 16 keys from t0 on; lane < 16 has the earlier sum of key t0 + lane in `was`
-            auto sums = [&](const uint32_t (&ka)[KS][4], float kf0, float kf1, int t0, bool masked, float was) {
+            // the rows' weights of 16 keys from t0 on, into 16 places of `to`
+            auto weigh = [&](const uint32_t (&ka)[KS][4], float kf0, float kf1, int t0, bool masked, float *to) {
                 float sum[2] = {0.0f, 0.0f};
                 for (int nt = 0; nt < nts; ++nt) {
                     float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -170,116 +163,81 @@ __global__ void __launch_bounds__(kDecThreads, WeighCfg<D>::ctas) k_kv_weigh_few
                     sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
                     sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
                 }
-                const float lo = __shfl_sync(0xffffffffu, sum[0], (lane & 7) * 4), hi = __shfl_sync(0xffffffffu, sum[1], (lane & 7) * 4);
-                if (lane < 16 && t0 + lane < s.len) a.acc_out[acc_at + t0 + lane] = was + (lane < 8 ? lo : hi);
+                if (j < 2) to[g + 8 * j] = j ? sum[1] : sum[0];
             };
-            auto earlier = [&](int t0) -> float {
-                const int t = t0 + lane;
-                if (lane >= 16 || t >= s.len) return 0.0f;
-                if (rb > 0) return a.acc_out[acc_at + t];
-                return a.acc_in && t < old ? a.decay * a.acc_in[acc_at + t] : 0.0f;
+            // n sums (of pieces p_first + W i from i = first on, or of the tokens from t0 on) onto the earlier ones
+            auto flush = [&](int n, int first, int t0) {
+                __syncwarp();
+#pragma unroll 4
+                for (int k = lane; k < n; k += 32) {
+                    const int t = t0 >= 0 ? t0 + k : ((p_first + W * (first + k / 16)) << 4) + k % 16;
+                    if (t < s.len) {
+                        float was = 0.0f;
+                        if (rb > 0)
+                            was = a.acc_out[acc_at + t];
+                        else if (a.acc_in && t < old)
+                            was = a.decay * a.acc_in[acc_at + t];
+                        a.acc_out[acc_at + t] = was + sums[k];
+                    }
+                }
+                __syncwarp();
             };
 
-            const int t_stop = min(t_end, paged_tiles), count = t_stop - t_first;
-            int pid0 = -2, pid1 = -2;
-            float ks0 = 0.0f, ks1 = 0.0f;
-            auto fetch = [&](int set, int first) {
-                const int t = first + lane, token = (t_first + t) * 64 + 16 * w;
-                int p = -2;
-                if (t < count && token < paged) p = (int)load_page(c, b, token >> a.log_page);
-                const float f = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : __int_as_float(0x7fc00000);
-                if (set) {
-                    pid1 = p;
-                    ks1 = f;
-                } else {
-                    pid0 = p;
-                    ks0 = f;
+            int stage = 0;
+            for (int i = 0; i < count; ++i) {
+                if ((i & 31) == 0 && i > 0) {
+                    flush(512, i - 32, -1);
+                    if (i + 32 < count) fetch(((i >> 5) + 1) & 1, i + 32);
                 }
-            };
-            auto copy = [&](int t) {
-                if (t < count) {
-                    const int p = __shfl_sync(0xffffffffu, (t & 32) ? pid1 : pid0, t & 31);
-                    if (p >= 0) {
-                        const int64_t at = page_at(c, p, h) + (int64_t)(((t_first + t) * 64 + 16 * w) & (c.P - 1)) * D;
-                        const uint32_t to = ring + (t % Cfg::stages) * Cfg::stage;
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            const int ci = lane + 32 * k;
-                            cp_async16(to + tile_at<D>(ci / CH, ci % CH), c.kc + at + ci * 16);
-                        }
-                    }
-                }
-                cp_async_commit();
-            };
-            float was = 0.0f, was_next = 0.0f;
-            if (count > 0) {
-                fetch(0, 0);
-                fetch(1, 32);
-#pragma unroll
-                for (int t = 0; t < Cfg::stages - 1; ++t) copy(t);
-                was_next = earlier(t_first * 64 + 16 * w);
-            }
-            for (int t = 0; t < count; ++t) {
-                if ((t & 31) == 0 && t > 0) fetch(((t >> 5) + 1) & 1, (t & ~31) + 32);
-                copy(t + Cfg::stages - 1);
-                was = was_next;
-                if (t + 1 < count) was_next = earlier((t_first + t + 1) * 64 + 16 * w);
+                copy(i + Cfg::stages - 1, stage == 0 ? Cfg::stages - 1 : stage - 1);
                 cp_async_wait<Cfg::stages - 1>();
                 __syncwarp();
-                const int p = __shfl_sync(0xffffffffu, (t & 32) ? pid1 : pid0, t & 31);
-                const float ks = __shfl_sync(0xffffffffu, (t & 32) ? ks1 : ks0, t & 31);
-                const int t0 = (t_first + t) * 64 + 16 * w;
-                if (p == -2) continue;
-                const uint32_t kt = ring + (t % Cfg::stages) * Cfg::stage;
+                const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
+                const float ks = __shfl_sync(0xffffffffu, (i & 32) ? ks1 : ks0, i & 31);
+                const int t0 = (p_first + W * i) << 4;
+                const uint32_t kt = ring + stage * Cfg::stage;
+                stage = stage + 1 == Cfg::stages ? 0 : stage + 1;
                 uint32_t ka[KS][4];
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i)
+                for (int q = 0; q < D / 64; ++q)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        uint4 x = lds128(kt + tile_at<D>(8 * n + g, k_dim<D>(j, i) / 16));
+                        uint4 x = lds128(kt + tile_at<D>(8 * n + g, k_dim<D>(j, q) / 16));
                         if (p < 0) x = make_uint4(0, 0, 0, 0);  // (a page outside the cache: its factor is NaN)
-                        codes_to_half<CODE>(code_bias<CODE>(x.x), ka[4 * i][n], ka[4 * i][2 + n]);
-                        codes_to_half<CODE>(code_bias<CODE>(x.y), ka[4 * i + 1][n], ka[4 * i + 1][2 + n]);
-                        codes_to_half<CODE>(code_bias<CODE>(x.z), ka[4 * i + 2][n], ka[4 * i + 2][2 + n]);
-                        codes_to_half<CODE>(code_bias<CODE>(x.w), ka[4 * i + 3][n], ka[4 * i + 3][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.x), ka[4 * q][n], ka[4 * q][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.y), ka[4 * q + 1][n], ka[4 * q + 1][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.z), ka[4 * q + 2][n], ka[4 * q + 2][2 + n]);
+                        codes_to_half<CODE>(code_bias<CODE>(x.w), ka[4 * q + 3][n], ka[4 * q + 3][2 + n]);
                     }
-                sums(ka, ks, ks, t0, t0 + 16 > lim_min, was);
+                if (t0 + 16 <= lim_min)
+                    weigh(ka, ks, ks, t0, false, sums + (i & 31) * 16);
+                else
+                    weigh(ka, ks, ks, t0, true, sums + (i & 31) * 16);
                 __syncwarp();
             }
             cp_async_wait<0>();
+            if (count > 0) flush(((count - 1) % 32 + 1) * 16, (count - 1) & ~31, -1);
 
-            // ---- the unfinished page's rows
-            const int tail = s.len - paged, key0 = 16 * w;
-            if (t_end > paged_tiles && key0 < tail) {
+            // ---- the unfinished page's rows, 16 for each of the last four warps
+            const int tail = s.len - paged, key0 = 16 * (w - (W - 4));
+            if (t_end > paged_tiles && key0 >= 0 && key0 < tail) {
                 uint32_t ka[KS][4];
                 float kf[2];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const int key = key0 + 8 * n + g;
                     const bool live = key < tail && s.slot >= 0;
-                    const uint16_t *src = c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0));
-                    uint4 x[D / 32];
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < D / 64; ++k)
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
-                            amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
-                        }
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                    float mul;
-                    row_scale(amax, mul, kf[n]);
+                    uint2 op[KS];
+                    kf[n] = row_operand<D>(c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)), live, j, bf16, op);
                     if (s.slot < 0) kf[n] = __int_as_float(0x7fc00000);
 #pragma unroll
                     for (int st = 0; st < KS; ++st) {
-                        const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
-                        ka[st][n] = scale2(st & 1 ? v.z : v.x, mul, bf16);
-                        ka[st][2 + n] = scale2(st & 1 ? v.w : v.y, mul, bf16);
+                        ka[st][n] = op[st].x;
+                        ka[st][2 + n] = op[st].y;
                     }
                 }
-                sums(ka, kf[0], kf[1], paged + key0, true, earlier(paged + key0));
+                weigh(ka, kf[0], kf[1], paged + key0, true, sums);
+                flush(16, 0, paged + key0);
             }
         }
         u += t_end - t_first;
@@ -457,7 +415,7 @@ static cudaError_t few(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighCfg<D>;
     cudaError_t e = allow_smem<k_kv_weigh_few<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_weigh_few<CODE, D><<<p.sm_count * Cfg::ctas, kDecThreads, Cfg::smem, s>>>(a);
+    k_kv_weigh_few<CODE, D><<<p.sm_count, Cfg::warps * 32, Cfg::smem, s>>>(a);
     return cudaGetLastError();
 }
 template <int CODE, int D>
