@@ -34,7 +34,7 @@ size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int 
     // A buffer for larger bounds serves smaller ones, so this takes the most that any call within the bounds needs:
     // a call with fewer sequences or rows may be split more (at most sm_count CTAs of 256 rows together).
     const size_t D = p.desc.head_dim;
-    size_t most = (size_t)p.sm_count * 2 * (size_t)partial_floats(8 * row_tiles(p, max_new), p.desc.head_dim) * sizeof(float);
+    size_t most = (size_t)p.sm_count * DecodeCfg<64, 1>::ctas * 2 * (size_t)partial_floats(8 * row_tiles(p, max_new), p.desc.head_dim) * sizeof(float);
     if (many_rows(p, max_new)) {
         const size_t row_heads = (size_t)total_new * p.desc.n_heads;
         size_t n = row_heads * 32;                                         // 32 splits at most, and

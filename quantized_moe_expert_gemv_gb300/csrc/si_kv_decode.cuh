@@ -17,8 +17,9 @@
 //    quarter of the matrix and softmax work, and a batch of 64 sequences took
 //    273 us.  Between the two products P^T is transposed in registers.
 //  * Work: units of 64 tokens of one (sequence, kv head, row group), numbered in
-//    order; each CTA (one an SM) takes an equal share of consecutive units,
-//    whatever the sequences' lengths.  A CTA joins its warps' results for each
+//    order; each CTA (two an SM, so that one copies while the other joins its
+//    warps) takes an equal share of consecutive units, whatever the sequences'
+//    lengths.  A CTA joins its warps' results for each
 //    item it touches; an item that lies in several CTAs is joined by the last of
 //    them to arrive (in groups of 16 where there are many), in the CTAs' order:
 //    the same inputs give the same bits.
@@ -44,12 +45,13 @@ constexpr float kLazy = 4.0f, kWeightUnit = 2048.0f;
 constexpr float kNoScore = -1e30f;  // a running maximum before the first score
 
 // R8: column tiles of 8 rows.  As many warps as the registers allow (the second product's sums are
-// D R8 / 4 a lane), then as many stages as fit 192 KB.
+// D R8 / 4 a lane), then as many stages as fit 96 KB a CTA.
 template <int D, int R8>
 struct DecodeCfg {
-    static constexpr int warps = D * R8 <= 128 ? 16 : D * R8 <= 256 ? 12 : 8;
+    static constexpr int ctas = 2;  // a SM
+    static constexpr int warps = D * R8 <= 128 ? 8 : D * R8 <= 256 ? 6 : 4;
     static constexpr int stage = 32 * D;  // bytes of one piece, K and V
-    static constexpr int stages = 192 * 1024 / (warps * stage);
+    static constexpr int stages = 96 * 1024 / (warps * stage);
     static constexpr int ring = warps * stages * stage;
     static constexpr bool q_in_regs = D * R8 <= 256;
     static constexpr int q_bytes = q_in_regs ? 0 : R8 * (D / 16) * 256;
@@ -141,13 +143,12 @@ __device__ __forceinline__ Share take_share(int B, F units_of) {
 }
 
 template <int CODE, int D, int R8>
-__global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(const DecodeArgs a) {
+__global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>::ctas) k_kv_decode(const DecodeArgs a) {
     using Cfg = DecodeCfg<D, R8>;
     constexpr int W = Cfg::warps, THREADS = W * 32;
     constexpr int R = 8 * R8;       // rows of an item
     constexpr int MT = D / 16;      // row tiles of the second product
     constexpr int KS = D / 16;      // steps of the first
-    constexpr int CH = D / 16;      // 16-byte chunks of a key
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_last;
     __shared__ __align__(8) float s_ml[W][R][2];
@@ -178,9 +179,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
 
     const uint32_t ring = smem_addr(smem) + w * (Cfg::stages * Cfg::stage);
     uint8_t *q_smem = smem + Cfg::ring;
-    uint32_t chunk_at[D / 32];  // where this lane's chunks of a piece go
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) chunk_at[k] = tile_at<D>((lane + 32 * k) / CH, (lane + 32 * k) % CH);
+    PieceCopy<D> piece;
+    piece.init(lane);
+    KeyLoad<D> keys;
+    keys.init(g, j);
+    // V: keys 2j and 2j + 1 (and eight on), this lane's run of d's
+    const uint32_t v_at0 = D == 64 ? tile_at<D>(2 * j, g >> 1) + (g & 1) * 8 : tile_at<D>(2 * j, g);
+    const uint32_t v_at1 = D == 64 ? tile_at<D>(2 * j + 1, g >> 1) + (g & 1) * 8 : tile_at<D>(2 * j + 1, g);
 
     while (u < u_end) {
         const Seq s = load_seq(c, b);
@@ -204,14 +209,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
         const int p_first = 4 * t_first + w;
         const int p_stop = min(min(4 * t_end, paged >> 4), (lim_max + 15) >> 4);  // no row sees a later piece
         const int count = p_stop > p_first ? (p_stop - p_first + W - 1) / W : 0;
-        int pid0 = -1, pid1 = -1;
+        int pid0 = 0, pid1 = 0;
         float ks0 = 0.0f, ks1 = 0.0f, vs0 = 0.0f, vs1 = 0.0f;
         auto fetch = [&](int set, int first) {
             const int i = first + lane;
-            int p = -1;
-            if (i < count) p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
-            const float ks = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : 0.0f;
-            const float vs = p >= 0 ? __ldg(c.vs + (int64_t)p * c.Hk + h) : 0.0f;
+            int p = 0;
+            float ks = 0.0f, vs = 0.0f;
+            if (i < count) {
+                p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
+                ks = vs = __int_as_float(0x7fc00000);
+                if (p >= 0) {
+                    ks = __ldg(c.ks + (int64_t)p * c.Hk + h);
+                    vs = __ldg(c.vs + (int64_t)p * c.Hk + h);
+                }
+                p = max(p, 0);  // (not one of the cache's pages: the first one's codes, and NaN for what sees them)
+            }
             if (set) {
                 pid1 = p;
                 ks1 = ks;
@@ -225,16 +237,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
         auto copy = [&](int i, int stage) {
             if (i < count) {
                 const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
-                if (p >= 0) {
-                    const int64_t at = page_at(c, p, h) + (uint32_t)((((p_first + W * i) << 4) & (c.P - 1)) * D + lane * 16);
-                    const uint8_t *kc = c.kc + at, *vc = c.vc + at;
-                    const uint32_t to = ring + stage * Cfg::stage;
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        cp_async16(to + chunk_at[k], kc + 512 * k);
-                        cp_async16(to + chunk_at[k] + 16 * D, vc + 512 * k);
-                    }
-                }
+                const int64_t at = page_at(c, p, h) + (uint32_t)((((p_first + W * i) << 4) & (c.P - 1)) * D + lane * 16);
+                const uint32_t to = ring + stage * Cfg::stage;
+                piece.template run<0>(to, c.kc + at);
+                piece.template run<16 * D>(to, c.vc + at);
             }
             cp_async_commit();
         };
@@ -375,27 +381,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
             copy(i + Cfg::stages - 1, stage == 0 ? Cfg::stages - 1 : stage - 1);
             cp_async_wait<Cfg::stages - 1>();
             __syncwarp();
-            const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
             const float ks = __shfl_sync(0xffffffffu, (i & 32) ? ks1 : ks0, i & 31);
             const float vs = __shfl_sync(0xffffffffu, (i & 32) ? vs1 : vs0, i & 31);
             const int t0 = (p_first + W * i) << 4;
-            const uint32_t kt = ring + stage * Cfg::stage, vt = kt + 16 * D;
+            const uint32_t kt = ring + stage * Cfg::stage;
             stage = stage + 1 == Cfg::stages ? 0 : stage + 1;
-            if (p < 0) {  // not one of the cache's pages: NaN for the rows that see it
-#pragma unroll
-                for (int n = 0; n < R8; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (t0 < lim[n][e]) l[n][e] = __int_as_float(0x7fc00000);
-                continue;
-            }
             float sc[R8][4];
 #pragma unroll
             for (int n = 0; n < R8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-#pragma unroll
-            for (int q = 0; q < D / 64; ++q) {
-                const uint4 x = lds128(kt + tile_at<D>(g, k_dim<D>(j, q) / 16));
-                const uint4 y = lds128(kt + tile_at<D>(8 + g, k_dim<D>(j, q) / 16));
+            auto chunk = [&](const uint4 &x, const uint4 &y, int q) {
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -404,6 +398,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
                     codes_to_half<CODE>(code_bias<CODE>(ys[e]), ka[1], ka[3]);
                     scores(sc, ka, 4 * q + e);
                 }
+            };
+            chunk(keys.template load<0, 0>(kt), keys.template load<0, 1>(kt), 0);
+            if constexpr (D > 64) chunk(keys.template load<1, 0>(kt), keys.template load<1, 1>(kt), 1);
+            if constexpr (D > 128) {
+                chunk(keys.template load<2, 0>(kt), keys.template load<2, 1>(kt), 2);
+                chunk(keys.template load<3, 0>(kt), keys.template load<3, 1>(kt), 3);
             }
             uint32_t pb[R8][2];
             if (t0 + 16 <= lim_min)
@@ -412,24 +412,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
                 weights(sc, ks, ks, vs, vs, vs, t0, true, pb);
             // V^T: keys 2j, 2j+1 and 2j+8, 2j+9; rows g and g + 8 of a row tile are two of this lane's run of d's
             constexpr int HW = D == 64 ? 2 : 4;  // words of a lane's run of d's (8 or 16 of each 64 or 128)
-#pragma unroll
-            for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-                uint32_t x[4][HW];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = 2 * j + (k & 1) + 8 * (k >> 1);
-                    if constexpr (D == 64) {
-                        const uint2 v = lds64(vt + tile_at<D>(key, g >> 1) + (g & 1) * 8);
-                        x[k][0] = code_bias<CODE>(v.x);
-                        x[k][1] = code_bias<CODE>(v.y);
-                    } else {
-                        const uint4 v = lds128(vt + tile_at<D>(key, 8 * half + g));
-                        x[k][0] = code_bias<CODE>(v.x);
-                        x[k][1] = code_bias<CODE>(v.y);
-                        x[k][2] = code_bias<CODE>(v.z);
-                        x[k][3] = code_bias<CODE>(v.w);
-                    }
-                }
+            auto values = [&](const uint32_t (&x)[4][HW], int half) {
 #pragma unroll
                 for (int q = 0; q < HW; ++q) {  // d = 4 q + e of the run: row tile (4 q + e) / 2, its rows g or g + 8
                     uint32_t b0[4], b1[4];
@@ -443,6 +426,29 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, 1) k_kv_decode(c
 #pragma unroll
                         for (int n = 0; n < R8; ++n) mma16816(o[n][8 * half + 2 * q + e], va, pb[n][0], pb[n][1]);
                     }
+                }
+            };
+            constexpr int VT = 16 * D;  // V's tile lies behind K's
+            if constexpr (D == 64) {
+                uint32_t x[4][HW];
+                codes2<CODE>(lds64<VT>(kt + v_at0), x[0]);
+                codes2<CODE>(lds64<VT>(kt + v_at1), x[1]);
+                codes2<CODE>(lds64<VT + 8 * D>(kt + v_at0), x[2]);
+                codes2<CODE>(lds64<VT + 8 * D>(kt + v_at1), x[3]);
+                values(x, 0);
+            } else {
+                uint32_t x[4][HW];
+                codes4<CODE>(lds128<VT>(kt + v_at0), x[0]);
+                codes4<CODE>(lds128<VT>(kt + v_at1), x[1]);
+                codes4<CODE>(lds128<VT + 8 * D>(kt + v_at0), x[2]);
+                codes4<CODE>(lds128<VT + 8 * D>(kt + v_at1), x[3]);
+                values(x, 0);
+                if constexpr (D == 256) {
+                    codes4<CODE>(lds128<VT + 128>(kt + v_at0), x[0]);
+                    codes4<CODE>(lds128<VT + 128>(kt + v_at1), x[1]);
+                    codes4<CODE>(lds128<VT + 8 * D + 128>(kt + v_at0), x[2]);
+                    codes4<CODE>(lds128<VT + 8 * D + 128>(kt + v_at1), x[3]);
+                    values(x, 1);
                 }
             }
             __syncwarp();
@@ -696,7 +702,7 @@ cudaError_t decode_launch(const Plan &p, const DecodeArgs &a, cudaStream_t s) {
     using Cfg = DecodeCfg<D, R8>;
     const cudaError_t e = allow_smem<k_kv_decode<CODE, D, R8>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_decode<CODE, D, R8><<<p.sm_count, Cfg::warps * 32, Cfg::smem, s>>>(a);
+    k_kv_decode<CODE, D, R8><<<p.sm_count * Cfg::ctas, Cfg::warps * 32, Cfg::smem, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -60,6 +60,19 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t
     }
 }
 
+template <int CODE>
+__device__ __forceinline__ void codes4(const uint4 &v, uint32_t (&to)[4]) {
+    to[0] = code_bias<CODE>(v.x);
+    to[1] = code_bias<CODE>(v.y);
+    to[2] = code_bias<CODE>(v.z);
+    to[3] = code_bias<CODE>(v.w);
+}
+template <int CODE>
+__device__ __forceinline__ void codes2(const uint2 &v, uint32_t (&to)[2]) {
+    to[0] = code_bias<CODE>(v.x);
+    to[1] = code_bias<CODE>(v.y);
+}
+
 // The power-of-two scaling of a row whose largest magnitude is amax: values
 // are multiplied by `mul`, and `factor` undoes it.  mul is zero, and factor NaN,
 // for a row that is not finite.
@@ -109,24 +122,63 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
     return (uint32_t)(r * D + (((c & ~7) | ((c ^ r) & 7)) << 4));
 }
 
+// 16 bytes at src + SRC to dst + DST.
+template <int DST, int SRC>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+template <int OFF = 0>
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4 + %5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a), "n"(OFF));
     return v;
 }
+template <int OFF = 0>
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2 + %3];" : "=r"(v.x), "=r"(v.y) : "r"(a), "n"(OFF));
     return v;
 }
+
+// A warp's copy of a piece, 16 rows of D bytes that follow each other at src,
+// into a tile: lane's chunks are lane + 32 k.  Rows eight apart have the same
+// place but for their distance, so a lane needs few addresses.
+template <int D>
+struct PieceCopy {
+    static constexpr int CH = D / 16, STEP = 32 / CH, DISTINCT = 8 / STEP;  // rows between a lane's chunks; addresses
+    uint32_t at[DISTINCT];
+    __device__ __forceinline__ void init(int lane) {
+#pragma unroll
+        for (int k = 0; k < DISTINCT; ++k) at[k] = tile_at<D>(lane / CH + STEP * k, lane % CH);
+    }
+    // chunks of `src` (already at the lane's first) to the tile at `to`, OFF bytes on
+    template <int OFF>
+    __device__ __forceinline__ void run(uint32_t to, const uint8_t *src) const {
+        if constexpr (D == 64) {
+            cp_async16<OFF, 0>(to + at[0], src);
+            cp_async16<OFF + 8 * 64, 512>(to + at[0], src);
+        } else if constexpr (D == 128) {
+            cp_async16<OFF, 0>(to + at[0], src);
+            cp_async16<OFF, 512>(to + at[1], src);
+            cp_async16<OFF + 8 * 128, 1024>(to + at[0], src);
+            cp_async16<OFF + 8 * 128, 1536>(to + at[1], src);
+        } else {
+            cp_async16<OFF, 0>(to + at[0], src);
+            cp_async16<OFF, 512>(to + at[1], src);
+            cp_async16<OFF, 1024>(to + at[2], src);
+            cp_async16<OFF, 1536>(to + at[3], src);
+            cp_async16<OFF + 8 * 256, 2048>(to + at[0], src);
+            cp_async16<OFF + 8 * 256, 2560>(to + at[1], src);
+            cp_async16<OFF + 8 * 256, 3072>(to + at[2], src);
+            cp_async16<OFF + 8 * 256, 3584>(to + at[3], src);
+        }
+    }
+};
 
 // Which d's a lane's bytes of a key hold.  Lane (g, j) = (lane / 4, lane % 4).  In
 // the first product its bytes of a key are D/4 values in D/64 chunks of 16: chunk
@@ -163,6 +215,22 @@ __device__ __forceinline__ float row_operand(const uint16_t *src, bool live, int
     }
     return f;
 }
+
+// The keys' operand of every step, from a tile of codes: keys g (ka[.][0], [2]) and g + 8 ([1], [3]).
+// at[q]: tile_at<D>(g, k_dim(j, q) / 16) for q < 2.
+template <int D>
+struct KeyLoad {
+    uint32_t at[D == 64 ? 1 : 2];
+    __device__ __forceinline__ void init(int g, int j) {
+        at[0] = tile_at<D>(g, k_dim<D>(j, 0) / 16);
+        if constexpr (D > 64) at[1] = tile_at<D>(g, k_dim<D>(j, 1) / 16);
+    }
+    // chunk Q of key g (HI 0) or g + 8 (HI 1)
+    template <int Q, int HI>
+    __device__ __forceinline__ uint4 load(uint32_t tile) const {
+        return lds128<128 * (Q >> 1) + 8 * D * HI>(tile + at[D == 64 ? 0 : Q & 1]);
+    }
+};
 
 }  // namespace kv
 }  // namespace si

@@ -47,7 +47,7 @@ struct WeighCfg {
 template <int CODE, int D>
 __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(const WeighArgs a) {
     using Cfg = WeighCfg<D>;
-    constexpr int W = Cfg::warps, KS = D / 16, CH = D / 16;
+    constexpr int W = Cfg::warps, KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     const Ctx &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
@@ -61,9 +61,10 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
     uint8_t *q_smem = smem + Cfg::ring;
     float *sums = reinterpret_cast<float *>(smem + Cfg::ring + Cfg::q_bytes) + w * 512;
     float2 *rowf = reinterpret_cast<float2 *>(smem + Cfg::ring + Cfg::q_bytes + Cfg::sums);  // factor, lse log2 e
-    uint32_t chunk_at[D / 32];
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) chunk_at[k] = tile_at<D>((lane + 32 * k) / CH, (lane + 32 * k) % CH);
+    PieceCopy<D> piece;
+    piece.init(lane);
+    KeyLoad<D> keys;
+    keys.init(g, j);
 
     while (u < share.end) {
         const Seq s = load_seq(c, b);
@@ -87,13 +88,17 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
         for (int rb = 0; rb == 0 || rb * kWeighRows < all_rows; ++rb) {
             const int rows = min(kWeighRows, all_rows - rb * kWeighRows), nts = (rows + 7) / 8;
             const int lim_min = old + rb * kWeighRows / c.G + 1;
-            int pid0 = -1, pid1 = -1;
+            int pid0 = 0, pid1 = 0;
             float ks0 = 0.0f, ks1 = 0.0f;
             auto fetch = [&](int set, int first) {
                 const int i = first + lane;
-                int p = -1;
-                if (i < count) p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
-                const float f = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : __int_as_float(0x7fc00000);
+                int p = 0;
+                float f = 0.0f;
+                if (i < count) {
+                    p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
+                    f = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : __int_as_float(0x7fc00000);
+                    p = max(p, 0);  // (not one of the cache's pages: the first one's codes, and NaN for their weights)
+                }
                 if (set) {
                     pid1 = p;
                     ks1 = f;
@@ -105,12 +110,8 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
             auto copy = [&](int i, int stage) {
                 if (i < count) {
                     const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
-                    if (p >= 0) {
-                        const uint8_t *kc = c.kc + page_at(c, p, h) + (uint32_t)((((p_first + W * i) << 4) & (c.P - 1)) * D + lane * 16);
-                        const uint32_t to = ring + stage * Cfg::stage;
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) cp_async16(to + chunk_at[k], kc + 512 * k);
-                    }
+                    const uint8_t *kc = c.kc + page_at(c, p, h) + (uint32_t)((((p_first + W * i) << 4) & (c.P - 1)) * D + lane * 16);
+                    piece.template run<0>(ring + stage * Cfg::stage, kc);
                 }
                 cp_async_commit();
             };
@@ -192,23 +193,29 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
                 copy(i + Cfg::stages - 1, stage == 0 ? Cfg::stages - 1 : stage - 1);
                 cp_async_wait<Cfg::stages - 1>();
                 __syncwarp();
-                const int p = __shfl_sync(0xffffffffu, (i & 32) ? pid1 : pid0, i & 31);
                 const float ks = __shfl_sync(0xffffffffu, (i & 32) ? ks1 : ks0, i & 31);
                 const int t0 = (p_first + W * i) << 4;
                 const uint32_t kt = ring + stage * Cfg::stage;
                 stage = stage + 1 == Cfg::stages ? 0 : stage + 1;
                 uint32_t ka[KS][4];
-#pragma unroll
-                for (int q = 0; q < D / 64; ++q)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        uint4 x = lds128(kt + tile_at<D>(8 * n + g, k_dim<D>(j, q) / 16));
-                        if (p < 0) x = make_uint4(0, 0, 0, 0);  // (a page outside the cache: its factor is NaN)
-                        codes_to_half<CODE>(code_bias<CODE>(x.x), ka[4 * q][n], ka[4 * q][2 + n]);
-                        codes_to_half<CODE>(code_bias<CODE>(x.y), ka[4 * q + 1][n], ka[4 * q + 1][2 + n]);
-                        codes_to_half<CODE>(code_bias<CODE>(x.z), ka[4 * q + 2][n], ka[4 * q + 2][2 + n]);
-                        codes_to_half<CODE>(code_bias<CODE>(x.w), ka[4 * q + 3][n], ka[4 * q + 3][2 + n]);
-                    }
+                auto chunk = [&](const uint4 &x, int q, int n) {
+                    codes_to_half<CODE>(code_bias<CODE>(x.x), ka[4 * q][n], ka[4 * q][2 + n]);
+                    codes_to_half<CODE>(code_bias<CODE>(x.y), ka[4 * q + 1][n], ka[4 * q + 1][2 + n]);
+                    codes_to_half<CODE>(code_bias<CODE>(x.z), ka[4 * q + 2][n], ka[4 * q + 2][2 + n]);
+                    codes_to_half<CODE>(code_bias<CODE>(x.w), ka[4 * q + 3][n], ka[4 * q + 3][2 + n]);
+                };
+                chunk(keys.template load<0, 0>(kt), 0, 0);
+                chunk(keys.template load<0, 1>(kt), 0, 1);
+                if constexpr (D > 64) {
+                    chunk(keys.template load<1, 0>(kt), 1, 0);
+                    chunk(keys.template load<1, 1>(kt), 1, 1);
+                }
+                if constexpr (D > 128) {
+                    chunk(keys.template load<2, 0>(kt), 2, 0);
+                    chunk(keys.template load<2, 1>(kt), 2, 1);
+                    chunk(keys.template load<3, 0>(kt), 3, 0);
+                    chunk(keys.template load<3, 1>(kt), 3, 1);
+                }
                 if (t0 + 16 <= lim_min)
                     weigh(ka, ks, ks, t0, false, sums + (i & 31) * 16);
                 else
