@@ -84,6 +84,27 @@ __device__ __forceinline__ int seq_tiles(const Ctx &c, int len) {
     return (paged + 63) / 64 + (paged < len ? 1 : 0);
 }
 
+// An item's start and end (its first pages' addresses, q, the join) take a CTA as long as some units of
+// tokens: that many units without tokens go before each item's own, so that a share of many short sequences
+// costs no more than one of a long one.
+constexpr int kDecodeOver = 6, kWeighOver = 10;
+struct Segment {  // what a share takes of an item: its tiles [first, end) of `tiles`
+    int item, first, end, step;       // step: units that the share has used up
+    long long unit0, unit1;           // the units of the item's first and last tile
+};
+__device__ __forceinline__ Segment take_segment(int tiles, int over, long long off, long long u, long long u_end) {
+    Segment s;
+    const int all = tiles + over;
+    s.item = (int)(off / all);
+    const int x0 = (int)(off % all), x1 = (int)min((long long)all, x0 + (u_end - u));
+    s.first = max(0, x0 - over);
+    s.end = max(0, x1 - over);
+    s.step = x1 - x0;
+    s.unit0 = u - x0 + over;
+    s.unit1 = u - x0 + all - 1;
+    return s;
+}
+
 // A CTA's equal share [begin, end) of all units, and the sequence that `begin` lies in.  `units_of(b)`:
 // units of sequence b.  All threads call this; `some_empty`: whether a sequence has none.
 struct Share {
@@ -159,7 +180,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
 
     const Share share = take_share<W>(c.B, [&](int b) -> long long {
         const Seq s = load_seq(c, b);
-        return (long long)seq_tiles(c, s.len) * c.Hk * ((s.n * c.G + R - 1) / R);
+        const int tiles = seq_tiles(c, s.len);
+        return tiles == 0 ? 0ll : (long long)(tiles + kDecodeOver) * c.Hk * ((s.n * c.G + R - 1) / R);
     });
     // rows whose sequence has no token at all are in no unit: zeros
     if (share.some_empty)
@@ -191,15 +213,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
         const Seq s = load_seq(c, b);
         const int tiles = seq_tiles(c, s.len);
         const int groups = (s.n * c.G + R - 1) / R;
-        const long long n_units = (long long)tiles * c.Hk * groups;
+        const long long n_units = tiles == 0 ? 0ll : (long long)(tiles + kDecodeOver) * c.Hk * groups;
         if (off >= n_units) {  // on to the next sequence (one without units among them)
             off -= n_units;
             ++b;
             continue;
         }
-        const int item = (int)(off / tiles), t_first = (int)(off % tiles);
-        const int h = item / groups, rb = item % groups;
-        const int t_end = (int)min((long long)tiles, t_first + (u_end - u));
+        const Segment seg = take_segment(tiles, kDecodeOver, off, u, u_end);
+        u += seg.step;
+        off += seg.step;
+        const int t_first = seg.first, t_end = seg.end;
+        if (t_first == t_end) continue;
+        const int h = seg.item / groups, rb = seg.item % groups;
         const int rows = min(R, s.n * c.G - rb * R);
         const int paged = s.len & ~(c.P - 1), old = s.len - s.n;
         const int lim_min = old + rb * R / c.G + 1, lim_max = old + (rb * R + rows - 1) / c.G + 1;
@@ -613,8 +638,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             // The CTAs that share the item: those of its first and of its last unit.  Each leaves its part in
             // the scratch and counts itself; the last of a group joins the group's parts (in the place of the
             // group's first), the last group's the groups'.
-            const long long N = share.ctas, total = share.total, i0 = u - t_first, i1 = i0 + tiles - 1;
-            const int c0 = (int)(((i0 + 1) * N - 1) / total), c1 = (int)(((i1 + 1) * N - 1) / total);
+            const long long N = share.ctas, total = share.total;
+            const int c0 = (int)(((seg.unit0 + 1) * N - 1) / total), c1 = (int)(((seg.unit1 + 1) * N - 1) / total);
             const int nc = c1 - c0 + 1, me = (int)blockIdx.x - c0;
             const int64_t pf = partial_floats(R, D);
             auto slot_of = [&](int k) { return a.partial + (2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * pf; };
@@ -692,8 +717,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             }
             __syncthreads();
         }
-        u += t_end - t_first;
-        off += t_end - t_first;
     }
 }
 

@@ -35,9 +35,10 @@ constexpr int kWeighRows = 64;  // rows whose operand lies in shared memory at a
 
 template <int D>
 struct WeighCfg {
-    static constexpr int warps = D == 256 ? 8 : 16;
+    static constexpr int ctas = 2;  // a SM
+    static constexpr int warps = D == 256 ? 4 : 8;
     static constexpr int stage = 16 * D;  // a piece of 16 keys
-    static constexpr int stages = 128 * 1024 / (warps * stage);
+    static constexpr int stages = 64 * 1024 / (warps * stage);
     static constexpr int ring = warps * stages * stage;
     static constexpr int q_bytes = kWeighRows / 8 * (D / 16) * 256;
     static constexpr int sums = warps * 32 * 16 * 4;  // the sums of a warp's last 32 pieces
@@ -45,7 +46,7 @@ struct WeighCfg {
 };
 
 template <int CODE, int D>
-__global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(const WeighArgs a) {
+__global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_kv_weigh_few(const WeighArgs a) {
     using Cfg = WeighCfg<D>;
     constexpr int W = Cfg::warps, KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -53,7 +54,10 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
     const bool bf16 = a.bf16;
 
-    const Share share = take_share<W>(c.B, [&](int b) -> long long { return (long long)seq_tiles(c, load_seq(c, b).len) * c.Hk; });
+    const Share share = take_share<W>(c.B, [&](int b) -> long long {
+        const int tiles = seq_tiles(c, load_seq(c, b).len);
+        return tiles == 0 ? 0ll : (long long)(tiles + kWeighOver) * c.Hk;
+    });
     if (blockIdx.x >= share.ctas) return;
     int b = share.b;
     long long off = share.off, u = share.begin;
@@ -69,14 +73,17 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
     while (u < share.end) {
         const Seq s = load_seq(c, b);
         const int tiles = seq_tiles(c, s.len);
-        const long long n_units = (long long)tiles * c.Hk;
+        const long long n_units = tiles == 0 ? 0ll : (long long)(tiles + kWeighOver) * c.Hk;
         if (off >= n_units) {
             off -= n_units;
             ++b;
             continue;
         }
-        const int h = (int)(off / tiles), t_first = (int)(off % tiles);
-        const int t_end = (int)min((long long)tiles, t_first + (share.end - u));
+        const Segment seg = take_segment(tiles, kWeighOver, off, u, share.end);
+        u += seg.step;
+        off += seg.step;
+        const int h = seg.item, t_first = seg.first, t_end = seg.end;
+        if (t_first == t_end) continue;
         const int paged = s.len & ~(c.P - 1), old = s.len - s.n, paged_tiles = (paged + 63) / 64;
         const int all_rows = s.n * c.G;
         const int64_t acc_at = ((int64_t)b * c.Hk + h) * a.acc_stride;
@@ -247,8 +254,6 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, 1) k_kv_weigh_few(con
                 flush(16, 0, paged + key0);
             }
         }
-        u += t_end - t_first;
-        off += t_end - t_first;
     }
 }
 
@@ -422,7 +427,7 @@ static cudaError_t few(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighCfg<D>;
     cudaError_t e = allow_smem<k_kv_weigh_few<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_weigh_few<CODE, D><<<p.sm_count, Cfg::warps * 32, Cfg::smem, s>>>(a);
+    k_kv_weigh_few<CODE, D><<<p.sm_count * Cfg::ctas, Cfg::warps * 32, Cfg::smem, s>>>(a);
     return cudaGetLastError();
 }
 template <int CODE, int D>
