@@ -11,7 +11,7 @@
 // Roles: warps 0-3 and 4-7 are the softmax of the two row tiles, a thread a row;
 // warps 8-11 turn codes into fp16 tiles in shared memory (K with d innermost, V
 // with d innermost too: the second product takes V as its transposed operand);
-// one thread of warp 12 issues the products.  While one row tile's products run,
+// warp 12 issues the products (warps 13-15 only lend their registers).  While one row tile's products run,
 // the other's softmax does.
 // Bound: at D = 128 a pair of row tiles and 128 keys takes 2048 cycles of the
 // tensor cores and 2048 of the exponential unit (256 x 128 at 16 a cycle), so
@@ -24,7 +24,9 @@ namespace si {
 namespace kv {
 
 constexpr int kPrRows = 256, kPrKeys = kTileRows;
-constexpr int kPrThreads = 13 * 32;
+constexpr int kPrThreads = 16 * 32;
+// Registers a thread after the roles part (of 128 each at the launch): 2 x 128 x 176 + 128 x 112 + 128 x 40 = 64512 <= 65536.
+constexpr int kPrRegSoftmax = 176, kPrRegTiles = 112, kPrRegMma = 40;
 constexpr int kPrFactorSlots = 4;
 
 template <int D>
@@ -52,13 +54,22 @@ struct PromptArgs {
     float *partial;  // [splits][T][H][D], then [splits][T][H][2]
 };
 
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int CODE, int D>
 __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a) {
     using Cfg = PromptCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     const Ctx &c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform)
     const bool bf16 = a.bf16;
 
     // ---- which rows: the last ones of each sequence first (they see the most keys)
@@ -115,8 +126,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
     bool ok = true;
-    // Bounded waits, of a warp (its lanes give up together) and of the one thread that issues the
-    // products.  A role that gives up goes on to the end of the kernel; the others run out in turn.
+    // A warp's bounded wait (its lanes give up together).  A role that gives up goes on to the end of
+    // the kernel; the others run out in turn.
     auto wait = [&](int i, int parity) {
         if (ok && !mbar_wait_warp(bar(i), (uint32_t)parity, a.budget)) {
             ok = false;
@@ -124,16 +135,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         }
         return ok;
     };
-    auto wait_one = [&](int i, int parity) {
-        if (ok && !mbar_wait_spin(bar(i), (uint32_t)parity, a.budget)) {
-            ok = false;
-            set_status(c.status, SI_ERR_TIMEOUT);
-        }
-        return ok;
-    };
-
     if (warp < 8) {
         // ================================================= softmax: a thread a row
+        reg_inc<kPrRegSoftmax>();
         const int x = warp >> 2, r = tid & 127;
         const int rr = rb * kPrRows + x * 128 + r;
         const bool live = x * 128 + r < rows;
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         }
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
-        float m = kNoScore, v_ref = 1e-30f;
+        float m = kNoScore, v_ref = 1e-30f, v_inv = kWeightUnit / 1e-30f;
         f32x2 l2 = pk2(0.0f, 0.0f);
         const int n = ntx[x];
         for (int i = 0; i < n; ++i) {
@@ -171,34 +175,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             tc::fence_after_sync();
             const bool whole = key0 + kPrKeys <= paged;                 // a factor for every 16 keys
             const bool all = __all_sync(0xffffffffu, !live || key0 + kPrKeys <= lim) && whole;
-            // the largest score
-            float top = -INFINITY, v_top = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t z[32];
-                tc::tmem_ld32(ts + 32 * q, z);
-                tc::tmem_wait_ld();
-                if (all) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float t = __uint_as_float(z[16 * e]);
-#pragma unroll
-                        for (int k = 1; k < 16; ++k) t = fmaxf(t, __uint_as_float(z[16 * e + k]));
-                        top = fmaxf(top, t * kf[32 * q + 16 * e]);
-                        v_top = fmaxf(v_top, vf[32 * q + 16 * e]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int col = 32 * q + k;
-                        if (key0 + col < lim) top = fmaxf(top, __uint_as_float(z[k]) * kf[col]);
-                        v_top = fmaxf(v_top, vf[col]);
-                    }
-                }
-            }
-            top *= qf;
-            const bool grow = top > m + kLazy, scale = v_top > v_ref;
-            if (__any_sync(0xffffffffu, grow || scale)) {
+            // Rescale of the sums so far where the maximum or the V scales' reference moves.
+            auto adjust = [&](float top, float v_top) {
+                const bool grow = top > m + kLazy, scale = v_top > v_ref;
+                if (!__any_sync(0xffffffffu, grow || scale)) return;
                 float f = 1.0f;
                 if (grow) {
                     f = ex2(m - top);
@@ -208,9 +188,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 if (scale) {
                     f *= v_ref / v_top;
                     v_ref = v_top;
+                    v_inv = kWeightUnit / v_top;
                 }
                 if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
                         tc::tmem_ld32(to + 32 * q, o);
@@ -220,31 +201,68 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         tmem_st32(to + 32 * q, o);
                     }
                 }
-            }
-            const float inv = kWeightUnit / v_ref;
-            const f32x2 m2 = pk2(-m, -m);
+            };
+            if (all) {
+                uint32_t z[4][32];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t z[32], p[16];
-                tc::tmem_ld32(ts + 32 * q, z);
+                for (int q = 0; q < 4; ++q) tc::tmem_ld32(ts + 32 * q, z[q]);
                 tc::tmem_wait_ld();
-                if (all) {
+                float top = -INFINITY, v_top = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float y = __uint_as_float(z[q >> 1][16 * (q & 1)]);
+#pragma unroll
+                    for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(z[q >> 1][16 * (q & 1) + k]));
+                    top = fmaxf(top, y * kf[16 * q]);
+                    v_top = fmaxf(v_top, vf[16 * q]);
+                }
+                adjust(top * qf, v_top);
+                const f32x2 m2 = pk2(-m, -m);
+                f32x2 lo = pk2(0.0f, 0.0f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float f = kf[32 * q + 16 * e] * qf, w = vf[32 * q + 16 * e] * inv;
+                        const float f = kf[32 * q + 16 * e] * qf, w = vf[32 * q + 16 * e] * v_inv;
                         const f32x2 f2 = pk2(f, f), w2 = pk2(w, w);
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
-                            const f32x2 t = fma2(pk2(__uint_as_float(z[16 * e + k]), __uint_as_float(z[16 * e + k + 1])), f2, m2);
-                            float t0, t1;
-                            up2(t, t0, t1);
-                            const f32x2 pp = pk2(ex2(t0), ex2(t1));
-                            l2 = add2(l2, pp);
-                            up2(mul2(pp, w2), t0, t1);
-                            p[8 * e + k / 2] = half2_bits(t0, t1);
+                            const f32x2 y = fma2(pk2(__uint_as_float(z[q][16 * e + k]), __uint_as_float(z[q][16 * e + k + 1])), f2, m2);
+                            float y0, y1;
+                            up2(y, y0, y1);
+                            const f32x2 pp = pk2(ex2(y0), ex2(y1));
+                            if (k & 2)
+                                lo = add2(lo, pp);
+                            else
+                                l2 = add2(l2, pp);
+                            up2(mul2(pp, w2), y0, y1);
+                            p[8 * e + k / 2] = half2_bits(y0, y1);
                         }
                     }
-                } else {
+                    tmem_st16(ts + 16 * q, p);
+                }
+                l2 = add2(l2, lo);
+            } else {
+                float top = -INFINITY, v_top = 0.0f;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t z[32];
+                    tc::tmem_ld32(ts + 32 * q, z);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int col = 32 * q + k;
+                        if (key0 + col < lim) top = fmaxf(top, __uint_as_float(z[k]) * kf[col]);
+                        v_top = fmaxf(v_top, vf[col]);
+                    }
+                }
+                adjust(top * qf, v_top);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t z[32], p[16];
+                    tc::tmem_ld32(ts + 32 * q, z);
+                    tc::tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
                         float w[2], pp[2];
@@ -252,13 +270,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         for (int e = 0; e < 2; ++e) {
                             const int col = 32 * q + k + e;
                             pp[e] = key0 + col < lim ? ex2(fmaf(__uint_as_float(z[k + e]), kf[col] * qf, -m)) : 0.0f;
-                            w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (vf[col] * inv);
+                            w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (vf[col] * v_inv);
                         }
                         l2 = add2(l2, pk2(pp[0], pp[1]));
                         p[k / 2] = half2_bits(w[0], w[1]);
                     }
+                    tmem_st16(ts + 16 * q, p);
                 }
-                tmem_st16(ts + 16 * q, p);
             }
             tmem_wait_st();
             tc::fence_before_sync();
@@ -323,25 +341,34 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         tc::fence_before_sync();
     } else if (warp < 12) {
         // ================================================= codes to fp16 tiles
+        reg_dec<kPrRegTiles>();
         const int pt = tid - 256;              // 0..127
         const int ch = pt & 3, r0 = pt >> 2;   // chunks ch, ch + 4 of rows r0 + 32 k
         constexpr int CC = D / 64;             // chunks of 16 codes of one row that a thread takes
         uint4 kx[4 * CC], vx[4 * CC];
         float kfx = 0.0f, vfx = 0.0f;          // factors of column pt
-        const float nan = __int_as_float(0x7fc00000);
-        // (a tile of full pages: the pages of this thread's four rows and of its column, then their codes)
-        auto page_of = [&](int t) -> int64_t { return load_page(c, b, t >> a.log_page); };
+        // A tile of full pages takes three steps, each a tile ahead of the next so that no load waits for
+        // another: the pages of this thread's four rows and of its column, their codes and scales, the tile.
+        // (A page outside the cache: the first one's codes, and factors NaN.)
+        int pg[5];
+        auto pages = [&](int i) {
+            const int key0 = (t_first + i) * kPrKeys;
+            if (i >= nt || key0 + kPrKeys > paged) return;
+            const int32_t *row = c.table + (int64_t)b * c.table_stride;
+#pragma unroll
+            for (int k = 0; k < 5; ++k) pg[k] = __ldg(row + ((key0 + (k < 4 ? r0 + 32 * k : pt)) >> a.log_page));
+        };
+        auto named = [&](int p) { return p >= 0 && p < c.n_pages; };
         auto load = [&](int i, bool v) {
             const int key0 = (t_first + i) * kPrKeys;
-            if (key0 + kPrKeys > paged) return;
+            if (i >= nt || key0 + kPrKeys > paged) return;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int t = key0 + r0 + 32 * k;
-                const int64_t p = page_of(t);
-                const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, p < 0 ? 0 : p, h) + (int64_t)(t & (c.P - 1)) * D + ch * 16;
+                const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, named(pg[k]) ? pg[k] : 0, h) +
+                                    ((key0 + r0 + 32 * k) & (c.P - 1)) * D + ch * 16;
 #pragma unroll
                 for (int q = 0; q < CC; ++q) {
-                    const uint4 y = *reinterpret_cast<const uint4 *>(at + 64 * q);
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + 64 * q));
                     if (v)
                         vx[k * CC + q] = y;
                     else
@@ -349,9 +376,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 }
             }
             if (!v) {
-                const int64_t p = page_of(key0 + pt);
-                kfx = p < 0 ? nan : c.ks[p * c.Hk + h];
-                vfx = p < 0 ? nan : c.vs[p * c.Hk + h];
+                const int64_t at = (int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + h;
+                kfx = __ldg(c.ks + at);
+                vfx = __ldg(c.vs + at);
+                if (!named(pg[4])) {
+                    set_status(c.status, SI_ERR_DEVICE);
+                    kfx = vfx = __int_as_float(0x7fc00000);
+                }
             }
         };
         auto store = [&](uint32_t tile, int i, bool v) {
@@ -373,10 +404,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             }
             key_rows<CODE, D>(c, s, b, h, v, key0, a.log_page, bf16, tile, kf + (v ? 128 : 0), pt);
         };
-        if (nt > 0) {
-            load(0, false);
-            load(0, true);
-        }
+        pages(0);
+        load(0, false);
+        load(0, true);
+        pages(1);
         for (int i = 0; i < nt; ++i) {
             const int st = i & 1;
             const bool whole = (t_first + i + 1) * kPrKeys <= paged;
@@ -390,66 +421,73 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             }
             tc::fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + st));
-            if (i + 1 < nt) load(i + 1, false);
+            load(i + 1, false);
             if (whole) {
                 if (i >= 2 && !wait(kBarVEmpty + st, ((i >> 1) - 1) & 1)) break;
                 store(base + Cfg::v + st * Cfg::tile, i, true);
                 tc::fence_proxy_async_smem();
             }
             mbar_arrive(bar(kBarVFull + st));
-            if (i + 1 < nt) load(i + 1, true);
+            load(i + 1, true);
+            pages(i + 2);
         }
-    } else if (lane == 0) {
+    } else {
+      reg_dec<kPrRegMma>();
+      if (warp == 12) {
         // ================================================= the products
         constexpr uint32_t id_qk = tc::idesc_f16_f32(128, kPrKeys);
         constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // V: transposed operand
+        const uint64_t q_desc = tc::sdesc_sw128(base + Cfg::q), k_desc = tc::sdesc_sw128(base + Cfg::k);
+        const uint64_t v_desc = sdesc_sw128_mn(base + Cfg::v, 16384);
         auto qk = [&](int x, int st) {
+            const uint64_t qd = q_desc + (x * Cfg::tile >> 4), kd = k_desc + (st * Cfg::tile >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                tc::mma_f16kind(tmem + x * 128, tc::sdesc_sw128(base + Cfg::q + x * Cfg::tile + at),
-                                tc::sdesc_sw128(base + Cfg::k + st * Cfg::tile + at), id_qk, k > 0);
+                constexpr int half = 16384 >> 4;
+                mma_ss(tmem + x * 128, qd + ((k >> 2) * half + (k & 3) * 2), kd + ((k >> 2) * half + (k & 3) * 2), id_qk, k > 0);
             }
-            tc::mma_commit(bar(kBarS + x));
+            mma_done(bar(kBarS + x));
         };
         auto pv = [&](int x, int st, bool acc) {
+            const uint64_t vd = v_desc + (st * Cfg::tile >> 4);
 #pragma unroll
             for (int k = 0; k < kPrKeys / 16; ++k)
-                mma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + 8 * k,
-                           sdesc_sw128_mn(base + Cfg::v + st * Cfg::tile + k * 2048, 16384), id_pv, acc || k > 0);
+                mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, vd + k * (2048 >> 4), id_pv, acc || k > 0);
         };
-        if (a.fault) wait_one(kBarNever, 0);
-        if (nt > 0 && wait_one(kBarQ, 0) && wait_one(kBarKFull, 0)) {
+        if (a.fault) wait(kBarNever, 0);
+        if (nt > 0 && wait(kBarQ, 0) && wait(kBarKFull, 0)) {
             tc::fence_after_sync();
-            for (int x = 0; x < 2; ++x)
-                if (ntx[x] > 0) qk(x, 0);
-            if (nt > 2) tc::mma_commit(bar(kBarKEmpty));
-            for (int i = 0; i < nt; ++i) {
+            if (ntx[0] > 0) qk(0, 0);
+            if (ntx[1] > 0) qk(1, 0);
+            if (nt > 2) mma_done(bar(kBarKEmpty));
+            for (int i = 0; i < nt && ok; ++i) {
                 const int st = i & 1;
-                if (!wait_one(kBarVFull + st, (i >> 1) & 1)) break;
-                if (i + 1 < nt && !wait_one(kBarKFull + (st ^ 1), ((i + 1) >> 1) & 1)) break;
+                if (!wait(kBarVFull + st, (i >> 1) & 1)) break;
+                if (i + 1 < nt && !wait(kBarKFull + (st ^ 1), ((i + 1) >> 1) & 1)) break;
+#pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (i >= ntx[x]) continue;
-                    if (!wait_one(kBarP + x, i & 1)) break;
+                    if (!wait(kBarP + x, i & 1)) break;
                     tc::fence_after_sync();
                     pv(x, st, i > 0);
                     if (i + 1 < ntx[x])
                         qk(x, st ^ 1);
                     else
-                        tc::mma_commit(bar(kBarO + x));
+                        mma_done(bar(kBarO + x));
                 }
                 if (!ok) break;
                 // (only what the producers will wait for: nothing arrives after the CTA's end)
-                if (i + 2 < nt) tc::mma_commit(bar(kBarVEmpty + st));
-                if (i + 3 < nt) tc::mma_commit(bar(kBarKEmpty + (st ^ 1)));
+                if (i + 2 < nt) mma_done(bar(kBarVEmpty + st));
+                if (i + 3 < nt) mma_done(bar(kBarKEmpty + (st ^ 1)));
             }
         }
         // whatever was issued is over before the tensor memory goes back
         if (!ok) {
-            tc::mma_commit(bar(kBarNever));
+            mma_done(bar(kBarNever));
             mbar_wait_bounded(bar(kBarNever), 0, 4000000000LL);
         }
         tc::fence_before_sync();
+      }
     }
     __syncwarp();
     __syncthreads();

@@ -29,12 +29,36 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+// The products (M = 128, k = 16) are issued by one elected lane of a warp whose
+// 32 lanes all run the issuing code: descriptors and tensor-memory addresses
+// then stay in the warp's uniform registers.  Issued from a branch that one lane
+// takes, each product cost 150 to 180 cycles of moving them there; so, 64, which
+// is what the product itself takes at N = 128.
+// D[tmem] (+)= A[smem] B[smem]; the same with A in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on an mbarrier once the products that the elected lane issued so far are done.
+__device__ __forceinline__ void mma_done(uint32_t mbar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(mbar)
         : "memory");
 }
 // Descriptor of an operand whose 64 innermost values (128 swizzled bytes) run
@@ -78,32 +102,36 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 }
 
 // One row of 16-bit values into an fp16 tile, by the four neighbouring threads
-// ch = 0..3 of its quad (each D/4 values); returns the factor that undoes the scaling.
+// ch = 0..3 of its quad (each D/4 values): the loads, then the scaled tile.
 template <int D>
-__device__ __forceinline__ float row_to_tile(const uint16_t *src, bool live, uint32_t tile, int row, int ch, bool bf16) {
-    constexpr int CC = D / 64;
-    uint4 y[CC][2];
-    float amax = 0.0f;
+struct RowLoad {
+    uint4 y[D / 64][2];
+    __device__ __forceinline__ void load(const uint16_t *src, bool live, int ch) {
 #pragma unroll
-    for (int q = 0; q < CC; ++q)
+        for (int q = 0; q < D / 64; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            y[q][e] = live ? *reinterpret_cast<const uint4 *>(src + ch * 16 + 64 * q + 8 * e) : make_uint4(0, 0, 0, 0);
-            amax = fmaxf(amax, amax8(y[q][e], bf16));
-        }
-    const unsigned quad = 0xfu << (threadIdx.x & 28);  // (the quad may be apart from the rest of its warp)
-    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
-    float mul, f;
-    row_scale(amax, mul, f);
+            for (int e = 0; e < 2; ++e)
+                y[q][e] = live ? *reinterpret_cast<const uint4 *>(src + ch * 16 + 64 * q + 8 * e) : make_uint4(0, 0, 0, 0);
+    }
+    // Returns the factor that undoes the scaling.
+    __device__ __forceinline__ float store(uint32_t tile, int row, int ch, bool bf16) const {
+        float amax = 0.0f;
 #pragma unroll
-    for (int q = 0; q < CC; ++q)
+        for (int q = 0; q < D / 64; ++q) amax = fmaxf(amax, fmaxf(amax8(y[q][0], bf16), amax8(y[q][1], bf16)));
+        const unsigned quad = 0xfu << (threadIdx.x & 28);  // (the quad may be apart from the rest of its warp)
+        amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+        float mul, f;
+        row_scale(amax, mul, f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            sts128(tile + f16_tile_at(row, 2 * (ch + 4 * q) + e), scale2(y[q][e].x, mul, bf16), scale2(y[q][e].y, mul, bf16),
-                   scale2(y[q][e].z, mul, bf16), scale2(y[q][e].w, mul, bf16));
-    return f;
-}
+        for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                sts128(tile + f16_tile_at(row, 2 * (ch + 4 * q) + e), scale2(y[q][e].x, mul, bf16), scale2(y[q][e].y, mul, bf16),
+                       scale2(y[q][e].z, mul, bf16), scale2(y[q][e].w, mul, bf16));
+        return f;
+    }
+};
 
 // 16 codes (chunk u/2 of a row) into units u and u + 1 of an fp16 tile.
 template <int CODE>
@@ -140,7 +168,9 @@ __device__ __forceinline__ void key_rows(const Ctx &c, const Seq &s, int b, int 
             f = p < 0 ? nan : (v ? c.vs : c.ks)[p * c.Hk + h];
         } else {
             const bool in = t < s.len && s.slot >= 0;
-            f = row_to_tile<D>((v ? c.vt : c.kt) + ring_at(c, in ? s.slot : 0, h, t), in, tile, row, ch, bf16);
+            RowLoad<D> x;
+            x.load((v ? c.vt : c.kt) + ring_at(c, in ? s.slot : 0, h, t), in, ch);
+            f = x.store(tile, row, ch, bf16);
             if (t < s.len && s.slot < 0) f = nan;
             if (t >= s.len) f = 0.0f;
         }

@@ -263,7 +263,7 @@ template <int D>
 struct WeighManyCfg {
     static constexpr int tile = kTileRows * D * 2;
     static constexpr int q = tile;
-    static constexpr int rows = q + 2 * tile;                 // [4][128] (factor, lse)
+    static constexpr int rows = q + 2 * tile;                 // [4][2][128] factor, -lse log2 e
     static constexpr int keyf = rows + 4 * 128 * 8;           // [128]
     static constexpr int bars = keyf + 128 * 4;
     static constexpr int smem = bars + 16 * 8 + 1024;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
     const Ctx &c = a.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform)
     const int b = blockIdx.z, h = blockIdx.y, key0 = blockIdx.x * kTileRows;
     const Seq s = load_seq(c, b);
     if (key0 >= s.len) return;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
 
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t *aligned = smem_raw + (base - smem_addr(smem_raw));
-    float2 *rowf = reinterpret_cast<float2 *>(aligned + Cfg::rows);
+    float *rowf = reinterpret_cast<float *>(aligned + Cfg::rows);  // [4][2][128]: factor, -lse log2 e
     float *keyf = reinterpret_cast<float *>(aligned + Cfg::keyf);
     auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
     if (tid == 0) {
@@ -317,13 +317,6 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
         }
         return ok;
     };
-    auto wait_one = [&](int i, int parity) {
-        if (ok && !mbar_wait_spin(bar(i), (uint32_t)parity, a.budget)) {
-            ok = false;
-            set_status(c.status, SI_ERR_TIMEOUT);
-        }
-        return ok;
-    };
 
     if (warp < 4) {
         // ================================================= a thread a key
@@ -332,7 +325,7 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
         const float was = t < old && a.acc_in ? a.decay * a.acc_in[at] : 0.0f;
         const int r_min = max(0, t - old) * c.G;  // the first row that sees the key
         const uint32_t ts = tmem + ((uint32_t)(32 * warp) << 16);
-        f32x2 sum = pk2(0.0f, 0.0f);
+        f32x2 sum = pk2(0.0f, 0.0f), sum1 = sum;
         float kf = 0.0f;
         if (wait(kWbK, 0)) kf = keyf[tid];
         const f32x2 kf2 = pk2(kf, kf);
@@ -340,33 +333,37 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
             if (!wait(kWbSFull + (i & 1), (i >> 1) & 1)) break;
             tc::fence_after_sync();
             const int r0 = (first + i) * kTileRows;
-            const float4 *rf = reinterpret_cast<const float4 *>(rowf + (i & 3) * 128);  // two rows each
+            const float4 *rf = reinterpret_cast<const float4 *>(rowf + (i & 3) * 256), *rl = rf + 32;  // four rows each
             const bool all = __all_sync(0xffffffffu, r0 >= r_min);
+            uint32_t z[2][32];
+            tc::tmem_ld32(ts + (i & 1) * 128, z[0]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t z[32];
-                tc::tmem_ld32(ts + (i & 1) * 128 + 32 * q, z);
                 tc::tmem_wait_ld();
+                if (q < 3) tc::tmem_ld32(ts + (i & 1) * 128 + 32 * q + 32, z[(q + 1) & 1]);
+                const uint32_t(&y)[32] = z[q & 1];
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const float4 v = rf[16 * q + k / 2];
-                    const f32x2 f2 = mul2(kf2, pk2(v.x, v.z));
-                    const f32x2 e = fma2(pk2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), f2, pk2(-v.y, -v.w));
-                    float e0, e1;
-                    up2(e, e0, e1);
-                    float p0 = ex2(e0), p1 = ex2(e1);
-                    if (!all) {
-                        if (r0 + 32 * q + k < r_min) p0 = 0.0f;
-                        if (r0 + 32 * q + k + 1 < r_min) p1 = 0.0f;
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 f = rf[8 * q + k / 4], l = rl[8 * q + k / 4];
+                    const f32x2 e0 = fma2(pk2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), mul2(kf2, pk2(f.x, f.y)), pk2(l.x, l.y));
+                    const f32x2 e1 = fma2(pk2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), mul2(kf2, pk2(f.z, f.w)), pk2(l.z, l.w));
+                    float p[4];
+                    up2(e0, p[0], p[1]);
+                    up2(e1, p[2], p[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2(p[e]);
+                        if (!all && r0 + 32 * q + k + e < r_min) p[e] = 0.0f;
                     }
-                    sum = add2(sum, pk2(p0, p1));
+                    sum = add2(sum, pk2(p[0], p[1]));
+                    sum1 = add2(sum1, pk2(p[2], p[3]));
                 }
             }
             tc::fence_before_sync();
             mbar_arrive(bar(kWbSEmpty + (i & 1)));
         }
         float x, y;
-        up2(sum, x, y);
+        up2(add2(sum, sum1), x, y);
         if (ok && t < s.len) a.acc_out[at] = was + (x + y);
     } else if (warp < 8) {
         // ================================================= K's tile, then q's
@@ -374,42 +371,57 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
         key_rows<CODE, D>(c, s, b, h, false, key0, a.log_page, a.bf16, base, keyf, pt);
         tc::fence_proxy_async_smem();
         mbar_arrive(bar(kWbK));
-        for (int i = 0; i < nt; ++i) {
-            if (i >= 2 && !wait(kWbQEmpty + (i & 1), ((i >> 1) - 1) & 1)) break;
+        RowLoad<D> x[4];
+        float lse = 0.0f;  // of row pt of the tile
+        auto load = [&](int i) {  // this thread's part of four rows of q tile i, and a row's lse
+            if (i >= nt) return;
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int r = (pt >> 2) + 32 * k, rr = (first + i) * kTileRows + r;
+                const int rr = (first + i) * kTileRows + (pt >> 2) + 32 * k;
                 const bool live = rr < all_rows;
                 const int row = s.row0 + (live ? rr / c.G : 0), head = h * c.G + (live ? rr % c.G : 0);
-                const float f = row_to_tile<D>(a.q.p + row * a.q.row + head * a.q.head, live, base + Cfg::q + (i & 1) * Cfg::tile,
-                                               r, ch, a.bf16);
-                if (ch == 0)
-                    rowf[(i & 3) * 128 + r] = live ? make_float2(f * a.scale2, a.lse[(int64_t)row * c.H + head] * kLog2e)
-                                                   : make_float2(0.0f, INFINITY);
+                x[k].load(a.q.p + row * a.q.row + head * a.q.head, live, ch);
             }
+            const int rr = (first + i) * kTileRows + pt;
+            lse = rr < all_rows ? a.lse[(int64_t)(s.row0 + rr / c.G) * c.H + h * c.G + rr % c.G] : INFINITY;
+        };
+        load(0);
+        for (int i = 0; i < nt; ++i) {
+            if (i >= 2 && !wait(kWbQEmpty + (i & 1), ((i >> 1) - 1) & 1)) break;
+            float *rf = rowf + (i & 3) * 256;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = (pt >> 2) + 32 * k;
+                const float f = x[k].store(base + Cfg::q + (i & 1) * Cfg::tile, r, ch, a.bf16);
+                if (ch == 0) rf[r] = f * a.scale2;
+            }
+            rf[128 + pt] = -lse * kLog2e;  // (a row that pads weighs nothing)
             tc::fence_proxy_async_smem();
             mbar_arrive(bar(kWbQFull + (i & 1)));
+            load(i + 1);
         }
-    } else if (lane == 0) {
+    } else {
         // ================================================= the products
         constexpr uint32_t id = tc::idesc_f16_f32(128, kTileRows);
-        if (a.fault) wait_one(kWbNever, 0);
-        if (wait_one(kWbK, 0))
+        const uint64_t k_desc = tc::sdesc_sw128(base), q_desc = tc::sdesc_sw128(base + Cfg::q);
+        if (a.fault) wait(kWbNever, 0);
+        if (wait(kWbK, 0))
             for (int i = 0; i < nt; ++i) {
                 const int st = i & 1;
-                if (!wait_one(kWbQFull + st, (i >> 1) & 1)) break;
-                if (i >= 2 && !wait_one(kWbSEmpty + st, ((i >> 1) - 1) & 1)) break;
+                if (!wait(kWbQFull + st, (i >> 1) & 1)) break;
+                if (i >= 2 && !wait(kWbSEmpty + st, ((i >> 1) - 1) & 1)) break;
                 tc::fence_after_sync();
+                const uint64_t qd = q_desc + (st * Cfg::tile >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                    tc::mma_f16kind(tmem + st * 128, tc::sdesc_sw128(base + at),
-                                    tc::sdesc_sw128(base + Cfg::q + st * Cfg::tile + at), id, k > 0);
+                    constexpr int half = 16384 >> 4;
+                    mma_ss(tmem + st * 128, k_desc + ((k >> 2) * half + (k & 3) * 2), qd + ((k >> 2) * half + (k & 3) * 2), id, k > 0);
                 }
-                tc::mma_commit(bar(kWbSFull + st));
-                if (i + 2 < nt) tc::mma_commit(bar(kWbQEmpty + st));
+                mma_done(bar(kWbSFull + st));
+                if (i + 2 < nt) mma_done(bar(kWbQEmpty + st));
             }
         if (!ok) {  // whatever was issued is over before the tensor memory goes back
-            tc::mma_commit(bar(kWbNever));
+            mma_done(bar(kWbNever));
             mbar_wait_bounded(bar(kWbNever), 0, 4000000000LL);
         }
         tc::fence_before_sync();
