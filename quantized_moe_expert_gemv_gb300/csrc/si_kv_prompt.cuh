@@ -11,7 +11,8 @@
 // Roles: warps 0-3 and 4-7 are the softmax of the two row tiles, a thread a row;
 // warps 8-11 turn codes into fp16 tiles in shared memory (K with d innermost, V
 // with d innermost too: the second product takes V as its transposed operand);
-// warp 12 issues the products (warps 13-15 only lend their registers).  While one row tile's products run,
+// warps 12 and 13 issue the two row tiles'
+// products (warps 14 and 15 only lend their registers).  While one row tile's products run,
 // the other's softmax does.
 // Bound: at D = 128 a pair of row tiles and 128 keys takes 2048 cycles of the
 // tensor cores and 2048 of the exponential unit (256 x 128 at 16 a cycle), so
@@ -39,7 +40,10 @@ struct PromptCfg {
     static constexpr int bars = factors + kPrFactorSlots * 2 * 128 * 4;
     static constexpr int smem = bars + 32 * 8 + 1024;                  // + alignment slack
 };
-enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarNever = 15, kBars = 16 };
+enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarNever = 16 };
+// Tensor memory columns: one S (the row tiles take turns: a softmax thread has its whole row in registers
+// before the other tile's product is issued), P of each row tile, O of each.
+constexpr int kTmS = 0, kTmP = 128, kTmO = 256;
 
 struct PromptArgs {
     Ctx c;
@@ -54,6 +58,8 @@ struct PromptArgs {
     float *partial;  // [splits][T][H][D], then [splits][T][H][2]
 };
 
+// The CTA's first barrier, which each role reaches from its own code once its first loads are under way.
+__device__ __forceinline__ void role_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPrThreads) : "memory"); }
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -103,28 +109,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     float *factors = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)) + Cfg::factors);
     auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
 
-    if (tid == 0) {
-        mbar_init(bar(kBarQ), 256);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kBarKFull + i), 128);
-            mbar_init(bar(kBarKEmpty + i), 1);
-            mbar_init(bar(kBarVFull + i), 128);
-            mbar_init(bar(kBarVEmpty + i), 1);
-            mbar_init(bar(kBarS + i), 1);
-            mbar_init(bar(kBarP + i), 128);
-            mbar_init(bar(kBarO + i), 1);
-        }
-        mbar_init(bar(kBarNever), 1);
-        fence_mbar_init();
-    }
-    if (warp == 12) {
-        tc::tmem_alloc(smem_addr(&s_tmem), 512);
-        tc::tmem_relinquish();
-    }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = s_tmem;
     bool ok = true;
     // A warp's bounded wait (its lanes give up together).  A role that gives up goes on to the end of
     // the kernel; the others run out in turn.
@@ -161,10 +145,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 sts128(base + Cfg::q + x * Cfg::tile + f16_tile_at(r, u), scale2(v[u].x, mul, bf16),
                        scale2(v[u].y, mul, bf16), scale2(v[u].z, mul, bf16), scale2(v[u].w, mul, bf16));
             tc::fence_proxy_async_smem();
-            mbar_arrive(bar(kBarQ));
         }
+        role_sync();
+        tc::fence_after_sync();
+        const uint32_t tmem = s_tmem;
+        mbar_arrive(bar(kBarQ));
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+        const uint32_t ts = tmem + lanes + kTmS, tp = tmem + lanes + kTmP + x * 64, to = tmem + lanes + kTmO + x * 128;
         float m = kNoScore, v_ref = 1e-30f, v_inv = kWeightUnit / 1e-30f;
         f32x2 l2 = pk2(0.0f, 0.0f);
         const int n = ntx[x];
@@ -174,7 +161,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             if (!wait(kBarS + x, i & 1)) break;
             tc::fence_after_sync();
             const bool whole = key0 + kPrKeys <= paged;                 // a factor for every 16 keys
-            const bool all = __all_sync(0xffffffffu, !live || key0 + kPrKeys <= lim) && whole;
             // Rescale of the sums so far where the maximum or the V scales' reference moves.
             auto adjust = [&](float top, float v_top) {
                 const bool grow = top > m + kLazy, scale = v_top > v_ref;
@@ -202,47 +188,28 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     }
                 }
             };
-            if (all) {
+            if (whole) {
                 uint32_t z[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32(ts + 32 * q, z[q]);
+                float v_top = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v_top = fmaxf(v_top, vf[16 * q]);
                 tc::tmem_wait_ld();
-                float top = -INFINITY, v_top = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float y = __uint_as_float(z[q >> 1][16 * (q & 1)]);
-#pragma unroll
-                    for (int k = 1; k < 16; ++k) y = fmaxf(y, __uint_as_float(z[q >> 1][16 * (q & 1) + k]));
-                    top = fmaxf(top, y * kf[16 * q]);
-                    v_top = fmaxf(v_top, vf[16 * q]);
-                }
-                adjust(top * qf, v_top);
-                const f32x2 m2 = pk2(-m, -m);
-                f32x2 lo = pk2(0.0f, 0.0f);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = kf[32 * q + 16 * e] * qf, w = vf[32 * q + 16 * e] * v_inv;
-                        const f32x2 f2 = pk2(f, f), w2 = pk2(w, w);
-#pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const f32x2 y = fma2(pk2(__uint_as_float(z[q][16 * e + k]), __uint_as_float(z[q][16 * e + k + 1])), f2, m2);
-                            float y0, y1;
-                            up2(y, y0, y1);
-                            const f32x2 pp = pk2(ex2(y0), ex2(y1));
-                            if (k & 2)
-                                lo = add2(lo, pp);
-                            else
-                                l2 = add2(l2, pp);
-                            up2(mul2(pp, w2), y0, y1);
-                            p[8 * e + k / 2] = half2_bits(y0, y1);
-                        }
-                    }
-                    tmem_st16(ts + 16 * q, p);
-                }
-                l2 = add2(l2, lo);
+                tc::fence_before_sync();
+                mbar_arrive(bar(kBarSFree));
+                const int see = lim - key0;
+                const bool all = __all_sync(0xffffffffu, !live || see >= kPrKeys);
+                f32x2 sum;
+                const float top = (all ? row_top<false>(z, kf, see) : row_top<true>(z, kf, see)) * qf;
+                if (i > 0 && !wait(kBarO + x, (i - 1) & 1)) break;  // P and O are free: the last second product is done
+                tc::fence_after_sync();
+                adjust(top, v_top);
+                if (all)
+                    row_weights<false>(z, kf, vf, qf, v_inv, m, see, tp, sum);
+                else
+                    row_weights<true>(z, kf, vf, qf, v_inv, m, see, tp, sum);
+                l2 = add2(l2, sum);
             } else {
                 float top = -INFINITY, v_top = 0.0f;
 #pragma unroll 1
@@ -257,6 +224,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         v_top = fmaxf(v_top, vf[col]);
                     }
                 }
+                if (i > 0 && !wait(kBarO + x, (i - 1) & 1)) break;
+                tc::fence_after_sync();
                 adjust(top * qf, v_top);
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
@@ -275,15 +244,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         l2 = add2(l2, pk2(pp[0], pp[1]));
                         p[k / 2] = half2_bits(w[0], w[1]);
                     }
-                    tmem_st16(ts + 16 * q, p);
+                    tmem_st16(tp + 16 * q, p);
                 }
+                tc::fence_before_sync();
+                mbar_arrive(bar(kBarSFree));
             }
             tmem_wait_st();
             tc::fence_before_sync();
             mbar_arrive(bar(kBarP + x));
         }
         // ---- the rows' results
-        if (n > 0) wait(kBarO + x, 0);
+        if (n > 0) wait(kBarO + x, (n - 1) & 1);
         tc::fence_after_sync();
         float l, l_odd;
         up2(l2, l, l_odd);
@@ -408,6 +379,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         load(0, false);
         load(0, true);
         pages(1);
+        role_sync();
         for (int i = 0; i < nt; ++i) {
             const int st = i & 1;
             const bool whole = (t_first + i + 1) * kPrKeys <= paged;
@@ -434,57 +406,88 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     } else {
       reg_dec<kPrRegMma>();
       if (warp == 12) {
+        if (lane == 0) {
+            mbar_init(bar(kBarQ), 256);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar(kBarKFull + i), 128);
+                mbar_init(bar(kBarKEmpty + i), 2);
+                mbar_init(bar(kBarVFull + i), 128);
+                mbar_init(bar(kBarVEmpty + i), 2);
+                mbar_init(bar(kBarS + i), 1);
+                mbar_init(bar(kBarP + i), 128);
+                mbar_init(bar(kBarO + i), 1);
+            }
+            mbar_init(bar(kBarSFree), 128);
+            mbar_init(bar(kBarNever), 1);
+            mbar_init(bar(kBarNever + 1), 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc(smem_addr(&s_tmem), 512);
+        tc::tmem_relinquish();
+        tc::fence_before_sync();
+      }
+      role_sync();
+      if (warp < 14) {
+        tc::fence_after_sync();
+        const uint32_t tmem = s_tmem;
+        const int x = warp - 12;  // a warp for each row tile: neither's waits hold up the other's products
+        const int n = x ? ntx[1] : ntx[0], n0 = ntx[0], n1 = ntx[1];
         // ================================================= the products
         constexpr uint32_t id_qk = tc::idesc_f16_f32(128, kPrKeys);
         constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // V: transposed operand
         const uint64_t q_desc = tc::sdesc_sw128(base + Cfg::q), k_desc = tc::sdesc_sw128(base + Cfg::k);
         const uint64_t v_desc = sdesc_sw128_mn(base + Cfg::v, 16384);
-        auto qk = [&](int x, int st) {
+        auto qk = [&](int st) {
             const uint64_t qd = q_desc + (x * Cfg::tile >> 4), kd = k_desc + (st * Cfg::tile >> 4);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 constexpr int half = 16384 >> 4;
-                mma_ss(tmem + x * 128, qd + ((k >> 2) * half + (k & 3) * 2), kd + ((k >> 2) * half + (k & 3) * 2), id_qk, k > 0);
+                mma_ss(tmem + kTmS, qd + ((k >> 2) * half + (k & 3) * 2), kd + ((k >> 2) * half + (k & 3) * 2), id_qk, k > 0);
             }
             mma_done(bar(kBarS + x));
         };
-        auto pv = [&](int x, int st, bool acc) {
+        auto pv = [&](int st, bool acc) {
             const uint64_t vd = v_desc + (st * Cfg::tile >> 4);
 #pragma unroll
             for (int k = 0; k < kPrKeys / 16; ++k)
-                mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, vd + k * (2048 >> 4), id_pv, acc || k > 0);
+                mma_ts(tmem + kTmO + x * 128, tmem + kTmP + x * 64 + 8 * k, vd + k * (2048 >> 4), id_pv, acc || k > 0);
+            mma_done(bar(kBarO + x));
         };
+        // S is used in the order (tile 0, x 0), (tile 0, x 1), (tile 1, x 0) ..: the uses before row tile x's
+        // i-th (row tile 0 has no more key tiles than row tile 1, or the latter has none)
+        auto uses_before = [&](int i) { return x ? i + min(i + 1, n0) : i + min(i, n1); };
         if (a.fault) wait(kBarNever, 0);
-        if (nt > 0 && wait(kBarQ, 0) && wait(kBarKFull, 0)) {
-            tc::fence_after_sync();
-            if (ntx[0] > 0) qk(0, 0);
-            if (ntx[1] > 0) qk(1, 0);
-            if (nt > 2) mma_done(bar(kBarKEmpty));
-            for (int i = 0; i < nt && ok; ++i) {
+        if (nt > 0 && wait(kBarQ, 0)) {
+            // S of step i, then the second product of step i - 1
+            for (int i = 0; i <= nt; ++i) {
                 const int st = i & 1;
-                if (!wait(kBarVFull + st, (i >> 1) & 1)) break;
-                if (i + 1 < nt && !wait(kBarKFull + (st ^ 1), ((i + 1) >> 1) & 1)) break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (i >= ntx[x]) continue;
-                    if (!wait(kBarP + x, i & 1)) break;
-                    tc::fence_after_sync();
-                    pv(x, st, i > 0);
-                    if (i + 1 < ntx[x])
-                        qk(x, st ^ 1);
-                    else
-                        mma_done(bar(kBarO + x));
+                if (i < nt) {
+                    if (!wait(kBarKFull + st, (i >> 1) & 1)) break;
+                    if (i < n) {
+                        const int u = uses_before(i);
+                        if (u > 0 && !wait(kBarSFree, (u - 1) & 1)) break;
+                        tc::fence_after_sync();
+                        qk(st);
+                    }
+                    // (only what the producers will wait for: nothing arrives after the CTA's end)
+                    if (i + 2 < nt) mma_done(bar(kBarKEmpty + st));
                 }
-                if (!ok) break;
-                // (only what the producers will wait for: nothing arrives after the CTA's end)
-                if (i + 2 < nt) mma_done(bar(kBarVEmpty + st));
-                if (i + 3 < nt) mma_done(bar(kBarKEmpty + (st ^ 1)));
+                if (i > 0) {
+                    if (!wait(kBarVFull + (st ^ 1), ((i - 1) >> 1) & 1)) break;
+                    if (i - 1 < n) {
+                        if (!wait(kBarP + x, (i - 1) & 1)) break;
+                        tc::fence_after_sync();
+                        pv(st ^ 1, i > 1);
+                    }
+                    if (i + 1 < nt) mma_done(bar(kBarVEmpty + (st ^ 1)));
+                }
             }
         }
         // whatever was issued is over before the tensor memory goes back
         if (!ok) {
-            mma_done(bar(kBarNever));
-            mbar_wait_bounded(bar(kBarNever), 0, 4000000000LL);
+            mma_done(bar(kBarNever + x));
+            mbar_wait_bounded(bar(kBarNever + x), 0, 4000000000LL);
         }
         tc::fence_before_sync();
       }
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     __syncthreads();
     if (warp == 12) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 512);
+        tc::tmem_dealloc(s_tmem, 512);
     }
 }
 

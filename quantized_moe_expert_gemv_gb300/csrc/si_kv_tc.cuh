@@ -178,5 +178,72 @@ __device__ __forceinline__ void key_rows(const Ctx &c, const Seq &s, int b, int 
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// One row's scores of a tile of full pages (a factor for every 16 tokens): z raw, the first `see` of them
+// visible (MASK; else all).
+// The largest score over the row's factor.
+template <bool MASK>
+__device__ __forceinline__ float row_top(const uint32_t (&z)[4][32], const float *kf, int see) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        auto at = [&](int k) {
+            const float x = __uint_as_float(z[q >> 1][16 * (q & 1) + k]);
+            return MASK && 16 * q + k >= see ? -INFINITY : x;
+        };
+        float a = max3(at(0), at(1), at(2)), b = max3(at(3), at(4), at(5));
+        a = max3(a, at(6), at(7));
+        b = max3(b, at(8), at(9));
+        a = max3(a, at(10), at(11));
+        b = max3(b, at(12), at(13));
+        top = fmaxf(top, max3(a, b, fmaxf(at(14), at(15))) * kf[16 * q]);
+    }
+    return top;
+}
+// Their weights 2^(score - m), with their sum, and in tensor memory at ts (two a column) the weights
+// times V's factors and v_inv, as fp16.
+template <bool MASK>
+__device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const float *kf, const float *vf, float qf, float v_inv,
+                                            float m, int see, uint32_t ts, f32x2 &sum) {
+    const f32x2 m2 = pk2(-m, -m);
+    f32x2 s0 = pk2(0.0f, 0.0f), s1 = s0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float f = kf[32 * q + 16 * e] * qf, w = vf[32 * q + 16 * e] * v_inv;
+            const f32x2 f2 = pk2(f, f), w2 = pk2(w, w);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                const f32x2 y = fma2(pk2(__uint_as_float(z[q][16 * e + k]), __uint_as_float(z[q][16 * e + k + 1])), f2, m2);
+                float y0, y1;
+                up2(y, y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                const bool in0 = !MASK || 32 * q + 16 * e + k < see, in1 = !MASK || 32 * q + 16 * e + k + 1 < see;
+                if (!in0) y0 = 0.0f;
+                if (!in1) y1 = 0.0f;
+                const f32x2 pp = pk2(y0, y1);
+                if (k & 2)
+                    s1 = add2(s1, pp);
+                else
+                    s0 = add2(s0, pp);
+                up2(mul2(pp, w2), y0, y1);
+                if (!in0) y0 = 0.0f;  // (whatever V's factor is)
+                if (!in1) y1 = 0.0f;
+                p[8 * e + k / 2] = half2_bits(y0, y1);
+            }
+        }
+        tmem_st16(ts + 16 * q, p);
+    }
+    sum = add2(s0, s1);
+}
+
 }  // namespace kv
 }  // namespace si
