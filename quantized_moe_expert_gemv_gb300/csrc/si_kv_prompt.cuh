@@ -28,6 +28,9 @@ constexpr int kPrRows = 256, kPrKeys = kTileRows;
 constexpr int kPrThreads = 16 * 32;
 // Registers a thread after the roles part (of 128 each at the launch): 2 x 128 x 176 + 128 x 112 + 128 x 40 = 64512 <= 65536.
 constexpr int kPrRegSoftmax = 176, kPrRegTiles = 112, kPrRegMma = 40;
+static_assert(kPrRegSoftmax >= 128 && kPrRegTiles <= 128 && kPrRegMma <= 128 &&
+                  2 * kPrRegSoftmax + kPrRegTiles + kPrRegMma <= 4 * 128,
+              "more than the launch's registers would be waited for without end, and dec only goes down");
 constexpr int kPrFactorSlots = 4;
 
 template <int D>
@@ -40,7 +43,7 @@ struct PromptCfg {
     static constexpr int bars = factors + kPrFactorSlots * 2 * 128 * 4;
     static constexpr int smem = bars + 32 * 8 + 1024;                  // + alignment slack
 };
-enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarNever = 16 };
+enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarNever = 17 };
 // Tensor memory columns: one S (the row tiles take turns: a softmax thread has its whole row in registers
 // before the other tile's product is issued), P of each row tile, O of each.
 constexpr int kTmS = 0, kTmP = 128, kTmO = 256;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 for (int q = 0; q < 8; ++q) v_top = fmaxf(v_top, vf[16 * q]);
                 tc::tmem_wait_ld();
                 tc::fence_before_sync();
-                mbar_arrive(bar(kBarSFree));
+                mbar_arrive(bar(kBarSFree + x));
                 const int see = lim - key0;
                 const bool all = __all_sync(0xffffffffu, !live || see >= kPrKeys);
                 f32x2 sum;
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     tmem_st16(tp + 16 * q, p);
                 }
                 tc::fence_before_sync();
-                mbar_arrive(bar(kBarSFree));
+                mbar_arrive(bar(kBarSFree + x));
             }
             tmem_wait_st();
             tc::fence_before_sync();
@@ -322,6 +325,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         // another: the pages of this thread's four rows and of its column, their codes and scales, the tile.
         // (A page outside the cache: the first one's codes, and factors NaN.)
         int pg[5];
+        uint64_t row_at[4];  // of the rows' codes, from this thread's chunk of the first page
+        const uint32_t page_bytes = (uint32_t)c.Hk * c.P * D;
+        const uint64_t own = (uint64_t)h * c.P * D + ch * 16;
+        const uint8_t *k_own = c.kc + own, *v_own = c.vc + own;
         auto pages = [&](int i) {
             const int key0 = (t_first + i) * kPrKeys;
             if (i >= nt || key0 + kPrKeys > paged) return;
@@ -329,44 +336,48 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
 #pragma unroll
             for (int k = 0; k < 5; ++k) pg[k] = __ldg(row + ((key0 + (k < 4 ? r0 + 32 * k : pt)) >> a.log_page));
         };
-        auto named = [&](int p) { return p >= 0 && p < c.n_pages; };
-        auto load = [&](int i, bool v) {
-            const int key0 = (t_first + i) * kPrKeys;
-            if (i >= nt || key0 + kPrKeys > paged) return;
+        auto named = [&](int p) { return (uint32_t)p < (uint32_t)c.n_pages; };
+        auto load_k = [&](int i) {
+            if (i >= nt || (t_first + i + 1) * kPrKeys > paged) return;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint8_t *at = (v ? c.vc : c.kc) + page_at(c, named(pg[k]) ? pg[k] : 0, h) +
-                                    ((key0 + r0 + 32 * k) & (c.P - 1)) * D + ch * 16;
+            for (int k = 0; k < 4; ++k)  // (a tile starts at a page)
+                row_at[k] = (uint64_t)(named(pg[k]) ? (uint32_t)pg[k] : 0u) * page_bytes + (uint32_t)(((r0 + 32 * k) & (c.P - 1)) * D);
 #pragma unroll
-                for (int q = 0; q < CC; ++q) {
-                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + 64 * q));
-                    if (v)
-                        vx[k * CC + q] = y;
-                    else
-                        kx[k * CC + q] = y;
-                }
-            }
-            if (!v) {
-                const int64_t at = (int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + h;
-                kfx = __ldg(c.ks + at);
-                vfx = __ldg(c.vs + at);
-                if (!named(pg[4])) {
-                    set_status(c.status, SI_ERR_DEVICE);
-                    kfx = vfx = __int_as_float(0x7fc00000);
-                }
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int q = 0; q < CC; ++q) kx[k * CC + q] = __ldg(reinterpret_cast<const uint4 *>(k_own + row_at[k] + 64 * q));
+            const int64_t at = (int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + h;
+            kfx = __ldg(c.ks + at);
+            vfx = __ldg(c.vs + at);
+            if (!named(pg[4])) {
+                set_status(c.status, SI_ERR_DEVICE);
+                kfx = vfx = __int_as_float(0x7fc00000);
             }
         };
+        auto load_v = [&](int i) {
+            if (i >= nt || (t_first + i + 1) * kPrKeys > paged) return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int q = 0; q < CC; ++q) vx[k * CC + q] = __ldg(reinterpret_cast<const uint4 *>(v_own + row_at[k] + 64 * q));
+        };
+        // units 2 ch and 2 ch + 1 of row r0; rows 32 on lie 4096 bytes on, the other half of D 16384
+        const uint32_t a0 = f16_tile_at(r0, 2 * ch), a1 = f16_tile_at(r0, 2 * ch + 1);
         auto store = [&](uint32_t tile, int i, bool v) {
             const int key0 = (t_first + i) * kPrKeys;
             float *kf = factors + (i % kPrFactorSlots) * 256;
             if (key0 + kPrKeys <= paged) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int q = 0; q < CC; ++q) {
-                        const uint4 y = v ? vx[k * CC + q] : kx[k * CC + q];
-                        codes_to_tile<CODE>(y, tile, r0 + 32 * k, 2 * (ch + 4 * q));
-                    }
+                const uint4(&x)[4 * CC] = v ? vx : kx;
+                codes_to_tile<CODE, 0>(x[0], tile + a0, tile + a1);
+                codes_to_tile<CODE, 4096>(x[CC], tile + a0, tile + a1);
+                codes_to_tile<CODE, 8192>(x[2 * CC], tile + a0, tile + a1);
+                codes_to_tile<CODE, 12288>(x[3 * CC], tile + a0, tile + a1);
+                if constexpr (CC == 2) {
+                    codes_to_tile<CODE, 16384>(x[1], tile + a0, tile + a1);
+                    codes_to_tile<CODE, 16384 + 4096>(x[3], tile + a0, tile + a1);
+                    codes_to_tile<CODE, 16384 + 8192>(x[5], tile + a0, tile + a1);
+                    codes_to_tile<CODE, 16384 + 12288>(x[7], tile + a0, tile + a1);
+                }
                 if (!v) {
                     kf[pt] = kfx;
                     kf[128 + pt] = vfx;
@@ -376,8 +387,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             key_rows<CODE, D>(c, s, b, h, v, key0, a.log_page, bf16, tile, kf + (v ? 128 : 0), pt);
         };
         pages(0);
-        load(0, false);
-        load(0, true);
+        load_k(0);
+        load_v(0);
         pages(1);
         role_sync();
         for (int i = 0; i < nt; ++i) {
@@ -393,14 +404,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             }
             tc::fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + st));
-            load(i + 1, false);
+            load_k(i + 1);
             if (whole) {
                 if (i >= 2 && !wait(kBarVEmpty + st, ((i >> 1) - 1) & 1)) break;
                 store(base + Cfg::v + st * Cfg::tile, i, true);
                 tc::fence_proxy_async_smem();
             }
             mbar_arrive(bar(kBarVFull + st));
-            load(i + 1, true);
+            load_v(i + 1);
             pages(i + 2);
         }
     } else {
@@ -416,8 +427,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 mbar_init(bar(kBarS + i), 1);
                 mbar_init(bar(kBarP + i), 128);
                 mbar_init(bar(kBarO + i), 1);
+                mbar_init(bar(kBarSFree + i), 128);
             }
-            mbar_init(bar(kBarSFree), 128);
             mbar_init(bar(kBarNever), 1);
             mbar_init(bar(kBarNever + 1), 1);
             fence_mbar_init();
@@ -454,9 +465,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 mma_ts(tmem + kTmO + x * 128, tmem + kTmP + x * 64 + 8 * k, vd + k * (2048 >> 4), id_pv, acc || k > 0);
             mma_done(bar(kBarO + x));
         };
-        // S is used in the order (tile 0, x 0), (tile 0, x 1), (tile 1, x 0) ..: the uses before row tile x's
-        // i-th (row tile 0 has no more key tiles than row tile 1, or the latter has none)
-        auto uses_before = [&](int i) { return x ? i + min(i + 1, n0) : i + min(i, n1); };
+        // S is used in the order (tile 0, x 0), (tile 0, x 1), (tile 1, x 0) .. (row tile 0 has no more key tiles
+        // than row tile 1, or the latter has none).  Before use, the last user's rows are in registers.  Each
+        // row tile says so on its own barrier, of which one warp sees every phase (a barrier of both would be
+        // taken for free two phases early).
+        auto s_free = [&](int i) {
+            if (x == 0) return i == 0 || wait(kBarSFree + (n1 > 0), (i - 1) & 1);
+            if (i < n0) return wait(kBarSFree, i & 1);
+            return i == 0 || wait(kBarSFree + 1, (i - 1) & 1);
+        };
         if (a.fault) wait(kBarNever, 0);
         if (nt > 0 && wait(kBarQ, 0)) {
             // S of step i, then the second product of step i - 1
@@ -465,8 +482,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 if (i < nt) {
                     if (!wait(kBarKFull + st, (i >> 1) & 1)) break;
                     if (i < n) {
-                        const int u = uses_before(i);
-                        if (u > 0 && !wait(kBarSFree, (u - 1) & 1)) break;
+                        if (!s_free(i)) break;
                         tc::fence_after_sync();
                         qk(st);
                     }

@@ -74,8 +74,9 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t smem_addr, uint32_t 
 __device__ __forceinline__ uint32_t f16_tile_at(int r, int u) {
     return (uint32_t)((u >> 3) * 16384 + r * 128 + (((u ^ r) & 7) << 4));
 }
+template <int OFF = 0>
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+    asm volatile("st.shared.v4.b32 [%0 + %5], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w), "n"(OFF) : "memory");
 }
 
 typedef unsigned long long f32x2;
@@ -133,16 +134,16 @@ struct RowLoad {
     }
 };
 
-// 16 codes (chunk u/2 of a row) into units u and u + 1 of an fp16 tile.
-template <int CODE>
-__device__ __forceinline__ void codes_to_tile(const uint4 &y, uint32_t tile, int row, int u) {
+// 16 codes as two 16-byte units of an fp16 tile, OFF bytes after a0 and a1.
+template <int CODE, int OFF>
+__device__ __forceinline__ void codes_to_tile(const uint4 &y, uint32_t a0, uint32_t a1) {
     uint32_t o[8];
     codes_to_half<CODE>(code_bias<CODE>(y.x), o[0], o[1]);
     codes_to_half<CODE>(code_bias<CODE>(y.y), o[2], o[3]);
     codes_to_half<CODE>(code_bias<CODE>(y.z), o[4], o[5]);
     codes_to_half<CODE>(code_bias<CODE>(y.w), o[6], o[7]);
-    sts128(tile + f16_tile_at(row, u), o[0], o[1], o[2], o[3]);
-    sts128(tile + f16_tile_at(row, u + 1), o[4], o[5], o[6], o[7]);
+    sts128<OFF>(a0, o[0], o[1], o[2], o[3]);
+    sts128<OFF>(a1, o[4], o[5], o[6], o[7]);
 }
 
 // The K (or V) rows of tokens key0 .. key0 + 127 of one kv head into an fp16
@@ -164,7 +165,8 @@ __device__ __forceinline__ void key_rows(const Ctx &c, const Seq &s, int b, int 
 #pragma unroll
             for (int q = 0; q < CC; ++q) y[q] = *reinterpret_cast<const uint4 *>(at + 64 * q);
 #pragma unroll
-            for (int q = 0; q < CC; ++q) codes_to_tile<CODE>(y[q], tile, row, 2 * (ch + 4 * q));
+            for (int q = 0; q < CC; ++q)
+                codes_to_tile<CODE, 0>(y[q], tile + f16_tile_at(row, 2 * (ch + 4 * q)), tile + f16_tile_at(row, 2 * (ch + 4 * q) + 1));
             f = p < 0 ? nan : (v ? c.vs : c.ks)[p * c.Hk + h];
         } else {
             const bool in = t < s.len && s.slot >= 0;
@@ -214,31 +216,31 @@ __device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const fl
     f32x2 s0 = pk2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+        float y[32];  // one step for all 32 values before the next: each step's are independent
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float f = kf[32 * q + (k & 16)] * qf;
+            up2(fma2(pk2(__uint_as_float(z[q][k]), __uint_as_float(z[q][k + 1])), pk2(f, f), m2), y[k], y[k + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            y[k] = ex2(y[k]);
+            if (MASK && 32 * q + k >= see) y[k] = 0.0f;
+        }
         uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float f = kf[32 * q + 16 * e] * qf, w = vf[32 * q + 16 * e] * v_inv;
-            const f32x2 f2 = pk2(f, f), w2 = pk2(w, w);
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-                const f32x2 y = fma2(pk2(__uint_as_float(z[q][16 * e + k]), __uint_as_float(z[q][16 * e + k + 1])), f2, m2);
-                float y0, y1;
-                up2(y, y0, y1);
-                y0 = ex2(y0);
-                y1 = ex2(y1);
-                const bool in0 = !MASK || 32 * q + 16 * e + k < see, in1 = !MASK || 32 * q + 16 * e + k + 1 < see;
-                if (!in0) y0 = 0.0f;
-                if (!in1) y1 = 0.0f;
-                const f32x2 pp = pk2(y0, y1);
-                if (k & 2)
-                    s1 = add2(s1, pp);
-                else
-                    s0 = add2(s0, pp);
-                up2(mul2(pp, w2), y0, y1);
-                if (!in0) y0 = 0.0f;  // (whatever V's factor is)
-                if (!in1) y1 = 0.0f;
-                p[8 * e + k / 2] = half2_bits(y0, y1);
-            }
+        for (int k = 0; k < 32; k += 2) {
+            const f32x2 pp = pk2(y[k], y[k + 1]);
+            if (k & 2)
+                s1 = add2(s1, pp);
+            else
+                s0 = add2(s0, pp);
+            const float w = vf[32 * q + (k & 16)] * v_inv;
+            float w0, w1;
+            up2(mul2(pp, pk2(w, w)), w0, w1);
+            if (MASK && 32 * q + k >= see) w0 = 0.0f;  // (whatever V's factor is)
+            if (MASK && 32 * q + k + 1 >= see) w1 = 0.0f;
+            p[k / 2] = half2_bits(w0, w1);
         }
         tmem_st16(ts + 16 * q, p);
     }
