@@ -12,7 +12,7 @@
 // warps 8-11 turn codes into fp16 tiles in shared memory (K with d innermost, V
 // with d innermost too: the second product takes V as its transposed operand);
 // warps 12 and 13 issue the two row tiles'
-// products (warps 14 and 15 only lend their registers).  While one row tile's products run,
+// products; warp 14 looks up pages and scales ahead (warp 15 only lends its registers).  While one row tile's products run,
 // the other's softmax does.
 // Bound: at D = 128 a pair of row tiles and 128 keys takes 2048 cycles of the
 // tensor cores and 2048 of the exponential unit (256 x 128 at 16 a cycle), so
@@ -31,7 +31,12 @@ constexpr int kPrRegSoftmax = 176, kPrRegTiles = 112, kPrRegMma = 40;
 static_assert(kPrRegSoftmax >= 128 && kPrRegTiles <= 128 && kPrRegMma <= 128 &&
                   2 * kPrRegSoftmax + kPrRegTiles + kPrRegMma <= 4 * 128,
               "more than the launch's registers would be waited for without end, and dec only goes down");
-constexpr int kPrFactorSlots = 4;
+constexpr int kPrFactorSlots = 4, kPrInfoSlots = 8;
+// What a tile of full pages needs for each 16 tokens: the page (0 where the table names none), K's and V's scale (NaN there).
+struct PromptInfo {
+    int32_t page[8];
+    float k[8], v[8];
+};
 
 template <int D>
 struct PromptCfg {
@@ -40,10 +45,11 @@ struct PromptCfg {
     static constexpr int k = 2 * tile;
     static constexpr int v = k + 2 * tile;
     static constexpr int factors = v + 2 * tile;                       // [slots][2][128] floats
-    static constexpr int bars = factors + kPrFactorSlots * 2 * 128 * 4;
+    static constexpr int info = factors + kPrFactorSlots * 2 * 128 * 4;  // [slots][3][8]: see PromptInfo
+    static constexpr int bars = info + kPrInfoSlots * 96;
     static constexpr int smem = bars + 32 * 8 + 1024;                  // + alignment slack
 };
-enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarNever = 17 };
+enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarInfo = 17, kBarNever = 19 };
 // Tensor memory columns: one S (the row tiles take turns: a softmax thread has its whole row in registers
 // before the other tile's product is issued), P of each row tile, O of each.
 constexpr int kTmS = 0, kTmP = 128, kTmO = 256;
@@ -110,6 +116,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
 
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     float *factors = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)) + Cfg::factors);
+    PromptInfo *infos = reinterpret_cast<PromptInfo *>(smem_raw + (base - smem_addr(smem_raw)) + Cfg::info);
     auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
 
     bool ok = true;
@@ -195,23 +202,24 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 uint32_t z[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32(ts + 32 * q, z[q]);
+                const PromptInfo &info = infos[i % kPrInfoSlots];
                 float v_top = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v_top = fmaxf(v_top, vf[16 * q]);
+                for (int q = 0; q < 8; ++q) v_top = fmaxf(v_top, info.v[q]);
                 tc::tmem_wait_ld();
                 tc::fence_before_sync();
                 mbar_arrive(bar(kBarSFree + x));
                 const int see = lim - key0;
                 const bool all = __all_sync(0xffffffffu, !live || see >= kPrKeys);
                 f32x2 sum;
-                const float top = (all ? row_top<false>(z, kf, see) : row_top<true>(z, kf, see)) * qf;
+                const float top = (all ? row_top<false>(z, info.k, see) : row_top<true>(z, info.k, see)) * qf;
                 if (i > 0 && !wait(kBarO + x, (i - 1) & 1)) break;  // P and O are free: the last second product is done
                 tc::fence_after_sync();
                 adjust(top, v_top);
                 if (all)
-                    row_weights<false>(z, kf, vf, qf, v_inv, m, see, tp, sum);
+                    row_weights<false>(z, info.k, info.v, qf, v_inv, m, see, tp, sum);
                 else
-                    row_weights<true>(z, kf, vf, qf, v_inv, m, see, tp, sum);
+                    row_weights<true>(z, info.k, info.v, qf, v_inv, m, see, tp, sum);
                 l2 = add2(l2, sum);
             } else {
                 float top = -INFINITY, v_top = 0.0f;
@@ -320,46 +328,28 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         const int ch = pt & 3, r0 = pt >> 2;   // chunks ch, ch + 4 of rows r0 + 32 k
         constexpr int CC = D / 64;             // chunks of 16 codes of one row that a thread takes
         uint4 kx[4 * CC], vx[4 * CC];
-        float kfx = 0.0f, vfx = 0.0f;          // factors of column pt
-        // A tile of full pages takes three steps, each a tile ahead of the next so that no load waits for
-        // another: the pages of this thread's four rows and of its column, their codes and scales, the tile.
-        // (A page outside the cache: the first one's codes, and factors NaN.)
-        int pg[5];
-        uint64_t row_at[4];  // of the rows' codes, from this thread's chunk of the first page
+        // The codes of a tile of full pages are loaded a tile ahead.
         const uint32_t page_bytes = (uint32_t)c.Hk * c.P * D;
         const uint64_t own = (uint64_t)h * c.P * D + ch * 16;
         const uint8_t *k_own = c.kc + own, *v_own = c.vc + own;
-        auto pages = [&](int i) {
-            const int key0 = (t_first + i) * kPrKeys;
-            if (i >= nt || key0 + kPrKeys > paged) return;
-            const int32_t *row = c.table + (int64_t)b * c.table_stride;
-#pragma unroll
-            for (int k = 0; k < 5; ++k) pg[k] = __ldg(row + ((key0 + (k < 4 ? r0 + 32 * k : pt)) >> a.log_page));
+        auto row_at = [&](uint32_t page, int k) -> uint64_t {  // of row r0 + 32 k's codes (a tile starts at a page)
+            return (uint64_t)page * page_bytes + (uint32_t)(((r0 + 32 * k) & (c.P - 1)) * D);
         };
-        auto named = [&](int p) { return (uint32_t)p < (uint32_t)c.n_pages; };
-        auto load_k = [&](int i) {
+        auto load = [&](int i, bool v) {
             if (i >= nt || (t_first + i + 1) * kPrKeys > paged) return;
+            const PromptInfo &info = infos[i % kPrInfoSlots];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)  // (a tile starts at a page)
-                row_at[k] = (uint64_t)(named(pg[k]) ? (uint32_t)pg[k] : 0u) * page_bytes + (uint32_t)(((r0 + 32 * k) & (c.P - 1)) * D);
+            for (int k = 0; k < 4; ++k) {
+                const uint8_t *at = (v ? v_own : k_own) + row_at((uint32_t)info.page[(r0 >> 4) + 2 * k], k);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int q = 0; q < CC; ++q) kx[k * CC + q] = __ldg(reinterpret_cast<const uint4 *>(k_own + row_at[k] + 64 * q));
-            const int64_t at = (int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + h;
-            kfx = __ldg(c.ks + at);
-            vfx = __ldg(c.vs + at);
-            if (!named(pg[4])) {
-                set_status(c.status, SI_ERR_DEVICE);
-                kfx = vfx = __int_as_float(0x7fc00000);
+                for (int q = 0; q < CC; ++q) {
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + 64 * q));
+                    if (v)
+                        vx[k * CC + q] = y;
+                    else
+                        kx[k * CC + q] = y;
+                }
             }
-        };
-        auto load_v = [&](int i) {
-            if (i >= nt || (t_first + i + 1) * kPrKeys > paged) return;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int q = 0; q < CC; ++q) vx[k * CC + q] = __ldg(reinterpret_cast<const uint4 *>(v_own + row_at[k] + 64 * q));
         };
         // units 2 ch and 2 ch + 1 of row r0; rows 32 on lie 4096 bytes on, the other half of D 16384
         const uint32_t a0 = f16_tile_at(r0, 2 * ch), a1 = f16_tile_at(r0, 2 * ch + 1);
@@ -378,19 +368,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     codes_to_tile<CODE, 16384 + 8192>(x[5], tile + a0, tile + a1);
                     codes_to_tile<CODE, 16384 + 12288>(x[7], tile + a0, tile + a1);
                 }
-                if (!v) {
-                    kf[pt] = kfx;
-                    kf[128 + pt] = vfx;
-                }
                 return;
             }
             key_rows<CODE, D>(c, s, b, h, v, key0, a.log_page, bf16, tile, kf + (v ? 128 : 0), pt);
         };
-        pages(0);
-        load_k(0);
-        load_v(0);
-        pages(1);
         role_sync();
+        if (nt > 0) wait(kBarInfo, 0);
+        load(0, false);
+        load(0, true);
         for (int i = 0; i < nt; ++i) {
             const int st = i & 1;
             const bool whole = (t_first + i + 1) * kPrKeys <= paged;
@@ -404,15 +389,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             }
             tc::fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + st));
-            load_k(i + 1);
+            if (i + 1 < nt && !wait(kBarInfo + (st ^ 1), ((i + 1) >> 1) & 1)) break;
+            load(i + 1, false);
             if (whole) {
                 if (i >= 2 && !wait(kBarVEmpty + st, ((i >> 1) - 1) & 1)) break;
                 store(base + Cfg::v + st * Cfg::tile, i, true);
                 tc::fence_proxy_async_smem();
             }
             mbar_arrive(bar(kBarVFull + st));
-            load_v(i + 1);
-            pages(i + 2);
+            load(i + 1, true);
         }
     } else {
       reg_dec<kPrRegMma>();
@@ -428,6 +413,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 mbar_init(bar(kBarP + i), 128);
                 mbar_init(bar(kBarO + i), 1);
                 mbar_init(bar(kBarSFree + i), 128);
+                mbar_init(bar(kBarInfo + i), 1);
             }
             mbar_init(bar(kBarNever), 1);
             mbar_init(bar(kBarNever + 1), 1);
@@ -506,6 +492,32 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             mbar_wait_bounded(bar(kBarNever + x), 0, 4000000000LL);
         }
         tc::fence_before_sync();
+      } else if (warp == 14) {
+        // ================================================= pages and scales, two tiles ahead of K's
+        // (tile j's once K's tile j - 2 is made: by then no one reads the slot or the phase that it takes)
+        auto look = [&](int j, int &page, float &ks, float &vs) {
+            const int key0 = (t_first + j) * kPrKeys;
+            if (lane >= 8 || j >= nt || key0 + kPrKeys > paged) return;
+            const int64_t p = load_page(c, b, (key0 + 16 * lane) >> a.log_page);
+            page = p < 0 ? 0 : (int)p;
+            ks = p < 0 ? __int_as_float(0x7fc00000) : __ldg(c.ks + p * c.Hk + h);
+            vs = p < 0 ? __int_as_float(0x7fc00000) : __ldg(c.vs + p * c.Hk + h);
+        };
+        int page = 0;
+        float ks = 0.0f, vs = 0.0f;
+        look(0, page, ks, vs);
+        for (int j = 0; j < nt; ++j) {
+            if (j >= 2 && !wait(kBarKFull + (j & 1), ((j - 2) >> 1) & 1)) break;
+            if (lane < 8) {
+                PromptInfo &info = infos[j % kPrInfoSlots];
+                info.page[lane] = page;
+                info.k[lane] = ks;
+                info.v[lane] = vs;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarInfo + (j & 1)));
+            look(j + 1, page, ks, vs);
+        }
       }
     }
     __syncwarp();

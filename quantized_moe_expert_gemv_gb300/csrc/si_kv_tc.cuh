@@ -186,7 +186,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// One row's scores of a tile of full pages (a factor for every 16 tokens): z raw, the first `see` of them
+// One row's scores of a tile of full pages (kf, vf: a factor for every 16 tokens): z raw, the first `see` of them
 // visible (MASK; else all).
 // The largest score over the row's factor.
 template <bool MASK>
@@ -203,7 +203,7 @@ __device__ __forceinline__ float row_top(const uint32_t (&z)[4][32], const float
         b = max3(b, at(8), at(9));
         a = max3(a, at(10), at(11));
         b = max3(b, at(12), at(13));
-        top = fmaxf(top, max3(a, b, fmaxf(at(14), at(15))) * kf[16 * q]);
+        top = fmaxf(top, max3(a, b, fmaxf(at(14), at(15))) * kf[q]);
     }
     return top;
 }
@@ -219,7 +219,7 @@ __device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const fl
         float y[32];  // one step for all 32 values before the next: each step's are independent
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-            const float f = kf[32 * q + (k & 16)] * qf;
+            const float f = kf[2 * q + k / 16] * qf;
             up2(fma2(pk2(__uint_as_float(z[q][k]), __uint_as_float(z[q][k + 1])), pk2(f, f), m2), y[k], y[k + 1]);
         }
 #pragma unroll
@@ -235,7 +235,7 @@ __device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const fl
                 s1 = add2(s1, pp);
             else
                 s0 = add2(s0, pp);
-            const float w = vf[32 * q + (k & 16)] * v_inv;
+            const float w = vf[2 * q + k / 16] * v_inv;
             float w0, w1;
             up2(mul2(pp, pk2(w, w)), w0, w1);
             if (MASK && 32 * q + k >= see) w0 = 0.0f;  // (whatever V's factor is)
