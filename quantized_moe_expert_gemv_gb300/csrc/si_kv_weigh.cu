@@ -9,11 +9,15 @@
 // so that a step of 8 query heads wastes none of it; units of 64 tokens are
 // dealt out evenly over the GPU as in the few-row attention, and nothing has to
 // be joined.
-// Many rows (k_kv_weigh_many, more than 64, head_dim 64 and 128): bound by the
-// exponential (16 a cycle and SM).  One CTA for 128 tokens: S^T = K Q^T on the
-// tcgen05 tensor cores, K's tile staying and q's tiles following each other
-// through two stages; a thread holds one token's sum and walks its row of
-// tensor memory.  Two CTAs fit an SM, so one's loads run under the other's sums.
+// A window of rows (k_kv_weigh_window, 65 to 512, head_dim 64 and 128): bound by
+// the exponential (32 a cycle and SM) and the products.  S^T = K Q^T on the tcgen05
+// tensor cores, 128 tokens by 256 rows; all of q's rows stay in shared memory while
+// the CTA's share of a kv head's tokens goes by, and a thread holds one token's sum
+// and walks half of the block's columns in tensor memory.
+// Many rows (k_kv_weigh_many): one CTA for 128 tokens, whose K tile stays while
+// q's tiles of 128 rows follow each other through two stages; for 512 rows it
+// took 117 us where the window kernel takes less than half (most of it in a
+// CTA's start).
 #include "si_kv_decode.cuh"
 #include "si_kv_tc.cuh"
 
@@ -31,6 +35,9 @@ struct WeighArgs {
     long long budget;
 };
 
+// The barrier of the window kernel's softmax warps.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+constexpr int kWindowOver = 3;
 constexpr int kWeighRows = 64;  // rows whose operand lies in shared memory at a time
 
 template <int D>
@@ -257,6 +264,321 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
     }
 }
 
+// ------------------------------------------------------------------ a window of rows
+constexpr int kWwRows = 512, kWwThreads = 13 * 32;
+template <int D>
+struct WeighWindowCfg {
+    static constexpr int block = 256 * D * 2;                  // 256 rows of q: [D / 64][256 rows][128 bytes]
+    static constexpr int tile = kTileRows * D * 2;
+    static constexpr int k = 2 * block;
+    static constexpr int lse = k + 2 * tile;                   // [512] -lse log2 e
+    static constexpr int keyf = lse + kWwRows * 4;             // [4][128]
+    static constexpr int part = keyf + 4 * 128 * 4;            // [2][128]
+    static constexpr int bars = part + 2 * 128 * 4;
+    static constexpr int smem = bars + 16 * 8 + 1024;
+};
+enum WindowBar { kXbQ = 0, kXbKFull = 1, kXbKEmpty = 3, kXbSFull = 5, kXbSEmpty = 7, kXbNever = 9 };
+
+// Tiles of 128 tokens of a sequence (the unfinished page is in the last).
+__device__ __forceinline__ int window_tiles(int len) { return (len + kTileRows - 1) / kTileRows; }
+
+template <int CODE, int D>
+__global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighArgs a) {
+    using Cfg = WeighWindowCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_top;  // the rows' largest magnitude (bits)
+    const Ctx &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform)
+    const bool bf16 = a.bf16;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t *at = smem_raw + (base - smem_addr(smem_raw));
+    float *lse_s = reinterpret_cast<float *>(at + Cfg::lse), *keyf = reinterpret_cast<float *>(at + Cfg::keyf);
+    float *part = reinterpret_cast<float *>(at + Cfg::part);
+    auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
+
+    const Share share = take_share<kWwThreads / 32>(c.B, [&](int b) -> long long {
+        const int tiles = window_tiles(load_seq(c, b).len);
+        return tiles == 0 ? 0ll : (long long)(tiles + kWindowOver) * c.Hk;
+    });
+    if (blockIdx.x >= share.ctas) return;
+    if (tid == 0) {
+        mbar_init(bar(kXbQ), 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kXbKFull + i), 128);
+            mbar_init(bar(kXbKEmpty + i), 1);
+            mbar_init(bar(kXbSFull + i), 1);
+            mbar_init(bar(kXbSEmpty + i), 256);
+        }
+        mbar_init(bar(kXbNever), 1);
+        fence_mbar_init();
+        s_top = 0;
+    }
+    if (warp == 12) {
+        tc::tmem_alloc(smem_addr(&s_tmem), 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    auto wait = [&](int i, int parity) {
+        if (ok && !mbar_wait_warp(bar(i), (uint32_t)parity, a.budget)) {
+            ok = false;
+            if (lane == 0) set_status(c.status, SI_ERR_TIMEOUT);
+        }
+        return ok;
+    };
+
+    // Every role walks the same segments (a run of one kv head's tiles), tiles (numbered over all of them) and
+    // blocks of 256 rows; a tile's blocks are those with a row that sees its first key.
+    int seq = share.b;
+    long long off = share.off, u = share.begin;
+    int tile_no = 0, seg_no = 0;
+    struct Place {
+        Seq s;
+        int b, h, first, end, rows, old;
+    };
+    auto next = [&](Place &p) {  // the next segment; false at the end
+        while (u < share.end) {
+            p.s = load_seq(c, seq);
+            const int tiles = window_tiles(p.s.len);
+            const long long n = tiles == 0 ? 0ll : (long long)(tiles + kWindowOver) * c.Hk;
+            if (off >= n) {
+                off -= n;
+                ++seq;
+                continue;
+            }
+            const Segment seg = take_segment(tiles, kWindowOver, off, u, share.end);
+            u += seg.step;
+            off += seg.step;
+            if (seg.first == seg.end) continue;
+            p.b = seq;
+            p.h = seg.item;
+            p.first = seg.first;
+            p.end = seg.end;
+            p.rows = p.s.n * c.G;
+            p.old = p.s.len - p.s.n;
+            return true;
+        }
+        return false;
+    };
+    auto first_block = [&](const Place &p, int t) { return max(0, t * kTileRows - p.old) * c.G / 256; };
+    int s_use[2] = {0, 0};  // uses of each block's S so far
+    Place p;
+
+    if (warp < 8) {
+        // ================================================= q, then a thread a key and half of a block's rows
+        const int x = warp >> 2, ch = tid & 3;
+        const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * x;
+        while (next(p)) {
+            // the rows' values times one power of two (a score is off by less than 2^-32 of the block's largest),
+            // a row that is not finite as zeros with the lse NaN
+            const int passes = (p.rows + 255) / 256 * 4;  // of 64 rows, to the end of the last block
+            auto row_ptr = [&](int r) -> const uint16_t * {
+                return a.q.p + (p.s.row0 + r / c.G) * a.q.row + (p.h * c.G + r % c.G) * a.q.head;
+            };
+            uint32_t top = 0;
+            for (int k = 0; k < passes; ++k) {
+                const int r = 64 * k + (tid >> 2);
+                RowLoad<D> v;
+                v.load(r < p.rows ? row_ptr(r) : a.q.p, r < p.rows, ch);
+                float m = 0.0f;
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) m = fmaxf(m, fmaxf(amax8(v.y[q][0], bf16), amax8(v.y[q][1], bf16)));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                if (m <= 3.4e38f) top = max(top, __float_as_uint(m));
+            }
+            for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) atomicMax(&s_top, top);  // (a maximum: the order does not matter)
+            softmax_sync();
+            float mul, f;
+            row_scale(__uint_as_float(s_top), mul, f);
+            for (int k = 0; k < passes; ++k) {
+                const int r = 64 * k + (tid >> 2);
+                RowLoad<D> v;
+                v.load(r < p.rows ? row_ptr(r) : a.q.p, r < p.rows, ch);
+                float m = 0.0f;
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) m = fmaxf(m, fmaxf(amax8(v.y[q][0], bf16), amax8(v.y[q][1], bf16)));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const bool fine = m <= 3.4e38f;
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int unit = 2 * (ch + 4 * q) + e;
+                        sts128(base + (r >> 8) * Cfg::block + (unit >> 3) * 32768 + (r & 255) * 128 + (((unit ^ r) & 7) << 4),
+                               scale2(v.y[q][e].x, fine ? mul : 0.0f, bf16), scale2(v.y[q][e].y, fine ? mul : 0.0f, bf16),
+                               scale2(v.y[q][e].z, fine ? mul : 0.0f, bf16), scale2(v.y[q][e].w, fine ? mul : 0.0f, bf16));
+                    }
+                if (ch == 0)  // (a row that pads weighs nothing)
+                    lse_s[r] = r >= p.rows ? -INFINITY
+                               : fine      ? -a.lse[(int64_t)(p.s.row0 + r / c.G) * c.H + p.h * c.G + r % c.G] * kLog2e
+                                           : __int_as_float(0x7fc00000);
+            }
+            tc::fence_proxy_async_smem();
+            softmax_sync();
+            if (tid == 0) s_top = 0;  // (read by everyone; its next use is a barrier away)
+            mbar_arrive(bar(kXbQ));
+            const int blocks = (p.rows + 255) / 256;
+            const float scale = f * a.scale2;
+            // (a warp whose wait ran out goes on through the tiles, without waits, for the barriers' sake)
+            for (int t = p.first; t < p.end; ++t, ++tile_no) {
+                const int token = t * kTileRows + (tid & 127), r_min = max(0, token - p.old) * c.G;
+                const int64_t acc_at = ((int64_t)p.b * c.Hk + p.h) * a.acc_stride + token;
+                const float was = x == 0 && a.acc_in && token < p.old ? a.decay * a.acc_in[acc_at] : 0.0f;
+                f32x2 sum = pk2(0.0f, 0.0f), sum1 = sum;
+                float kf = 0.0f;
+                for (int q = first_block(p, t); q < blocks; ++q) {
+                    const int n = q & 1 ? s_use[1]++ : s_use[0]++;
+                    if (!wait(kXbSFull + (q & 1), n & 1)) break;
+                    tc::fence_after_sync();
+                    kf = keyf[(tile_no & 3) * 128 + (tid & 127)] * scale;
+                    const f32x2 kf2 = pk2(kf, kf);
+                    const int r0 = q * 256 + 128 * x;
+                    const float4 *rl = reinterpret_cast<const float4 *>(lse_s + r0);
+                    const bool all = __all_sync(0xffffffffu, r0 >= r_min);
+                    uint32_t z[2][32];
+                    tc::tmem_ld32(ts + (q & 1) * 256, z[0]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        tc::tmem_wait_ld();
+                        if (e < 3)
+                            tc::tmem_ld32(ts + (q & 1) * 256 + 32 * e + 32, z[(e + 1) & 1]);
+                        const uint32_t(&y)[32] = z[e & 1];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 l = rl[8 * e + k / 4];
+                            float w[4];
+                            up2(fma2(pk2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), kf2, pk2(l.x, l.y)), w[0], w[1]);
+                            up2(fma2(pk2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), kf2, pk2(l.z, l.w)), w[2], w[3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                w[i] = ex2(w[i]);
+                                if (!all && r0 + 32 * e + k + i < r_min) w[i] = 0.0f;
+                            }
+                            sum = add2(sum, pk2(w[0], w[1]));
+                            sum1 = add2(sum1, pk2(w[2], w[3]));
+                        }
+                    }
+                    tc::fence_before_sync();
+                    mbar_arrive(bar(kXbSEmpty + (q & 1)));
+                }
+                float s0, s1;
+                up2(add2(sum, sum1), s0, s1);
+                if (x) part[(tile_no & 1) * 128 + (tid & 127)] = s0 + s1;
+                softmax_sync();
+                if (x == 0 && ok && token < p.s.len) a.acc_out[acc_at] = was + ((s0 + s1) + part[(tile_no & 1) * 128 + tid]);
+            }
+        }
+    } else if (warp < 12) {
+        // ================================================= K's tiles
+        const int pt = tid - 256, ch = pt & 3, r0 = pt >> 2;
+        constexpr int CC = D / 64;
+        const uint32_t a0 = f16_tile_at(r0, 2 * ch), a1 = f16_tile_at(r0, 2 * ch + 1);
+        while (next(p)) {
+            const int paged = p.s.len & ~(c.P - 1);
+            const int32_t *table = c.table + (int64_t)p.b * c.table_stride;
+            int pg[5];
+            uint4 kx[4 * CC];
+            float kfx = 0.0f;
+            auto whole = [&](int t) { return (t + 1) * kTileRows <= paged; };
+            auto named = [&](int v) { return (uint32_t)v < (uint32_t)c.n_pages; };
+            auto pages = [&](int t) {
+                if (t >= p.end || !whole(t)) return;
+#pragma unroll
+                for (int k = 0; k < 5; ++k) pg[k] = __ldg(table + ((t * kTileRows + (k < 4 ? r0 + 32 * k : pt)) >> a.log_page));
+            };
+            auto load = [&](int t) {
+                if (t >= p.end || !whole(t)) return;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint8_t *from = c.kc + page_at(c, named(pg[k]) ? pg[k] : 0, p.h) + ((r0 + 32 * k) & (c.P - 1)) * D + ch * 16;
+#pragma unroll
+                    for (int q = 0; q < CC; ++q) kx[k * CC + q] = __ldg(reinterpret_cast<const uint4 *>(from + 64 * q));
+                }
+                kfx = __ldg(c.ks + (int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + p.h);
+                if (!named(pg[4])) {
+                    set_status(c.status, SI_ERR_DEVICE);
+                    kfx = __int_as_float(0x7fc00000);
+                }
+            };
+            pages(p.first);
+            load(p.first);
+            pages(p.first + 1);
+            for (int t = p.first; t < p.end; ++t, ++tile_no) {
+                const int st = tile_no & 1;
+                if (tile_no >= 2 && !wait(kXbKEmpty + st, ((tile_no >> 1) - 1) & 1)) break;
+                const uint32_t tile = base + Cfg::k + st * Cfg::tile;
+                float *kf = keyf + (tile_no & 3) * 128;
+                if (whole(t)) {
+                    codes_to_tile<CODE, 0>(kx[0], tile + a0, tile + a1);
+                    codes_to_tile<CODE, 4096>(kx[CC], tile + a0, tile + a1);
+                    codes_to_tile<CODE, 8192>(kx[2 * CC], tile + a0, tile + a1);
+                    codes_to_tile<CODE, 12288>(kx[3 * CC], tile + a0, tile + a1);
+                    if constexpr (CC == 2) {
+                        codes_to_tile<CODE, 16384>(kx[1], tile + a0, tile + a1);
+                        codes_to_tile<CODE, 16384 + 4096>(kx[3], tile + a0, tile + a1);
+                        codes_to_tile<CODE, 16384 + 8192>(kx[5], tile + a0, tile + a1);
+                        codes_to_tile<CODE, 16384 + 12288>(kx[7], tile + a0, tile + a1);
+                    }
+                    kf[pt] = kfx;
+                } else {
+                    key_rows<CODE, D>(c, p.s, p.b, p.h, false, t * kTileRows, a.log_page, bf16, tile, kf, pt);
+                }
+                tc::fence_proxy_async_smem();
+                mbar_arrive(bar(kXbKFull + st));
+                load(t + 1);
+                pages(t + 2);
+            }
+            if (!ok) break;
+        }
+    } else {
+        // ================================================= the products: 128 keys by 256 rows
+        constexpr uint32_t id = tc::idesc_f16_f32(128, 256);
+        const uint64_t k_desc = tc::sdesc_sw128(base + Cfg::k), q_desc = tc::sdesc_sw128(base);
+        if (a.fault) wait(kXbNever, 0);
+        while (ok && next(p)) {
+            if (!wait(kXbQ, seg_no & 1)) break;
+            const int blocks = (p.rows + 255) / 256;
+            for (int t = p.first; t < p.end; ++t, ++tile_no) {
+                const int st = tile_no & 1;
+                if (!wait(kXbKFull + st, (tile_no >> 1) & 1)) break;
+                tc::fence_after_sync();
+                const uint64_t kd = k_desc + (st * Cfg::tile >> 4);
+                for (int q = first_block(p, t); q < blocks; ++q) {
+                    const int n = q & 1 ? s_use[1]++ : s_use[0]++;
+                    if (n > 0 && !wait(kXbSEmpty + (q & 1), (n - 1) & 1)) break;
+                    tc::fence_after_sync();
+                    const uint64_t qd = q_desc + (q * Cfg::block >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + (q & 1) * 256, kd + ((k >> 2) * (16384 >> 4) + (k & 3) * 2),
+                               qd + ((k >> 2) * (32768 >> 4) + (k & 3) * 2), id, k > 0);
+                    mma_done(bar(kXbSFull + (q & 1)));
+                }
+                if (!ok) break;
+                mma_done(bar(kXbKEmpty + st));
+            }
+            ++seg_no;
+        }
+        // whatever was issued is over before the tensor memory goes back (and the last commits, which no one waits for)
+        mma_done(bar(kXbNever));
+        mbar_wait_bounded(bar(kXbNever), 0, 4000000000LL);
+        tc::fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 12) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
 // ------------------------------------------------------------------ many rows
 constexpr int kWmThreads = 9 * 32;
 template <int D>
@@ -451,12 +773,20 @@ static cudaError_t many(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     k_kv_weigh_many<CODE, D><<<grid, kWmThreads, Cfg::smem, s>>>(a);
     return cudaGetLastError();
 }
+template <int CODE, int D>
+static cudaError_t window(const Plan &p, const WeighArgs &a, cudaStream_t s) {
+    using Cfg = WeighWindowCfg<D>;
+    cudaError_t e = allow_smem<k_kv_weigh_window<CODE, D>>(p, Cfg::smem);
+    if (e != cudaSuccess) return e;
+    k_kv_weigh_window<CODE, D><<<p.sm_count, kWwThreads, Cfg::smem, s>>>(a);
+    return cudaGetLastError();
+}
 template <int CODE>
 static cudaError_t weigh(const Plan &p, const WeighArgs &a, cudaStream_t s) {
-    const bool rows = (int64_t)a.c.max_new * a.c.G > kWeighRows;
+    const int64_t rows = (int64_t)a.c.max_new * a.c.G;
     switch (p.desc.head_dim) {
-        case 64: return rows ? many<CODE, 64>(p, a, s) : few<CODE, 64>(p, a, s);
-        case 128: return rows ? many<CODE, 128>(p, a, s) : few<CODE, 128>(p, a, s);
+        case 64: return rows > kWwRows ? many<CODE, 64>(p, a, s) : rows > kWeighRows ? window<CODE, 64>(p, a, s) : few<CODE, 64>(p, a, s);
+        case 128: return rows > kWwRows ? many<CODE, 128>(p, a, s) : rows > kWeighRows ? window<CODE, 128>(p, a, s) : few<CODE, 128>(p, a, s);
         default: return few<CODE, 256>(p, a, s);
     }
 }

@@ -252,6 +252,10 @@ def test_attend_reports_a_wait_that_runs_out(monkeypatch, dim):
     acc = torch.zeros((1, 2, 500), device=DEV)
     si.si_kv_weigh(d.plan, d.cache, d.batch, qd, torch.zeros((200, 8), device=DEV), None, acc, 1.0, 0.1, d.scratch)
     assert d.status() == si.SI_ERR_TIMEOUT
+    start = torch.tensor([0, 20], dtype=torch.int32, device=DEV)
+    few = si.kv_batch(1, 20, 20, 500, start, d.lens, d.table, d.slots)
+    si.si_kv_weigh(d.plan, d.cache, few, qd, torch.zeros((200, 8), device=DEV), None, acc, 1.0, 0.1, d.scratch)
+    assert d.status() == si.SI_ERR_TIMEOUT
     monkeypatch.delenv("SI_FAULT_WAIT_BUDGET")
     d = Dev(c)
     out, lse = d.attend(qd, 0.1)
@@ -410,7 +414,7 @@ def test_read(shape):
 
 # ------------------------------------------------------------------ weigh
 WEIGH = [([1], [1]), ([0, 5, 0], [0, 1, 2]), ([15, 16, 17, 130], [1, 1, 1, 2]), ([3, 300], [3, 64]), ([2], [5]),
-         ([900, 257], [5, 257]), ([3001], [1])]
+         ([900, 257], [5, 257]), ([3001], [1]), ([500, 2000, 64, 129], [60, 9, 17, 61])]
 
 
 @pytest.mark.parametrize("lens,news", WEIGH, ids=[str(i) for i in range(len(WEIGH))])
