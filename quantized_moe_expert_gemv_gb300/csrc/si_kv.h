@@ -57,6 +57,24 @@ cudaError_t allow_smem(const Plan &p, int smem) {
     return e;
 }
 
+// Launch with programmatic dependent launch: the kernel may start while the one
+// before it in the stream ends, and every kernel here waits for that one's end
+// (start_after) before it touches global memory.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int max_len);
 
 cudaError_t launch_append(const Plan &p, const Ctx &c, Rows k, Rows v, int32_t *lens_out, cudaStream_t s);

@@ -19,11 +19,13 @@ namespace kv {
 
 constexpr int kAppendThreads = 256;
 
-// UN: units of 16 values that a thread holds of one page's P*D values.
-template <int CODE, int DT, int UN>
+// UN: units of 16 values that a thread holds of one page's P*D values; PG: pages of a CTA (their loads are
+// under way together: with one page of 8 KB a CTA, the chain of loads, maximum and stores reached 4 TB/s).
+template <int CODE, int DT, int UN, int PG>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(Ctx c, Rows k, Rows v, int32_t *lens_out) {
-    __shared__ float s_max[kAppendThreads / 32];
-    const int j = blockIdx.x, h = blockIdx.y >> 1, b = blockIdx.z;
+    __shared__ float s_max[PG][kAppendThreads / 32];
+    start_after();
+    const int j = blockIdx.x * PG, h = blockIdx.y >> 1, b = blockIdx.z;
     const bool is_v = blockIdx.y & 1;
     const int tid = threadIdx.x;
     Seq s = load_seq(c, b);
@@ -36,58 +38,67 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(Ctx c, Rows k, Row
     if (s.n == 0) return;
     const int P = c.P, D = c.D;
     const int first = s.len / P, last = (s.len + s.n) / P;
-    const int page = first + j;
-    if (page >= last && j > 0) return;
+    const int count = min(PG, last - first - j);  // pages to quantise here
+    if (count <= 0 && j > 0) return;
     const Rows in = is_v ? v : k;
     uint16_t *ring = is_v ? c.vt : c.kt;
     const int upr = D / 16;  // units in a row
 
-    if (page < last) {
-        uint4 x[UN][2];
-        float amax = 0.0f;
-        bool bad = false;  // an infinity or NaN
+    if (count > 0) {
+        uint4 x[PG][UN][2];
+        int64_t dst[PG];
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int unit = u * kAppendThreads + tid;
-            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-            if (unit < P * upr) {
-                const int t = page * P + unit / upr, d = unit % upr * 16;
-                const uint16_t *src = t < s.len ? ring + ring_at(c, s.slot, h, t) + d
-                                                : in.p + (int64_t)(s.row0 + t - s.len) * in.row + h * in.head + d;
-                x[u][0] = *reinterpret_cast<const uint4 *>(src);
-                x[u][1] = *reinterpret_cast<const uint4 *>(src + 8);
+        for (int g = 0; g < PG; ++g) dst[g] = g < count ? load_page(c, b, first + j + g) : -1;
+#pragma unroll
+        for (int g = 0; g < PG; ++g)
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const int unit = u * kAppendThreads + tid;
+                x[g][u][0] = x[g][u][1] = make_uint4(0, 0, 0, 0);
+                if (g < count && unit < P * upr) {
+                    const int t = (first + j + g) * P + unit / upr, d = unit % upr * 16;
+                    const uint16_t *src = t < s.len ? ring + ring_at(c, s.slot, h, t) + d
+                                                    : in.p + (int64_t)(s.row0 + t - s.len) * in.row + h * in.head + d;
+                    x[g][u][0] = *reinterpret_cast<const uint4 *>(src);
+                    x[g][u][1] = *reinterpret_cast<const uint4 *>(src + 8);
+                }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const uint32_t *w = &x[u][0].x;
+        for (int g = 0; g < PG; ++g) {
+            float amax = 0.0f;
+            bool bad = false;  // an infinity or NaN
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float lo = fabsf(to_float<DT>((uint16_t)w[i])), hi = fabsf(to_float<DT>((uint16_t)(w[i] >> 16)));
-                bad |= !(lo <= 3.4e38f) || !(hi <= 3.4e38f);
-                amax = fmaxf(amax, fmaxf(lo, hi));
+            for (int u = 0; u < UN; ++u) {
+                const uint32_t *w = &x[g][u][0].x;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float lo = fabsf(to_float<DT>((uint16_t)w[i])), hi = fabsf(to_float<DT>((uint16_t)(w[i] >> 16)));
+                    bad |= !(lo <= 3.4e38f) || !(hi <= 3.4e38f);
+                    amax = fmaxf(amax, fmaxf(lo, hi));
+                }
             }
+            if (bad) amax = __int_as_float(0x7f800000);  // carried through the maximum as an infinity
+            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if ((tid & 31) == 0) s_max[g][tid >> 5] = amax;
         }
-        if (bad) amax = __int_as_float(0x7f800000);  // carried through the maximum as an infinity
-        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if ((tid & 31) == 0) s_max[tid >> 5] = amax;
         __syncthreads();
-        amax = s_max[0];
 #pragma unroll
-        for (int i = 1; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
-        const float Q = CODE == SI_KV_INT8 ? kQInt8 : kQE4m3;
-        const bool live = amax >= 0x1p-100f && amax <= 3.4e38f;
-        const float inv = live ? __fdiv_rn(Q, amax) : 0.0f;
-        const float scale = amax > 3.4e38f ? __int_as_float(0x7fc00000) : live ? __fdiv_rn(amax, Q) : 0.0f;
-        const int64_t dst = load_page(c, b, page);
-        if (dst >= 0) {
-            if (tid == 0) (is_v ? c.vs : c.ks)[dst * c.Hk + h] = scale;
-            uint8_t *codes = (is_v ? c.vc : c.kc) + page_at(c, dst, h);
+        for (int g = 0; g < PG; ++g) {
+            if (dst[g] < 0) continue;
+            float amax = s_max[g][0];
+#pragma unroll
+            for (int i = 1; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, s_max[g][i]);
+            const float Q = CODE == SI_KV_INT8 ? kQInt8 : kQE4m3;
+            const bool live = amax >= 0x1p-100f && amax <= 3.4e38f;
+            const float inv = live ? __fdiv_rn(Q, amax) : 0.0f;
+            const float scale = amax > 3.4e38f ? __int_as_float(0x7fc00000) : live ? __fdiv_rn(amax, Q) : 0.0f;
+            if (tid == 0) (is_v ? c.vs : c.ks)[dst[g] * c.Hk + h] = scale;
+            uint8_t *codes = (is_v ? c.vc : c.kc) + page_at(c, dst[g], h);
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
                 const int unit = u * kAppendThreads + tid;
                 if (unit >= P * upr) continue;
-                const uint32_t *w = &x[u][0].x;
+                const uint32_t *w = &x[g][u][0].x;
                 uint32_t o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -119,15 +130,14 @@ template <int CODE, int DT>
 static cudaError_t append_units(const Ctx &c, Rows k, Rows v, int32_t *lens_out, cudaStream_t s) {
     // a call of n rows completes at most (P - 1 + n) / P pages of a sequence
     const int pages = max(1, (c.P - 1 + c.max_new) / c.P);
-    const dim3 grid(pages, 2 * c.Hk, c.B);
     const int units = c.P * c.D / 16;
-    if (units <= kAppendThreads)
-        k_kv_append<CODE, DT, 1><<<grid, kAppendThreads, 0, s>>>(c, k, v, lens_out);
-    else if (units <= 2 * kAppendThreads)
-        k_kv_append<CODE, DT, 2><<<grid, kAppendThreads, 0, s>>>(c, k, v, lens_out);
-    else
-        k_kv_append<CODE, DT, 4><<<grid, kAppendThreads, 0, s>>>(c, k, v, lens_out);
-    return cudaGetLastError();
+    const bool many = pages >= 8;  // a prompt: several pages a CTA (a step has one page at most, and the fewest registers)
+    auto go = [&](auto kernel, int pg) {
+        return launch(kernel, dim3((pages + pg - 1) / pg, 2 * c.Hk, c.B), kAppendThreads, 0, s, c, k, v, lens_out);
+    };
+    if (units <= kAppendThreads) return many ? go(k_kv_append<CODE, DT, 1, 4>, 4) : go(k_kv_append<CODE, DT, 1, 1>, 1);
+    if (units <= 2 * kAppendThreads) return many ? go(k_kv_append<CODE, DT, 2, 2>, 2) : go(k_kv_append<CODE, DT, 2, 1>, 1);
+    return go(k_kv_append<CODE, DT, 4, 1>, 1);
 }
 
 cudaError_t launch_append(const Plan &p, const Ctx &c, Rows k, Rows v, int32_t *lens_out, cudaStream_t s) {
@@ -145,6 +155,7 @@ constexpr int kReadThreads = 256;
 template <int CODE, int DT>
 __global__ void __launch_bounds__(kReadThreads) k_kv_read(Ctx c, const int32_t *pages, int64_t units, uint16_t *k_out,
                                                           uint16_t *v_out) {
+    start_after();
     const int64_t unit = (int64_t)blockIdx.x * kReadThreads + threadIdx.x;  // of 16 values, in the output's order
     if (unit >= units) return;
     const int per = c.P * c.D / 16;
@@ -177,18 +188,10 @@ cudaError_t launch_read(const Plan &p, const Ctx &c, const int32_t *pages, int n
     const int64_t units = (int64_t)n * c.Hk * c.P * c.D / 16;
     const int64_t grid = (units + kReadThreads - 1) / kReadThreads;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if (p.desc.code == SI_KV_INT8) {
-        if (p.desc.dtype == SI_KV_BF16)
-            k_kv_read<SI_KV_INT8, SI_KV_BF16><<<(unsigned)grid, kReadThreads, 0, s>>>(c, pages, units, k_out, v_out);
-        else
-            k_kv_read<SI_KV_INT8, SI_KV_F16><<<(unsigned)grid, kReadThreads, 0, s>>>(c, pages, units, k_out, v_out);
-    } else {
-        if (p.desc.dtype == SI_KV_BF16)
-            k_kv_read<SI_KV_E4M3, SI_KV_BF16><<<(unsigned)grid, kReadThreads, 0, s>>>(c, pages, units, k_out, v_out);
-        else
-            k_kv_read<SI_KV_E4M3, SI_KV_F16><<<(unsigned)grid, kReadThreads, 0, s>>>(c, pages, units, k_out, v_out);
-    }
-    return cudaGetLastError();
+    auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)grid), kReadThreads, 0, s, c, pages, units, k_out, v_out); };
+    const bool bf16 = p.desc.dtype == SI_KV_BF16;
+    if (p.desc.code == SI_KV_INT8) return bf16 ? go(k_kv_read<SI_KV_INT8, SI_KV_BF16>) : go(k_kv_read<SI_KV_INT8, SI_KV_F16>);
+    return bf16 ? go(k_kv_read<SI_KV_E4M3, SI_KV_BF16>) : go(k_kv_read<SI_KV_E4M3, SI_KV_F16>);
 }
 
 }  // namespace kv

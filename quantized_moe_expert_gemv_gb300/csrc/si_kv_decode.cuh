@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
     const bool bf16 = a.bf16;
 
+    start_after();
     const Share share = take_share<W>(c.B, [&](int b) -> long long {
         const Seq s = load_seq(c, b);
         const int tiles = seq_tiles(c, s.len);
@@ -725,8 +726,7 @@ cudaError_t decode_launch(const Plan &p, const DecodeArgs &a, cudaStream_t s) {
     using Cfg = DecodeCfg<D, R8>;
     const cudaError_t e = allow_smem<k_kv_decode<CODE, D, R8>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_decode<CODE, D, R8><<<p.sm_count * Cfg::ctas, Cfg::warps * 32, Cfg::smem, s>>>(a);
-    return cudaGetLastError();
+    return launch(k_kv_decode<CODE, D, R8>, dim3(p.sm_count * Cfg::ctas), Cfg::warps * 32, Cfg::smem, s, a);
 }
 
 }  // namespace kv

@@ -11,6 +11,13 @@
 namespace si {
 namespace kv {
 
+// The start of every kernel: the next one may be launched, and this one goes on once the one before it
+// in the stream has ended.
+__device__ __forceinline__ void start_after() {
+    pdl_launch_dependents();
+    pdl_wait();
+}
+
 // One sequence of the call, checked against the host's bounds: a sequence
 // that breaks one has no rows and no tokens here, and the status says so.
 struct Seq {

@@ -2,8 +2,8 @@
 // each kv head's pages, and their move.
 //
 // Choice (k_kv_choose, one CTA for each sequence and kv head).  A page's score
-// is the sum of acc over its tokens in 64 bits (a page that is kept by a last-bit
-// difference of a 32-bit sum would depend on the order of the sum).  Scores
+// is the sum of acc over its tokens in twice 32 bits (a page that is kept by a
+// last-bit difference of a 32-bit sum would depend on the order of the sum).  Scores
 // become 64-bit keys whose unsigned order is the scores' order, the protected
 // pages get the largest key, and a radix selection finds the key of the last
 // page that stays: 8 bits a pass from the top, a histogram of the keys that
@@ -18,7 +18,7 @@
 namespace si {
 namespace kv {
 
-constexpr int kChooseThreads = 512;
+constexpr int kChooseMost = 1024;
 constexpr int kMoveThreads = 256;
 
 // Order-preserving key of a score; NaN counts as largest, -0 as +0.
@@ -29,16 +29,24 @@ __device__ __forceinline__ unsigned long long score_key(double x) {
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
+// Sums in twice 32 bits: s + e is the sum so far, e what its additions have rounded off (the error of each
+// addition is a number of 32 bits and is found by additions; D. Knuth's two-sum).  A page of 64 tokens is off by
+// less than 2^-40 of its sum; the 64-bit unit, of two lanes a cycle and SM, took 17 us for 32768 tokens.
+__device__ __forceinline__ void add_two(float &s, float &e, float x) {
+    const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
+    s = t;
+}
+
 // Exclusive prefix of a 0/1 flag over the CTA's threads in order; `total` = their sum.
 __device__ __forceinline__ int block_prefix(bool flag, int *s_warp, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kChooseThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const unsigned m = __ballot_sync(0xffffffffu, flag);
     __syncthreads();  // s_warp's earlier use is over
     if (lane == 0) s_warp[warp] = __popc(m);
     __syncthreads();
     int before = 0;
     total = 0;
-#pragma unroll
     for (int w = 0; w < warps; ++w) {
         before += w < warp ? s_warp[w] : 0;
         total += s_warp[w];
@@ -46,39 +54,62 @@ __device__ __forceinline__ int block_prefix(bool flag, int *s_warp, int &total) 
     return before + __popc(m & ((1u << lane) - 1));
 }
 
-__global__ void __launch_bounds__(kChooseThreads) k_kv_choose(Ctx c, const float *acc, int64_t acc_stride, int budget,
+__global__ void __launch_bounds__(kChooseMost) k_kv_choose(Ctx c, const float *acc, int64_t acc_stride, int budget,
                                                               int sink, int recent, int32_t *keep, int32_t *lens_out) {
     extern __shared__ unsigned long long s_key[];  // [max_len / P]
-    __shared__ int s_hist[256], s_warp[kChooseThreads / 32], s_digit, s_above, s_in;
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, P = c.P;
+    __shared__ int s_hist[256], s_warp[kChooseMost / 32], s_digit, s_above, s_in;
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, threads = blockDim.x, P = c.P;
+    start_after();
     const Seq s = load_seq(c, b, false);
     const int F = s.len / P, n_keep = min(F, budget);
     keep += ((int64_t)b * c.Hk + h) * budget;
     if (h == 0 && tid == 0) lens_out[b] = n_keep * P + s.len % P;
-    for (int i = n_keep + tid; i < budget; i += kChooseThreads) keep[i] = -1;
+    for (int i = n_keep + tid; i < budget; i += threads) keep[i] = -1;
     if (F <= budget) {
-        for (int i = tid; i < F; i += kChooseThreads) keep[i] = i;
+        for (int i = tid; i < F; i += threads) keep[i] = i;
         return;
     }
-    // A group of P/4.. threads per page would share lanes; 8 lanes a page read P/8 values each.
+    // 16 lanes a page, 8 pages' loads at a time under way (four a lane and page at most)
     const float *a = acc + ((int64_t)b * c.Hk + h) * acc_stride;
-    const int lane8 = tid & 7;
-    for (int j0 = 0; j0 < F; j0 += kChooseThreads / 8) {
-        const int j = j0 + (tid >> 3);
-        double sum = 0.0;
-        if (j < F)
-            for (int t = lane8; t < P; t += 8) sum += (double)a[(int64_t)j * P + t];
-        for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (j < F && lane8 == 0) s_key[j] = j < sink || j >= F - recent ? ~0ull : score_key(sum);
+    const int l16 = tid & 15, step = threads / 16;
+    const unsigned half = 0xffffu << (tid & 16);
+    for (int j0 = tid >> 4; j0 < F; j0 += 8 * step) {
+        float x[8][4];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = j0 + q * step, t = l16 + 16 * e;
+                x[q][e] = j < F && t < P ? a[(int64_t)j * P + t] : 0.0f;
+            }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int j = j0 + q * step;
+            if (j >= F) break;
+            float hi = x[q][0], lo = 0.0f;
+#pragma unroll
+            for (int e = 1; e < 4; ++e) add_two(hi, lo, x[q][e]);
+            for (int o = 8; o; o >>= 1) {
+                const float y = __shfl_xor_sync(half, hi, o), z = __shfl_xor_sync(half, lo, o);
+                add_two(hi, lo, y);
+                lo += z;
+            }
+            double sum = (double)hi + (double)lo;
+            if (!(fabsf(hi) <= 3.4e38f)) {  // infinite, NaN, or past 32 bits' range: in 64 bits after all
+                sum = ((double)x[q][0] + (double)x[q][1]) + ((double)x[q][2] + (double)x[q][3]);
+                for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
+            }
+            if (l16 == 0) s_key[j] = j < sink || j >= F - recent ? ~0ull : score_key(sum);
+        }
     }
     __syncthreads();
     unsigned long long prefix = 0, mask = 0;
     int want = n_keep;  // pages still to be taken among those that share the prefix
     bool ties = true;
     for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kChooseThreads) s_hist[i] = 0;
+        for (int i = tid; i < 256; i += threads) s_hist[i] = 0;
         __syncthreads();
-        for (int j = tid; j < F; j += kChooseThreads)
+        for (int j = tid; j < F; j += threads)
             if ((s_key[j] & mask) == prefix) atomicAdd(&s_hist[(s_key[j] >> shift) & 255], 1);
         __syncthreads();
         if (tid < 32) {  // the digit whose bin the last wanted page falls in, from the top
@@ -110,7 +141,7 @@ __global__ void __launch_bounds__(kChooseThreads) k_kv_choose(Ctx c, const float
     }
     // Taken: keys above the prefix, and of those that share it all, or the first `want`.
     int kept = 0, tied = 0;
-    for (int j0 = 0; j0 < F; j0 += kChooseThreads) {
+    for (int j0 = 0; j0 < F; j0 += threads) {
         const int j = j0 + tid;
         const unsigned long long k = j < F ? s_key[j] & mask : 0;
         bool take = j < F && k >= prefix;
@@ -131,6 +162,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(Ctx c, const float *ac
                                                           int budget, int most, const int32_t *new_table,
                                                           const int32_t *new_slots, const int32_t *keep) {
     const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, P = c.P;
+    start_after();
     const Seq s = load_seq(c, b, false);
     const int F = s.len / P, n_keep = min(F, budget);
     const int64_t bh = (int64_t)b * c.Hk + h;
@@ -183,13 +215,13 @@ cudaError_t launch_evict(const Plan &p, const Ctx &c, const float *acc_in, float
     const size_t smem = (size_t)(c.max_len / c.P) * sizeof(unsigned long long);
     cudaError_t e = allow_smem<k_kv_choose>(p, SI_KV_MAX_EVICT_PAGES * (int)sizeof(unsigned long long));
     if (e != cudaSuccess) return e;
-    k_kv_choose<<<dim3(c.Hk, c.B), kChooseThreads, smem, s>>>(c, acc_in, acc_stride, budget, sink, recent, keep,
-                                                              lens_out);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // as many threads as half-warps for a page, up to 1024 (a small cache's block-wide steps are quicker with few)
+    const int threads = c.max_len / c.P <= 64 ? 256 : kChooseMost;
+    e = launch(k_kv_choose, dim3(c.Hk, c.B), threads, smem, s, c, acc_in, acc_stride, budget, sink, recent, keep, lens_out);
+    if (e != cudaSuccess) return e;
     const int most = min(budget, c.max_len / c.P);  // no sequence keeps more
-    k_kv_move<<<dim3(most + 1, c.Hk, c.B), kMoveThreads, 0, s>>>(c, acc_in, acc_out, acc_stride, budget, most,
-                                                                 new_table, new_slots, keep);
-    return cudaGetLastError();
+    return launch(k_kv_move, dim3(most + 1, c.Hk, c.B), kMoveThreads, 0, s, c, acc_in, acc_out, acc_stride, budget, most,
+                  new_table, new_slots, keep);
 }
 
 }  // namespace kv

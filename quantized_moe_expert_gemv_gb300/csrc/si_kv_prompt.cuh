@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform)
     const bool bf16 = a.bf16;
 
+    start_after();
     // ---- which rows: the last ones of each sequence first (they see the most keys)
     const int bh = c.B * c.Hk;
     const int split = blockIdx.x % a.splits, id = blockIdx.x / a.splits;
@@ -531,6 +532,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
 // The splits' partial sums joined in their order: a thread four values of a row.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
+    start_after();
     const Ctx &c = a.c;
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t rh = at / (D / 4);
@@ -580,11 +582,10 @@ cudaError_t prompt_launch(const Plan &p, const PromptArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t blocks = ((int64_t)a.c.max_new * a.c.G + kPrRows - 1) / kPrRows * a.c.Hk * a.c.B * a.splits;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    k_kv_prompt<CODE, D><<<(unsigned)blocks, kPrThreads, Cfg::smem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+    e = launch(k_kv_prompt<CODE, D>, dim3((unsigned)blocks), kPrThreads, Cfg::smem, s, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
     const int64_t n = (int64_t)a.c.T * a.c.H * (D / 4);
-    k_kv_join<D><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(k_kv_join<D>, dim3((unsigned)((n + 255) / 256)), 256, 0, s, a);
 }
 
 }  // namespace kv

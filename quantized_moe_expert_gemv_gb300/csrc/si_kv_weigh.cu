@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, j = lane & 3;
     const bool bf16 = a.bf16;
 
+    start_after();
     const Share share = take_share<W>(c.B, [&](int b) -> long long {
         const int tiles = seq_tiles(c, load_seq(c, b).len);
         return tiles == 0 ? 0ll : (long long)(tiles + kWeighOver) * c.Hk;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
     float *part = reinterpret_cast<float *>(at + Cfg::part);
     auto bar = [&](int i) { return base + Cfg::bars + 8 * i; };
 
+    start_after();
     const Share share = take_share<kWwThreads / 32>(c.B, [&](int b) -> long long {
         const int tiles = window_tiles(load_seq(c, b).len);
         return tiles == 0 ? 0ll : (long long)(tiles + kWindowOver) * c.Hk;
@@ -599,6 +601,7 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
     __shared__ uint32_t s_tmem;
     const Ctx &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform)
+    start_after();
     const int b = blockIdx.z, h = blockIdx.y, key0 = blockIdx.x * kTileRows;
     const Seq s = load_seq(c, b);
     if (key0 >= s.len) return;
@@ -761,8 +764,7 @@ static cudaError_t few(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighCfg<D>;
     cudaError_t e = allow_smem<k_kv_weigh_few<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_weigh_few<CODE, D><<<p.sm_count * Cfg::ctas, Cfg::warps * 32, Cfg::smem, s>>>(a);
-    return cudaGetLastError();
+    return launch(k_kv_weigh_few<CODE, D>, dim3(p.sm_count * Cfg::ctas), Cfg::warps * 32, Cfg::smem, s, a);
 }
 template <int CODE, int D>
 static cudaError_t many(const Plan &p, const WeighArgs &a, cudaStream_t s) {
@@ -770,16 +772,14 @@ static cudaError_t many(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     cudaError_t e = allow_smem<k_kv_weigh_many<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((a.c.max_len + kTileRows - 1) / kTileRows, a.c.Hk, a.c.B);
-    k_kv_weigh_many<CODE, D><<<grid, kWmThreads, Cfg::smem, s>>>(a);
-    return cudaGetLastError();
+    return launch(k_kv_weigh_many<CODE, D>, grid, kWmThreads, Cfg::smem, s, a);
 }
 template <int CODE, int D>
 static cudaError_t window(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighWindowCfg<D>;
     cudaError_t e = allow_smem<k_kv_weigh_window<CODE, D>>(p, Cfg::smem);
     if (e != cudaSuccess) return e;
-    k_kv_weigh_window<CODE, D><<<p.sm_count, kWwThreads, Cfg::smem, s>>>(a);
-    return cudaGetLastError();
+    return launch(k_kv_weigh_window<CODE, D>, dim3(p.sm_count), kWwThreads, Cfg::smem, s, a);
 }
 template <int CODE>
 static cudaError_t weigh(const Plan &p, const WeighArgs &a, cudaStream_t s) {
