@@ -12,7 +12,7 @@
 // other CTA reads the ring.
 // Bound: HBM (2 bytes in, 1 byte out for each value of a completed page); a
 // decode step completes few pages and is bound by latency.
-#include "si_kv_device.cuh"
+#include "si_kv_mma.cuh"
 
 namespace si {
 namespace kv {
@@ -65,19 +65,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(Ctx c, Rows k, Row
             }
 #pragma unroll
         for (int g = 0; g < PG; ++g) {
-            float amax = 0.0f;
-            bool bad = false;  // an infinity or NaN
+            float amax = 0.0f;  // (infinite where a value is not finite)
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const uint32_t *w = &x[g][u][0].x;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float lo = fabsf(to_float<DT>((uint16_t)w[i])), hi = fabsf(to_float<DT>((uint16_t)(w[i] >> 16)));
-                    bad |= !(lo <= 3.4e38f) || !(hi <= 3.4e38f);
-                    amax = fmaxf(amax, fmaxf(lo, hi));
-                }
-            }
-            if (bad) amax = __int_as_float(0x7f800000);  // carried through the maximum as an infinity
+            for (int u = 0; u < UN; ++u)
+                amax = fmaxf(amax, fmaxf(amax8(x[g][u][0], DT == SI_KV_BF16), amax8(x[g][u][1], DT == SI_KV_BF16)));
             for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             if ((tid & 31) == 0) s_max[g][tid >> 5] = amax;
         }
@@ -98,19 +89,14 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(Ctx c, Rows k, Row
             for (int u = 0; u < UN; ++u) {
                 const int unit = u * kAppendThreads + tid;
                 if (unit >= P * upr) continue;
-                const uint32_t *w = &x[g][u][0].x;
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint16_t bits = (uint16_t)(w[2 * i + (e >> 1)] >> (16 * (e & 1)));
-                        f[e] = live ? to_float<DT>(bits) * inv : 0.0f;
-                    }
-                    o[i] = to_codes<CODE>(f[0], f[1], f[2], f[3]);
+                uint4 o = make_uint4(0, 0, 0, 0);
+                if (live) {
+                    o.x = to_codes<CODE, DT>(x[g][u][0].x, x[g][u][0].y, inv);
+                    o.y = to_codes<CODE, DT>(x[g][u][0].z, x[g][u][0].w, inv);
+                    o.z = to_codes<CODE, DT>(x[g][u][1].x, x[g][u][1].y, inv);
+                    o.w = to_codes<CODE, DT>(x[g][u][1].z, x[g][u][1].w, inv);
                 }
-                *reinterpret_cast<uint4 *>(codes + (int64_t)unit * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(codes + (int64_t)unit * 16) = o;
             }
         }
     }

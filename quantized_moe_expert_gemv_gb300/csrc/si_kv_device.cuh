@@ -90,17 +90,34 @@ __device__ __forceinline__ float code_value(uint8_t c) {
     v.__x = c;
     return (float)v;
 }
-// Four scaled values to four codes, the first in the low byte.  (An amax whose
-// reciprocal rounds up gives at most Q(1 + 2^-23), which rounds to Q.)
-template <int CODE>
-__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
-    if constexpr (CODE == SI_KV_INT8) {
-        const uint32_t x = (uint32_t)__float2int_rn(a) & 255u, y = (uint32_t)__float2int_rn(b) & 255u;
-        const uint32_t z = (uint32_t)__float2int_rn(c) & 255u, w = (uint32_t)__float2int_rn(d) & 255u;
-        return x | (y << 8) | (z << 16) | (w << 24);
+// Four 16-bit values (a pair a word) times inv, each product rounded to 32 bits, to four codes, the first in
+// the low byte.  (An amax whose reciprocal rounds up gives at most Q(1 + 2^-23), which rounds to Q.)
+template <int CODE, int DT>
+__device__ __forceinline__ uint32_t to_codes(uint32_t ab, uint32_t cd, float inv) {
+    float f[4];
+    if constexpr (DT == SI_KV_BF16) {
+        f[0] = __uint_as_float(ab << 16);
+        f[1] = __uint_as_float(ab & 0xffff0000u);
+        f[2] = __uint_as_float(cd << 16);
+        f[3] = __uint_as_float(cd & 0xffff0000u);
     } else {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&ab)), y = __half22float2(*reinterpret_cast<const __half2 *>(&cd));
+        f[0] = x.x;
+        f[1] = x.y;
+        f[2] = y.x;
+        f[3] = y.y;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = __fmul_rn(f[e], inv);
+    if constexpr (CODE == SI_KV_INT8) {
+        // 1.5 * 2^23 + x, rounded half to even, has round(x) in its low bits, in two's complement
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = __float_as_uint(__fadd_rn(f[e], 12582912.0f));
+        return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
         return lo | (hi << 16);
     }
 }
