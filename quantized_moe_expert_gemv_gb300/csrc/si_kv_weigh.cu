@@ -184,17 +184,20 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
             // n sums (of pieces p_first + W i from i = first on, or of the tokens from t0 on) onto the earlier ones
             auto flush = [&](int n, int first, int t0) {
                 __syncwarp();
-#pragma unroll 4
-                for (int k = lane; k < n; k += 32) {
-                    const int t = t0 >= 0 ? t0 + k : ((p_first + W * (first + k / 16)) << 4) + k % 16;
-                    if (t < s.len) {
-                        float was = 0.0f;
-                        if (rb > 0)
-                            was = a.acc_out[acc_at + t];
-                        else if (a.acc_in && t < old)
-                            was = a.decay * a.acc_in[acc_at + t];
-                        a.acc_out[acc_at + t] = was + sums[k];
-                    }
+                float was[16];  // (all of the earlier sums' loads at once)
+                const float *from = rb > 0 ? a.acc_out : a.acc_in;
+                const int stop = rb > 0 ? s.len : a.acc_in ? old : 0;
+                auto token = [&](int k) { return t0 >= 0 ? t0 + k : ((p_first + W * (first + k / 16)) << 4) + k % 16; };
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int k = 32 * q + lane, t = token(k);
+                    was[q] = k < n && t < stop ? from[acc_at + t] : 0.0f;
+                }
+                const float decay = rb > 0 ? 1.0f : a.decay;
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int k = 32 * q + lane, t = token(k);
+                    if (k < n && t < s.len) a.acc_out[acc_at + t] = decay * was[q] + sums[k];
                 }
                 __syncwarp();
             };
