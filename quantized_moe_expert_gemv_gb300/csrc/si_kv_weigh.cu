@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
     const Share share = take_share<W>(c.B, [&](int b) -> long long {
         const int tiles = seq_tiles(c, load_seq(c, b).len);
         return tiles == 0 ? 0ll : (long long)(tiles + kWeighOver) * c.Hk;
-    });
+    }, [&](int) { return c.Hk; }, 0);
     if (blockIdx.x >= share.ctas) return;
     int b = share.b;
     long long off = share.off, u = share.begin;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
     const Share share = take_share<kWwThreads / 32>(c.B, [&](int b) -> long long {
         const int tiles = window_tiles(load_seq(c, b).len);
         return tiles == 0 ? 0ll : (long long)(tiles + kWindowOver) * c.Hk;
-    });
+    }, [&](int) { return c.Hk; }, 0);
     if (blockIdx.x >= share.ctas) return;
     if (tid == 0) {
         mbar_init(bar(kXbQ), 256);
