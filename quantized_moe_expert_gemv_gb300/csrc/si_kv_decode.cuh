@@ -96,8 +96,9 @@ struct Segment {  // what a share takes of an item: its tiles [first, end) of `t
 __device__ __forceinline__ Segment take_segment(int tiles, int over, long long off, long long u, long long u_end) {
     Segment s;
     const int all = tiles + over;
-    s.item = (int)(off / all);
-    const int x0 = (int)(off % all), x1 = (int)min((long long)all, x0 + (u_end - u));
+    // (a 64-bit division takes a hundred instructions: only where the numbers need it)
+    s.item = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)all) : (int)(off / all);
+    const int x0 = (int)(off - (long long)s.item * all), x1 = (int)min((long long)all, x0 + (u_end - u));
     s.first = max(0, x0 - over);
     s.end = max(0, x1 - over);
     s.step = x1 - x0;
@@ -105,6 +106,17 @@ __device__ __forceinline__ Segment take_segment(int tiles, int over, long long o
     s.unit1 = u - x0 + all - 1;
     return s;
 }
+
+// k of n parts of a total, and the part that unit u lies in (k n fits 32 bits for totals up to 2^21).
+__device__ __forceinline__ long long part_of(uint32_t k, long long total, long long n) {
+    if (total < (1 << 21)) return (uint32_t)(k * (uint32_t)total) / (uint32_t)n;
+    return k * total / n;
+}
+__device__ __forceinline__ int part_with(long long u, long long total, long long n) {
+    if (total < (1 << 21)) return (int)(((uint32_t)(u + 1) * (uint32_t)n - 1) / (uint32_t)total);
+    return (int)(((u + 1) * n - 1) / total);
+}
+static_assert(kMaxDecodeCtas <= 2047, "k and n of part_of and part_with");
 
 // A CTA's equal share [begin, end) of all units, and the sequence that `begin` lies in.  `units_of(b)`:
 // units of sequence b.  All threads call this; `some_empty`: whether a sequence has none.
@@ -156,8 +168,8 @@ __device__ __forceinline__ Share take_share(int B, F units_of, G items_of, int a
     s.ctas = s.ctas < (long long)gridDim.x ? s.ctas : (long long)gridDim.x;
     s.begin = s.end = 0;
     if (blockIdx.x < s.ctas) {
-        s.begin = blockIdx.x * s.total / s.ctas;
-        s.end = (blockIdx.x + 1) * s.total / s.ctas;
+        s.begin = part_of(blockIdx.x, s.total, s.ctas);
+        s.end = part_of(blockIdx.x + 1, s.total, s.ctas);
         if (before <= s.begin && s.begin < before + mine) {
             int b = tid * per;
             long long at = before, n;
@@ -243,6 +255,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
         const int lim_min = old + rb * R / c.G + 1, lim_max = old + (rb * R + rows - 1) / c.G + 1;
         const int paged_tiles = (paged + 63) / 64;
 
+        // q's rows are on their way first: nothing else waits for them
+        RowPart<D> q_part[Cfg::q_in_regs ? R8 : 1];
+        auto q_load = [&](int n, RowPart<D> &to) {
+            const int r = rb * R + n * 8 + g;
+            const bool live = n * 8 + g < rows;
+            to.load(a.q.p + (s.row0 + (live ? r / c.G : 0)) * a.q.row + (h * c.G + (live ? r % c.G : 0)) * a.q.head, live, j);
+        };
+        if constexpr (Cfg::q_in_regs) {
+#pragma unroll
+            for (int n = 0; n < R8; ++n) q_load(n, q_part[n]);
+        }
+
         // this warp's pieces of full pages: page and scales of 32 pieces at a time (a lane a piece), two sets
         const int p_first = 4 * t_first + w;
         const int p_stop = min(min(4 * t_end, paged >> 4), (lim_max + 15) >> 4);  // no row sees a later piece
@@ -296,11 +320,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
         if (!Cfg::q_in_regs) __syncthreads();  // the last item's readers are done
 #pragma unroll
         for (int n = 0; n < R8; ++n) {
-            const int r = rb * R + n * 8 + g;
-            const bool live = n * 8 + g < rows;
-            const int i = live ? r / c.G : 0, head = h * c.G + (live ? r % c.G : 0);
             uint2 op[KS];
-            const float f = row_operand<D>(a.q.p + (s.row0 + i) * a.q.row + head * a.q.head, live, j, bf16, op) * a.scale2;
+            if constexpr (!Cfg::q_in_regs) q_load(n, q_part[0]);
+            const float f = q_part[Cfg::q_in_regs ? n : 0].operand(bf16, op) * a.scale2;
             if constexpr (Cfg::q_in_regs) {
 #pragma unroll
                 for (int st = 0; st < KS; ++st) qb[n][st] = op[st];
@@ -496,42 +518,62 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
         // ---- the unfinished page's rows, in 16 bits: 16 of them for each of the last four warps
         const int tail = s.len - paged, key0 = 16 * (w - (W - 4));
         if (t_end > paged_tiles && key0 >= 0 && paged + key0 < min(s.len, lim_max)) {
+            constexpr bool AT_ONCE = D * R8 <= 64;   // K's and V's loads together, as far as the registers go
+            constexpr int VW = D / 64;               // loads of 8 values of a V row that a lane makes (in halves of a 128)
             float sc[R8][4];
-            uint32_t ka[KS][4];
-            float kf[2];
+            float kf[2], vmul[4], vf[4];
+            RowPart<D> k_part[2];
+            uint4 v_part[4][VW];
+            auto key_of = [&](int k) { return key0 + 2 * j + (k & 1) + 8 * (k >> 1); };
+            auto v_row = [&](int k) {
+                const int key = key_of(k);
+                return c.vt + ring_at(c, s.slot >= 0 ? s.slot : 0, h, paged + (key < tail ? key : 0));
+            };
+            auto load_v = [&]() {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int z = 0; z < VW; ++z) {
+                        const int d = D == 64 ? g * 8 : 128 * (z >> 1) + g * 16 + 8 * (z & 1);
+                        v_part[k][z] = key_of(k) < tail && s.slot >= 0 ? *reinterpret_cast<const uint4 *>(v_row(k) + d) : make_uint4(0, 0, 0, 0);
+                    }
+            };
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int key = key0 + 8 * e + g;
                 const bool live = key < tail && s.slot >= 0;
-                uint2 op[KS];
-                kf[e] = row_operand<D>(c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)), live, j, bf16, op);
-                if (s.slot < 0) kf[e] = __int_as_float(0x7fc00000);
-#pragma unroll
-                for (int st = 0; st < KS; ++st) {
-                    ka[st][e] = op[st].x;
-                    ka[st][2 + e] = op[st].y;
-                }
+                k_part[e].load(c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)), live, j);
             }
+            if constexpr (AT_ONCE) load_v();
+            {
+                uint32_t ka[KS][4];
 #pragma unroll
-            for (int n = 0; n < R8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+                for (int e = 0; e < 2; ++e) {
+                    uint2 op[KS];
+                    kf[e] = k_part[e].operand(bf16, op);
+                    if (s.slot < 0) kf[e] = __int_as_float(0x7fc00000);
 #pragma unroll
-            for (int st = 0; st < KS; ++st) scores(sc, ka[st], st);
-            // V rows: a first pass for the keys' scales, a second for the products
-            float vmul[4], vf[4];
+                    for (int st = 0; st < KS; ++st) {
+                        ka[st][e] = op[st].x;
+                        ka[st][2 + e] = op[st].y;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < R8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+                for (int st = 0; st < KS; ++st) scores(sc, ka[st], st);
+            }
+            if constexpr (!AT_ONCE) load_v();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int key = key0 + 2 * j + (k & 1) + 8 * (k >> 1);
-                const bool live = key < tail && s.slot >= 0;
-                const uint16_t *src = c.vt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)) + g * (D / 8);
                 float amax = 0.0f;
 #pragma unroll
-                for (int z = 0; z < D / 64; ++z)
-                    if (live) amax = fmaxf(amax, amax8(*reinterpret_cast<const uint4 *>(src + 8 * z), bf16));
+                for (int z = 0; z < VW; ++z) amax = fmaxf(amax, amax8(v_part[k][z], bf16));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
                 row_scale(amax, vmul[k], vf[k]);
-                if (!live) vf[k] = 0.0f, vmul[k] = 0.0f;
+                if (!(key_of(k) < tail && s.slot >= 0)) vf[k] = 0.0f, vmul[k] = 0.0f;
             }
             float v_top = fmaxf(fmaxf(vf[0], vf[1]), fmaxf(vf[2], vf[3]));  // (NaN leaves it)
             v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, 1));
@@ -547,30 +589,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             uint32_t pb[R8][2];
             weights(sc, kf[0], kf[1], g & 1 ? of[1] : of[0], g & 1 ? of[3] : of[2], v_top, paged + key0, true, pb);
 #pragma unroll
-            for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-                constexpr int HV = D == 64 ? 1 : 2;  // loads of 8 values of a lane's run of d's
+            for (int z = 0; z < VW; ++z) {  // values d = 8 z .. of the lane's run: row tiles 4 z ..
+                uint32_t x[4][4];
 #pragma unroll
-                for (int z = 0; z < HV; ++z) {
-                    uint32_t x[4][4];
+                for (int k = 0; k < 4; ++k) {
+                    x[k][0] = scale2(v_part[k][z].x, vmul[k], bf16);
+                    x[k][1] = scale2(v_part[k][z].y, vmul[k], bf16);
+                    x[k][2] = scale2(v_part[k][z].z, vmul[k], bf16);
+                    x[k][3] = scale2(v_part[k][z].w, vmul[k], bf16);
+                }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int key = key0 + 2 * j + (k & 1) + 8 * (k >> 1);
-                        const bool live = key < tail && s.slot >= 0;
-                        const uint16_t *src = c.vt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)) + 128 * half +
-                                              g * (D == 64 ? 8 : 16) + 8 * z;
-                        const uint4 v = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                        x[k][0] = scale2(v.x, vmul[k], bf16);
-                        x[k][1] = scale2(v.y, vmul[k], bf16);
-                        x[k][2] = scale2(v.z, vmul[k], bf16);
-                        x[k][3] = scale2(v.w, vmul[k], bf16);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t va[4] = {__byte_perm(x[0][q], x[1][q], 0x5410), __byte_perm(x[0][q], x[1][q], 0x7632),
+                                            __byte_perm(x[2][q], x[3][q], 0x5410), __byte_perm(x[2][q], x[3][q], 0x7632)};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t va[4] = {__byte_perm(x[0][q], x[1][q], 0x5410), __byte_perm(x[0][q], x[1][q], 0x7632),
-                                                __byte_perm(x[2][q], x[3][q], 0x5410), __byte_perm(x[2][q], x[3][q], 0x7632)};
-#pragma unroll
-                        for (int n = 0; n < R8; ++n) mma16816(o[n][8 * half + 4 * z + q], va, pb[n][0], pb[n][1]);
-                    }
+                    for (int n = 0; n < R8; ++n) mma16816(o[n][4 * z + q], va, pb[n][0], pb[n][1]);
                 }
             }
         }
@@ -652,7 +685,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             // the scratch and counts itself; the last of a group joins the group's parts (in the place of the
             // group's first), the last group's the groups'.
             const long long N = share.ctas, total = share.total;
-            const int c0 = (int)(((seg.unit0 + 1) * N - 1) / total), c1 = (int)(((seg.unit1 + 1) * N - 1) / total);
+            const int c0 = part_with(seg.unit0, total, N), c1 = part_with(seg.unit1, total, N);
             const int nc = c1 - c0 + 1, me = (int)blockIdx.x - c0;
             const int64_t pf = partial_floats(R, D);
             auto slot_of = [&](int k) { return a.partial + (2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0)) * pf; };
@@ -667,6 +700,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             auto join = [&](int first, int n, int step, bool last) {
                 float2 *ml = reinterpret_cast<float2 *>(smem);  // [n][rows] maximum, sum; then the part's factor
                 float *top_sum = s_part[0];
+                auto at_of = [&](int k) { return k / (D / 4) * D + k % (D / 4) * 4; };
                 for (int k = tid; k < n * rows; k += THREADS)
                     ml[k] = __ldcg(reinterpret_cast<const float2 *>(slot_of(first + k / rows * step) + R * D) + k % rows);
                 __syncthreads();
@@ -685,19 +719,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 for (int k = tid; k < rows * (D / 4); k += THREADS) {
                     const int r = k / (D / 4), d = k % (D / 4) * 4;
                     float4 x = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-                    for (int q = 0; q < n; ++q) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + r * D + d));
+                    auto add = [&](const float4 &v, int q) {
                         const float f = ml[q * rows + r].x;
-                        x.x = fmaf(y.x, f, x.x);
-                        x.y = fmaf(y.y, f, x.y);
-                        x.z = fmaf(y.z, f, x.z);
-                        x.w = fmaf(y.w, f, x.w);
-                    }
+                        x.x = fmaf(v.x, f, x.x);
+                        x.y = fmaf(v.y, f, x.y);
+                        x.z = fmaf(v.z, f, x.z);
+                        x.w = fmaf(v.w, f, x.w);
+                    };
+#pragma unroll 8
+                    for (int q = 0; q < n; ++q) add(__ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + at_of(k))), q);
                     if (last)
                         store(r, d, x, top_sum[2 * r + 1]);
                     else
-                        __stcg(reinterpret_cast<float4 *>(slot_of(first) + r * D + d), x);
+                        __stcg(reinterpret_cast<float4 *>(slot_of(first) + at_of(k)), x);
                 }
                 if (tid < rows) {
                     if (last)

@@ -192,29 +192,34 @@ __device__ __forceinline__ constexpr int k_dim(int j, int i) {
 
 // The first product's operand of one 16-bit row, this lane's D/4 values of it: op[s] of step s is
 // (two values for k = 2j, 2j+1; two for k = 2j+8, 2j+9).  The four lanes of a g hold a row
-// together; all 32 lanes call this.  Returns the factor that undoes the scaling.
+// together.  The loads are apart, so that others can be under way with them; all 32 lanes call operand(), which
+// returns the factor that undoes the scaling.
 template <int D>
-__device__ __forceinline__ float row_operand(const uint16_t *src, bool live, int j, bool bf16, uint2 (&op)[D / 16]) {
+struct RowPart {
     uint4 x[D / 32];
-    float amax = 0.0f;
+    __device__ __forceinline__ void load(const uint16_t *src, bool live, int j) {
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k)
+        for (int k = 0; k < D / 64; ++k)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
-            amax = fmaxf(amax, amax8(x[2 * k + z], bf16));
-        }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    float mul, f;
-    row_scale(amax, mul, f);
-#pragma unroll
-    for (int st = 0; st < D / 16; ++st) {  // chunk st / 4, four values at 4 * (st % 4)
-        const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
-        op[st] = make_uint2(scale2(st & 1 ? v.z : v.x, mul, bf16), scale2(st & 1 ? v.w : v.y, mul, bf16));
+            for (int z = 0; z < 2; ++z)
+                x[2 * k + z] = live ? *reinterpret_cast<const uint4 *>(src + k_dim<D>(j, k) + 8 * z) : make_uint4(0, 0, 0, 0);
     }
-    return f;
-}
+    __device__ __forceinline__ float operand(bool bf16, uint2 (&op)[D / 16]) const {
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) amax = fmaxf(amax, amax8(x[k], bf16));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float mul, f;
+        row_scale(amax, mul, f);
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) {  // chunk st / 4, four values at 4 * (st % 4)
+            const uint4 &v = x[2 * (st >> 2) + ((st >> 1) & 1)];
+            op[st] = make_uint2(scale2(st & 1 ? v.z : v.x, mul, bf16), scale2(st & 1 ? v.w : v.y, mul, bf16));
+        }
+        return f;
+    }
+};
 
 // The keys' operand of every step, from a tile of codes: keys g (ka[.][0], [2]) and g + 8 ([1], [3]).
 // at[q]: tile_at<D>(g, k_dim(j, q) / 16) for q < 2.

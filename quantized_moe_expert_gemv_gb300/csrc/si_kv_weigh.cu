@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
                 const bool live = r < rows;
                 const int i = live ? rr / c.G : 0, head = h * c.G + (live ? rr % c.G : 0);
                 uint2 op[KS];
-                const float f = row_operand<D>(a.q.p + (s.row0 + i) * a.q.row + head * a.q.head, live, j, bf16, op);
+                RowPart<D> part;
+                part.load(a.q.p + (s.row0 + i) * a.q.row + head * a.q.head, live, j);
+                const float f = part.operand(bf16, op);
                 if (j == 0)  // (a row that pads weighs nothing)
                     rowf[r] = live ? make_float2(f * a.scale2, a.lse[(int64_t)(s.row0 + i) * c.H + head] * kLog2e)
                                    : make_float2(0.0f, INFINITY);
@@ -253,7 +255,9 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
                     const int key = key0 + 8 * n + g;
                     const bool live = key < tail && s.slot >= 0;
                     uint2 op[KS];
-                    kf[n] = row_operand<D>(c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)), live, j, bf16, op);
+                    RowPart<D> part;
+                    part.load(c.kt + ring_at(c, live ? s.slot : 0, h, paged + (live ? key : 0)), live, j);
+                    kf[n] = part.operand(bf16, op);
                     if (s.slot < 0) kf[n] = __int_as_float(0x7fc00000);
 #pragma unroll
                     for (int st = 0; st < KS; ++st) {
