@@ -267,6 +267,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             for (int n = 0; n < R8; ++n) q_load(n, q_part[n]);
         }
 
+        // and the unfinished page's rows on their way to the second-level cache
+        if (t_end > paged_tiles && w >= W - 4 && s.slot >= 0) {
+            constexpr int LINES = D / 64;  // of 128 bytes in a row
+#pragma unroll
+            for (int k = lane; k < 16 * LINES; k += 32) {
+                const int t = paged + 16 * (w - (W - 4)) + k / LINES;
+                if (t < s.len) {
+                    const int64_t at = ring_at(c, s.slot, h, t) + k % LINES * 64;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(c.kt + at));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(c.vt + at));
+                }
+            }
+        }
+
         // this warp's pieces of full pages: page and scales of 32 pieces at a time (a lane a piece), two sets
         const int p_first = 4 * t_first + w;
         const int p_stop = min(min(4 * t_end, paged >> 4), (lim_max + 15) >> 4);  // no row sees a later piece
