@@ -13,14 +13,22 @@ cudaError_t launch_prompt_e4m3(const Plan &p, const PromptArgs &a, cudaStream_t 
 static bool many_rows(const Plan &p, int max_new) {
     return p.desc.head_dim <= 128 && (int64_t)max_new * (p.desc.n_heads / p.desc.n_kv_heads) > 64;
 }
-// Its CTAs are split along the keys where a call has too few row blocks for
-// the SMs, as long as a part has four tiles of keys.
-static int prompt_splits(const Plan &p, int n_seqs, int max_new, int max_len) {
+// Its CTAs are split along the keys where the longest of them would outlast the
+// work of all of them spread over the SMs, into parts of four key tiles or more
+// (a tile takes about 1.7 us; a part's start and the join of the parts, 5 us).  Where
+// the parts' results lie is bounded: kPartialRows rows (query heads counted) for an SM.
+constexpr int kMaxSplits = 32, kPartialRows = 4 * kPrRows;
+static int prompt_splits(const Plan &p, int total_new, int max_new, int max_len) {
     const int64_t G = p.desc.n_heads / p.desc.n_kv_heads;
-    const int64_t ctas = (max_new * G + kPrRows - 1) / kPrRows * p.desc.n_kv_heads * n_seqs;
-    const int64_t parts = ctas > 0 ? p.sm_count / ctas : 1, most = max_len / kPrKeys / 4;
-    const int64_t n = parts < most ? parts : most;
-    return n < 1 ? 1 : n > 32 ? 32 : (int)n;
+    const int64_t blocks = (total_new * G + kPrRows - 1) / kPrRows * p.desc.n_kv_heads;
+    const int64_t longest = (max_len + kPrKeys - 1) / kPrKeys, mean = (max_len - max_new / 2 + kPrKeys - 1) / kPrKeys;
+    int64_t part = blocks * mean / p.sm_count;
+    if (part < 4) part = 4;
+    if (longest <= part + 3) return 1;
+    int64_t n = (longest + part - 1) / part;
+    const int64_t most = (int64_t)p.sm_count * kPartialRows / ((int64_t)total_new * p.desc.n_heads);
+    if (n > most) n = most;
+    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
 
 // Column tiles of 8 rows in a row group of the few-row kernel: the fewest that hold a sequence's rows,
@@ -30,19 +38,15 @@ static int row_tiles(const Plan &p, int max_new) {
     return rows <= 8 ? 1 : rows <= 16 || p.desc.head_dim == 256 ? 2 : 4;
 }
 
-size_t scratch_bytes(const Plan &p, int n_seqs, int total_new, int max_new, int max_len) {
+size_t scratch_bytes(const Plan &p, int, int total_new, int max_new, int) {
     // A buffer for larger bounds serves smaller ones, so this takes the most that any call within the bounds needs:
-    // a call with fewer sequences or rows may be split more (at most sm_count CTAs of 256 rows together).
+    // a call with fewer rows may be split more.
     const size_t D = p.desc.head_dim;
     size_t most = (size_t)p.sm_count * DecodeCfg<64, 1>::ctas * 2 * (size_t)partial_floats(8 * row_tiles(p, max_new), p.desc.head_dim) * sizeof(float);
     if (many_rows(p, max_new)) {
-        const size_t row_heads = (size_t)total_new * p.desc.n_heads;
-        size_t n = row_heads * 32;                                         // 32 splits at most, and
-        const size_t cap = (size_t)p.sm_count * kPrRows;                   // splits x CTAs <= sm_count: rows x splits
+        const size_t row_heads = (size_t)total_new * p.desc.n_heads, cap = (size_t)p.sm_count * kPartialRows;
+        size_t n = row_heads * kMaxSplits;
         n = n < cap ? n : cap;
-        n = n > row_heads ? n : row_heads;
-        (void)n_seqs;
-        (void)max_len;
         n = n * (D + 2) * sizeof(float);
         most = n > most ? n : most;
     }
@@ -60,7 +64,7 @@ cudaError_t launch_attend(const Plan &p, const Ctx &c, Rows q, Rows out, float *
         a.scale2 = sm * kLog2e;
         a.bf16 = p.desc.dtype == SI_KV_BF16;
         a.log_page = log_page;
-        a.splits = prompt_splits(p, c.B, c.max_new, c.max_len);
+        a.splits = prompt_splits(p, c.T, c.max_new, c.max_len);
         a.fault = p.fault_wait;
         a.budget = p.wait_budget;
         a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + kCtrlBytes);
