@@ -1,4 +1,7 @@
 // si_kv_attend.cu -- which kernel a call of si_kv_attend takes, and the scratch it needs.
+#include <algorithm>
+#include <cmath>
+
 #include "si_kv_prompt.cuh"
 
 namespace si {
@@ -13,22 +16,34 @@ cudaError_t launch_prompt_e4m3(const Plan &p, const PromptArgs &a, cudaStream_t 
 static bool many_rows(const Plan &p, int max_new) {
     return p.desc.head_dim <= 128 && (int64_t)max_new * (p.desc.n_heads / p.desc.n_kv_heads) > 64;
 }
-// Its CTAs are split along the keys where the longest of them would outlast the
-// work of all of them spread over the SMs, into parts of four key tiles or more
-// (a tile takes about 1.7 us; a part's start and the join of the parts, 5 us).  Where
-// the parts' results lie is bounded: kPartialRows rows (query heads counted) for an SM.
+// Its CTAs are split along the keys into as many parts as the estimate below
+// makes the call shortest with, from bounds that the host has: the longest CTA,
+// the waves of CTAs over the SMs (a CTA an SM), the mean work; a key tile takes
+// 1.6 us, a wave's start and end 8, the join of parts 6 and 0.9 for each MB of
+// partial results.  Measured, one part against the chosen number: 300 new tokens
+// behind 20000, 8 heads: 249 and 58 us (8 parts); 512 behind 8000, 32 heads: 121 and
+// 86 us (2).  Where it stays at one part, two would take: 1349 new tokens, 16
+// heads: 47 instead of 36 us; 1024 behind 24000, 32 heads: 353 instead of 306.
+// The partial results are bounded: kPartialRows rows (query heads counted) for an SM.
 constexpr int kMaxSplits = 32, kPartialRows = 4 * kPrRows;
 static int prompt_splits(const Plan &p, int total_new, int max_new, int max_len) {
-    const int64_t G = p.desc.n_heads / p.desc.n_kv_heads;
-    const int64_t blocks = (total_new * G + kPrRows - 1) / kPrRows * p.desc.n_kv_heads;
-    const int64_t longest = (max_len + kPrKeys - 1) / kPrKeys, mean = (max_len - max_new / 2 + kPrKeys - 1) / kPrKeys;
-    int64_t part = blocks * mean / p.sm_count;
-    if (part < 4) part = 4;
-    if (longest <= part + 3) return 1;
-    int64_t n = (longest + part - 1) / part;
-    const int64_t most = (int64_t)p.sm_count * kPartialRows / ((int64_t)total_new * p.desc.n_heads);
-    if (n > most) n = most;
-    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
+    const int64_t G = p.desc.n_heads / p.desc.n_kv_heads, row_heads = (int64_t)total_new * p.desc.n_heads;
+    const int64_t blocks = (total_new * G + kPrRows - 1) / kPrRows * p.desc.n_kv_heads, sms = p.sm_count;
+    const float longest = (float)max_len / kPrKeys, shortest = (float)(max_len - max_new) / kPrKeys;
+    const float even = 0.5f * (longest + shortest) * blocks / sms;
+    int best = 1;
+    float least = INFINITY;
+    for (int n = 1; n <= kMaxSplits; ++n) {
+        if (n > 1 && n * row_heads > sms * kPartialRows) break;
+        const float waves = (float)((blocks * n + sms - 1) / sms);
+        float us = 1.6f * std::max({longest / n, waves * shortest / n, even}) + 8.0f * waves;
+        if (n > 1) us += 6.0f + 0.9e-6f * 4 * (p.desc.head_dim + 2) * n * row_heads;
+        if (us < least) {
+            least = us;
+            best = n;
+        }
+    }
+    return best;
 }
 
 // Column tiles of 8 rows in a row group of the few-row kernel: the fewest that hold a sequence's rows,
