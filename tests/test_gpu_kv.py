@@ -646,3 +646,24 @@ def test_another_stream_and_a_graph(n):
     assert all(torch.equal(x, y) for x, y in zip((out, lse, acc, lens), got))
     assert not torch.equal(got[0], want[0])
     assert d.status() == si.SI_OK
+
+
+@pytest.mark.parametrize("lens,news", [([2600, 900], [2600, 900]), ([6000], [150]), ([4000, 31, 2500], [4, 1, 3])],
+                         ids=["prompts", "chunk", "steps"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_every_repetition_gives_the_same_bits(code, dim, lens, news):
+    """Warps and CTAs meet in another order each time; the sums keep theirs."""
+    shape = Shape(8, 2, dim, 32, code, "bf16")
+    c = ref.make_cache(shape, lens, news, seed=dim)
+    d = Dev(c)
+    _, qd = make_q(c, 4)
+    want = None
+    for _ in range(40):
+        out, lse = d.attend(qd, dim ** -0.5)
+        acc = torch.zeros((len(lens), 2, max(lens)), device=DEV)
+        si.si_kv_weigh(d.plan, d.cache, d.batch, qd, lse, None, acc, 1.0, dim ** -0.5, d.scratch)
+        if want is None:
+            want = (out, lse, acc)
+        assert all(torch.equal(x, y) for x, y in zip((out, lse, acc), want))
+    assert d.status() == si.SI_OK
