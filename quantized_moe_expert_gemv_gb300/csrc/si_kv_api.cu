@@ -42,14 +42,13 @@ si_status check_bounds(int32_t n_seqs, int32_t total_new, int32_t max_new, int32
     return SI_OK;
 }
 
-si_status check_cache(const Plan &p, const si_kv_cache *c) {
+si_status check_cache(const si_kv_cache *c) {
     if (!c || !c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail)
         return SI_ERR_INVALID_ARG;
     if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->n_slots < 1) return SI_ERR_INVALID_ARG;
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) ||
         !aligned(c->k_tail, 16) || !aligned(c->v_tail, 16))
         return SI_ERR_MISALIGNED;
-    (void)p;
     return SI_OK;
 }
 
@@ -182,7 +181,7 @@ si_status si_kv_append(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
                        const si_kv_rows *v, int32_t *lens_out, void *scratch, size_t scratch_bytes,
                        si_stream_t stream) {
     if (!plan || !lens_out) return SI_ERR_INVALID_ARG;
-    SI_KV_TRY(check_cache(plan->p, cache));
+    SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, true));
     SI_KV_TRY(check_rows(plan->p, k, false));
     SI_KV_TRY(check_rows(plan->p, v, false));
@@ -197,7 +196,7 @@ si_status si_kv_append(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
 si_status si_kv_read(si_kv_plan_t plan, const si_kv_cache *cache, const int32_t *pages, int32_t n, void *k_out,
                      void *v_out, void *scratch, size_t scratch_bytes, si_stream_t stream) {
     if (!plan || n < 0 || (n > 0 && (!pages || !k_out || !v_out))) return SI_ERR_INVALID_ARG;
-    SI_KV_TRY(check_cache(plan->p, cache));
+    SI_KV_TRY(check_cache(cache));
     if (!aligned(pages, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return SI_ERR_MISALIGNED;
     SI_KV_TRY(check_scratch(plan->p, nullptr, scratch, scratch_bytes));
     if (n == 0) return SI_OK;
@@ -210,7 +209,7 @@ si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
                        const si_kv_rows *out, float *lse, float sm_scale, void *scratch, size_t scratch_bytes,
                        si_stream_t stream) {
     if (!plan || !(sm_scale >= 0.0f) || !std::isfinite(sm_scale)) return SI_ERR_INVALID_ARG;
-    SI_KV_TRY(check_cache(plan->p, cache));
+    SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, true));
     SI_KV_TRY(check_rows(plan->p, q, false));
     SI_KV_TRY(check_rows(plan->p, out, true));
@@ -226,7 +225,7 @@ si_status si_kv_weigh(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_b
                       float sm_scale, void *scratch, size_t scratch_bytes, si_stream_t stream) {
     if (!plan || !lse || !acc_out || !(sm_scale >= 0.0f) || !std::isfinite(sm_scale) || !std::isfinite(decay))
         return SI_ERR_INVALID_ARG;
-    SI_KV_TRY(check_cache(plan->p, cache));
+    SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, true));
     SI_KV_TRY(check_rows(plan->p, q, false));
     if (acc_stride < batch->max_len) return SI_ERR_INVALID_ARG;
@@ -247,7 +246,7 @@ si_status si_kv_evict(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_b
                       void *scratch, size_t scratch_bytes, si_stream_t stream) {
     if (!plan || !acc_in || !acc_out || !new_table || !keep || !lens_out) return SI_ERR_INVALID_ARG;
     if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget) return SI_ERR_INVALID_ARG;
-    SI_KV_TRY(check_cache(plan->p, cache));
+    SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, false));
     if (batch->max_len / plan->p.desc.page_tokens > SI_KV_MAX_EVICT_PAGES) return SI_ERR_UNSUPPORTED;
     if (acc_stride < batch->max_len) return SI_ERR_INVALID_ARG;

@@ -11,7 +11,11 @@
 // than one page), so these writes come after that CTA's own reads, and no
 // other CTA reads the ring.
 // Bound: HBM (2 bytes in, 1 byte out for each value of a completed page); a
-// decode step completes few pages and is bound by latency.
+// decode step completes few pages and is bound by latency (9 us with the launch
+// from Python).  Maxima and conversions are packed, four values an instruction or
+// two: with one value at a time the issue slots bounded it (74 us for what takes 56).
+// Measured: 5 prompts of 1500 to 7000 tokens, 8 heads of 128, then their pages read back,
+// 56 us together, 80 % of the copy rate.
 #include "si_kv_mma.cuh"
 
 namespace si {

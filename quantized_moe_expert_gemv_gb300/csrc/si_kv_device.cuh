@@ -60,14 +60,6 @@ __device__ __forceinline__ int64_t ring_at(const Ctx &c, int slot, int h, int t)
 }
 
 // ------------------------------------------------------------------ 16-bit values
-template <int DT>
-__device__ __forceinline__ float to_float(uint16_t v) {
-    return DT == SI_KV_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
-}
-template <int DT>
-__device__ __forceinline__ uint16_t from_float(float v) {
-    return DT == SI_KV_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
 // Two values, the first in the low half.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

@@ -161,21 +161,21 @@ struct PieceCopy {
     __device__ __forceinline__ void run(uint32_t to, const uint8_t *src) const {
         if constexpr (D == 64) {
             cp_async16<OFF, 0>(to + at[0], src);
-            cp_async16<OFF + 8 * 64, 512>(to + at[0], src);
+            cp_async16<OFF + 8 * 64, 1 * 512>(to + at[0], src);
         } else if constexpr (D == 128) {
             cp_async16<OFF, 0>(to + at[0], src);
-            cp_async16<OFF, 512>(to + at[1], src);
-            cp_async16<OFF + 8 * 128, 1024>(to + at[0], src);
-            cp_async16<OFF + 8 * 128, 1536>(to + at[1], src);
+            cp_async16<OFF, 1 * 512>(to + at[1], src);
+            cp_async16<OFF + 8 * 128, 2 * 512>(to + at[0], src);
+            cp_async16<OFF + 8 * 128, 3 * 512>(to + at[1], src);
         } else {
             cp_async16<OFF, 0>(to + at[0], src);
-            cp_async16<OFF, 512>(to + at[1], src);
-            cp_async16<OFF, 1024>(to + at[2], src);
-            cp_async16<OFF, 1536>(to + at[3], src);
-            cp_async16<OFF + 8 * 256, 2048>(to + at[0], src);
-            cp_async16<OFF + 8 * 256, 2560>(to + at[1], src);
-            cp_async16<OFF + 8 * 256, 3072>(to + at[2], src);
-            cp_async16<OFF + 8 * 256, 3584>(to + at[3], src);
+            cp_async16<OFF, 1 * 512>(to + at[1], src);
+            cp_async16<OFF, 2 * 512>(to + at[2], src);
+            cp_async16<OFF, 3 * 512>(to + at[3], src);
+            cp_async16<OFF + 8 * 256, 4 * 512>(to + at[0], src);
+            cp_async16<OFF + 8 * 256, 5 * 512>(to + at[1], src);
+            cp_async16<OFF + 8 * 256, 6 * 512>(to + at[2], src);
+            cp_async16<OFF + 8 * 256, 7 * 512>(to + at[3], src);
         }
     }
 };

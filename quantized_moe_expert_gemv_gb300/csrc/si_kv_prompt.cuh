@@ -11,12 +11,20 @@
 // Roles: warps 0-3 and 4-7 are the softmax of the two row tiles, a thread a row;
 // warps 8-11 turn codes into fp16 tiles in shared memory (K with d innermost, V
 // with d innermost too: the second product takes V as its transposed operand);
-// warps 12 and 13 issue the two row tiles'
-// products; warp 14 looks up pages and scales ahead (warp 15 only lends its registers).  While one row tile's products run,
-// the other's softmax does.
+// warps 12 and 13 issue the two row tiles' products; warp 14 looks up pages and
+// scales ahead (warp 15 only lends its registers).  While one row tile's products
+// run, the other's softmax does.
 // Bound: at D = 128 a pair of row tiles and 128 keys takes 2048 cycles of the
-// tensor cores and 2048 of the exponential unit (256 x 128 at 16 a cycle), so
-// the two have to overlap; at D = 64 the exponential alone bounds it.
+// tensor cores (32 steps of 128 x 128 x 16, 64 cycles each) beside 1024 of the
+// exponential unit (256 x 128 at 32 a cycle) and the tiles' making, 64 KB written to
+// shared memory that the products then read; it takes about 3000, the rest being
+// the chain from a score to its weight.  At D = 64 the exponential and the products
+// are equal.
+// Two row tiles a CTA: every K and V tile is made once for 256 rows; with 128 rows
+// the making (2 x 128 x D codes) alone would take as long as the products.
+// Measured (head_dim 128): prompts of 3500 and 4000 tokens, 32/4 heads, 235 us, 49 %
+// of the measured dense rate (causal products only); 1024 tokens behind 24000,
+// 32/8 heads, 306 to 350 us, 62 to 70 %.
 #pragma once
 #include "si_kv_decode.cuh"
 #include "si_kv_tc.cuh"
@@ -98,7 +106,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     if (rb < 0) return;
     const int old = s.len - s.n, paged = s.len & ~(c.P - 1);
     const int rows = min(kPrRows, s.n * c.G - rb * kPrRows);
-    int t_from[2], t_to[2];  // key tiles of the two row tiles
+    int t_to[2];  // where the two row tiles' key tiles end
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int last = rb * kPrRows + min(rows, 128 * (x + 1)) - 1;
@@ -108,10 +116,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
     const int nt_all = max(t_to[0], t_to[1]);
     const int t_first = (int)((int64_t)nt_all * split / a.splits), t_last = (int)((int64_t)nt_all * (split + 1) / a.splits);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        t_from[x] = t_first;
-        t_to[x] = max(t_first, min(t_to[x], t_last));
-    }
+    for (int x = 0; x < 2; ++x) t_to[x] = max(t_first, min(t_to[x], t_last));
     const int nt = max(t_to[0], t_to[1]) - t_first;  // tiles of this CTA
     const int ntx[2] = {t_to[0] - t_first, t_to[1] - t_first};
 
