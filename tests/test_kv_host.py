@@ -192,7 +192,7 @@ def host_lib(tmp_path_factory):
     csrc = os.path.join(ROOT, "quantized_moe_expert_gemv_gb300", "csrc")
     cuda = os.path.dirname(os.path.dirname(build._nvcc()))
     so = str(d / "libkvhost.so")
-    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", csrc, "-I", os.path.join(cuda, "include"), "-o", so,
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", csrc, "-I", os.path.join(cuda, "include"), "-o", so,
                     str(d / "stubs.cc"), "-x", "c++", os.path.join(csrc, "si_kv_api.cu")], check=True)
     lib = ctypes.CDLL(so)
     binding._declare_kv(lib)
