@@ -290,6 +290,33 @@ struct WeighWindowCfg {
 };
 enum WindowBar { kXbQ = 0, kXbKFull = 1, kXbKEmpty = 3, kXbSFull = 5, kXbSEmpty = 7, kXbNever = 9 };
 
+// 128 columns of a lane's token: 2^(kf S - lse), added up.  MASK: columns below r_min see nothing of it.
+template <bool MASK>
+__device__ __forceinline__ void window_sums(uint32_t ts, const float4 *rl, f32x2 kf2, int r_min, f32x2 &sum, f32x2 &sum1) {
+    uint32_t z[2][32];
+    tc::tmem_ld32(ts, z[0]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        tc::tmem_wait_ld();
+        if (e < 3) tc::tmem_ld32(ts + 32 * e + 32, z[(e + 1) & 1]);
+        const uint32_t(&y)[32] = z[e & 1];
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const float4 l = rl[8 * e + k / 4];
+            float w[4];
+            up2(fma2(pk2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), kf2, pk2(l.x, l.y)), w[0], w[1]);
+            up2(fma2(pk2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), kf2, pk2(l.z, l.w)), w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = ex2(w[i]);
+                if (MASK && 32 * e + k + i < r_min) w[i] = 0.0f;
+            }
+            sum = add2(sum, pk2(w[0], w[1]));
+            sum1 = add2(sum1, pk2(w[2], w[3]));
+        }
+    }
+}
+
 // Tiles of 128 tokens of a sequence (the unfinished page is in the last).
 __device__ __forceinline__ int window_tiles(int len) { return (len + kTileRows - 1) / kTileRows; }
 
@@ -453,30 +480,10 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                     const f32x2 kf2 = pk2(kf, kf);
                     const int r0 = q * 256 + 128 * x;
                     const float4 *rl = reinterpret_cast<const float4 *>(lse_s + r0);
-                    const bool all = __all_sync(0xffffffffu, r0 >= r_min);
-                    uint32_t z[2][32];
-                    tc::tmem_ld32(ts + (q & 1) * 256, z[0]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        tc::tmem_wait_ld();
-                        if (e < 3)
-                            tc::tmem_ld32(ts + (q & 1) * 256 + 32 * e + 32, z[(e + 1) & 1]);
-                        const uint32_t(&y)[32] = z[e & 1];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 l = rl[8 * e + k / 4];
-                            float w[4];
-                            up2(fma2(pk2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), kf2, pk2(l.x, l.y)), w[0], w[1]);
-                            up2(fma2(pk2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), kf2, pk2(l.z, l.w)), w[2], w[3]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                w[i] = ex2(w[i]);
-                                if (!all && r0 + 32 * e + k + i < r_min) w[i] = 0.0f;
-                            }
-                            sum = add2(sum, pk2(w[0], w[1]));
-                            sum1 = add2(sum1, pk2(w[2], w[3]));
-                        }
-                    }
+                    if (__all_sync(0xffffffffu, r0 >= r_min))
+                        window_sums<false>(ts + (q & 1) * 256, rl, kf2, 0, sum, sum1);
+                    else
+                        window_sums<true>(ts + (q & 1) * 256, rl, kf2, r_min - r0, sum, sum1);
                     tc::fence_before_sync();
                     mbar_arrive(bar(kXbSEmpty + (q & 1)));
                 }
