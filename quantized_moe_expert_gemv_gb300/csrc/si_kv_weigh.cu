@@ -12,9 +12,9 @@
 // heads, 39 us, 64 % of the copy rate (a unit is two chains long and short of loads).
 // A window of rows (k_kv_weigh_window, 65 to 512, head_dim 64 and 128): bound by
 // the exponential (32 a cycle and SM) and the products.  S^T = K Q^T on the tcgen05
-// tensor cores, 128 tokens by 256 rows; all of q's rows stay in shared memory while
+// tensor cores, 128 tokens by 128 rows; all of q's rows stay in shared memory while
 // the CTA's share of a kv head's tokens goes by, and a thread holds one token's sum
-// and walks half of the block's columns in tensor memory.  Measured: 512 rows a kv
+// and walks every other block's columns in tensor memory.  Measured: 512 rows a kv
 // head over 4 sequences of 9000 to 16000 tokens, 4 kv heads of 128, 51 us, where the
 // products alone need 14.
 // Many rows (k_kv_weigh_many): one CTA for 128 tokens, whose K tile stays while
@@ -288,7 +288,7 @@ struct WeighWindowCfg {
     static constexpr int bars = part + 2 * 128 * 4;
     static constexpr int smem = bars + 16 * 8 + 1024;
 };
-enum WindowBar { kXbQ = 0, kXbKFull = 1, kXbKEmpty = 3, kXbSFull = 5, kXbSEmpty = 7, kXbNever = 9 };
+enum WindowBar { kXbQ = 0, kXbKFull = 1, kXbKEmpty = 3, kXbSFull = 5, kXbSEmpty = 9, kXbNever = 13 };
 
 // 128 columns of a lane's token: 2^(kf S - lse), added up.  MASK: columns below r_min see nothing of it.
 template <bool MASK>
@@ -346,8 +346,10 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kXbKFull + i), 128);
             mbar_init(bar(kXbKEmpty + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kXbSFull + i), 1);
-            mbar_init(bar(kXbSEmpty + i), 256);
+            mbar_init(bar(kXbSEmpty + i), 128);
         }
         mbar_init(bar(kXbNever), 1);
         fence_mbar_init();
@@ -371,7 +373,8 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
     };
 
     // Every role walks the same segments (a run of one kv head's tiles), tiles (numbered over all of them) and
-    // blocks of 256 rows; a tile's blocks are those with a row that sees its first key.
+    // blocks of 128 rows, each with a quarter of the tensor memory; a tile's blocks are those with a row that sees
+    // its first key.  Warps 0-3 take the even blocks, warps 4-7 the odd ones.
     int seq = share.b;
     long long off = share.off, u = share.begin;
     int tile_no = 0, seg_no = 0;
@@ -403,14 +406,15 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
         }
         return false;
     };
-    auto first_block = [&](const Place &p, int t) { return max(0, t * kTileRows - p.old) * c.G / 256; };
-    int s_use[2] = {0, 0};  // uses of each block's S so far
+    auto first_block = [&](const Place &p, int t) { return max(0, t * kTileRows - p.old) * c.G / 128; };
+    auto blocks_of = [&](const Place &p) { return (p.rows + 127) / 128; };
+    uint32_t s_use = 0;  // a bit a quarter: its uses so far are odd
     Place p;
 
     if (warp < 8) {
-        // ================================================= q, then a thread a key and half of a block's rows
+        // ================================================= q, then a thread a key and half of the blocks
         const int x = warp >> 2, ch = tid & 3;
-        const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * x;
+        const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         while (next(p)) {
             // the rows' values times one power of two (a score is off by less than 2^-32 of the block's largest),
             // a row that is not finite as zeros with the lse NaN
@@ -418,52 +422,67 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
             auto row_ptr = [&](int r) -> const uint16_t * {
                 return a.q.p + (p.s.row0 + r / c.G) * a.q.row + (p.h * c.G + r % c.G) * a.q.head;
             };
-            uint32_t top = 0;
-            for (int k = 0; k < passes; ++k) {
-                const int r = 64 * k + (tid >> 2);
-                RowLoad<D> v;
-                v.load(r < p.rows ? row_ptr(r) : a.q.p, r < p.rows, ch);
-                float m = 0.0f;
+            uint32_t top = 0, fine = 0;  // a bit a pass
+            auto place = [&](int r, int q, int e) {
+                const int unit = 2 * (ch + 4 * q) + e;
+                return base + (r >> 8) * Cfg::block + (unit >> 3) * 32768 + (r & 255) * 128 + (((unit ^ r) & 7) << 4);
+            };
+            // the values as they are into their places, four passes' loads under way, and the largest ...
+            for (int k0 = 0; k0 < passes; k0 += 4) {
+                RowLoad<D> v[4];
+                float l[4];
 #pragma unroll
-                for (int q = 0; q < D / 64; ++q) m = fmaxf(m, fmaxf(amax8(v.y[q][0], bf16), amax8(v.y[q][1], bf16)));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                if (m <= 3.4e38f) top = max(top, __float_as_uint(m));
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 64 * (k0 + k) + (tid >> 2);
+                    v[k].load(r < p.rows ? row_ptr(r) : a.q.p, r < p.rows, ch);
+                    l[k] = ch == 0 && r < p.rows
+                               ? __ldg(a.lse + (int64_t)(p.s.row0 + r / c.G) * c.H + p.h * c.G + r % c.G) : INFINITY;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 64 * (k0 + k) + (tid >> 2);
+                    float m = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < D / 64; ++q)
+                        m = fmaxf(m, fmaxf(amax8(v[k].y[q][0], bf16), amax8(v[k].y[q][1], bf16)));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    if (m <= 3.4e38f) {
+                        top = max(top, __float_as_uint(m));
+                        fine |= 1u << (k0 + k);
+                    }
+#pragma unroll
+                    for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            sts128(place(r, q, e), v[k].y[q][e].x, v[k].y[q][e].y, v[k].y[q][e].z, v[k].y[q][e].w);
+                    if (ch == 0)  // (a row that pads weighs nothing)
+                        lse_s[r] = m <= 3.4e38f ? -l[k] * kLog2e : __int_as_float(0x7fc00000);
+                }
             }
             for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (lane == 0) atomicMax(&s_top, top);  // (a maximum: the order does not matter)
             softmax_sync();
+            // ... then each thread's own places scaled
             float mul, f;
             row_scale(__uint_as_float(s_top), mul, f);
             for (int k = 0; k < passes; ++k) {
                 const int r = 64 * k + (tid >> 2);
-                RowLoad<D> v;
-                v.load(r < p.rows ? row_ptr(r) : a.q.p, r < p.rows, ch);
-                float m = 0.0f;
-#pragma unroll
-                for (int q = 0; q < D / 64; ++q) m = fmaxf(m, fmaxf(amax8(v.y[q][0], bf16), amax8(v.y[q][1], bf16)));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const bool fine = m <= 3.4e38f;
+                const float by = fine >> k & 1 ? mul : 0.0f;
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int unit = 2 * (ch + 4 * q) + e;
-                        sts128(base + (r >> 8) * Cfg::block + (unit >> 3) * 32768 + (r & 255) * 128 + (((unit ^ r) & 7) << 4),
-                               scale2(v.y[q][e].x, fine ? mul : 0.0f, bf16), scale2(v.y[q][e].y, fine ? mul : 0.0f, bf16),
-                               scale2(v.y[q][e].z, fine ? mul : 0.0f, bf16), scale2(v.y[q][e].w, fine ? mul : 0.0f, bf16));
+                        const uint4 y = *reinterpret_cast<const uint4 *>(at + (place(r, q, e) - base));
+                        sts128(place(r, q, e), scale2(y.x, by, bf16), scale2(y.y, by, bf16), scale2(y.z, by, bf16),
+                               scale2(y.w, by, bf16));
                     }
-                if (ch == 0)  // (a row that pads weighs nothing)
-                    lse_s[r] = r >= p.rows ? -INFINITY
-                               : fine      ? -a.lse[(int64_t)(p.s.row0 + r / c.G) * c.H + p.h * c.G + r % c.G] * kLog2e
-                                           : __int_as_float(0x7fc00000);
             }
             tc::fence_proxy_async_smem();
             softmax_sync();
             if (tid == 0) s_top = 0;  // (read by everyone; its next use is a barrier away)
             mbar_arrive(bar(kXbQ));
-            const int blocks = (p.rows + 255) / 256;
+            const int blocks = blocks_of(p);
             const float scale = f * a.scale2;
             // (a warp whose wait ran out goes on through the tiles, without waits, for the barriers' sake)
             for (int t = p.first; t < p.end; ++t, ++tile_no) {
@@ -472,20 +491,22 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                 const float was = x == 0 && a.acc_in && token < p.old ? a.decay * a.acc_in[acc_at] : 0.0f;
                 f32x2 sum = pk2(0.0f, 0.0f), sum1 = sum;
                 float kf = 0.0f;
-                for (int q = first_block(p, t); q < blocks; ++q) {
-                    const int n = q & 1 ? s_use[1]++ : s_use[0]++;
-                    if (!wait(kXbSFull + (q & 1), n & 1)) break;
+                int q = first_block(p, t);
+                for (q += (q ^ x) & 1; q < blocks; q += 2) {
+                    const int quarter = q & 3;
+                    if (!wait(kXbSFull + quarter, s_use >> quarter & 1)) break;
+                    s_use ^= 1u << quarter;
                     tc::fence_after_sync();
                     kf = keyf[(tile_no & 3) * 128 + (tid & 127)] * scale;
                     const f32x2 kf2 = pk2(kf, kf);
-                    const int r0 = q * 256 + 128 * x;
+                    const int r0 = q * 128;
                     const float4 *rl = reinterpret_cast<const float4 *>(lse_s + r0);
                     if (__all_sync(0xffffffffu, r0 >= r_min))
-                        window_sums<false>(ts + (q & 1) * 256, rl, kf2, 0, sum, sum1);
+                        window_sums<false>(ts + quarter * 128, rl, kf2, 0, sum, sum1);
                     else
-                        window_sums<true>(ts + (q & 1) * 256, rl, kf2, r_min - r0, sum, sum1);
+                        window_sums<true>(ts + quarter * 128, rl, kf2, r_min - r0, sum, sum1);
                     tc::fence_before_sync();
-                    mbar_arrive(bar(kXbSEmpty + (q & 1)));
+                    mbar_arrive(bar(kXbSEmpty + quarter));
                 }
                 float s0, s1;
                 up2(add2(sum, sum1), s0, s1);
@@ -557,28 +578,29 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
             if (!ok) break;
         }
     } else {
-        // ================================================= the products: 128 keys by 256 rows
-        constexpr uint32_t id = tc::idesc_f16_f32(128, 256);
+        // ================================================= the products: 128 keys by 128 rows
+        constexpr uint32_t id = tc::idesc_f16_f32(128, 128);
         const uint64_t k_desc = tc::sdesc_sw128(base + Cfg::k), q_desc = tc::sdesc_sw128(base);
         if (a.fault) wait(kXbNever, 0);
         while (ok && next(p)) {
             if (!wait(kXbQ, seg_no & 1)) break;
-            const int blocks = (p.rows + 255) / 256;
+            const int blocks = blocks_of(p);
             for (int t = p.first; t < p.end; ++t, ++tile_no) {
                 const int st = tile_no & 1;
                 if (!wait(kXbKFull + st, (tile_no >> 1) & 1)) break;
                 tc::fence_after_sync();
                 const uint64_t kd = k_desc + (st * Cfg::tile >> 4);
                 for (int q = first_block(p, t); q < blocks; ++q) {
-                    const int n = q & 1 ? s_use[1]++ : s_use[0]++;
-                    if (n > 0 && !wait(kXbSEmpty + (q & 1), (n - 1) & 1)) break;
+                    const int quarter = q & 3;
+                    if (!wait(kXbSEmpty + quarter, ~s_use >> quarter & 1)) break;  // (the first use waits for nothing)
+                    s_use ^= 1u << quarter;
                     tc::fence_after_sync();
-                    const uint64_t qd = q_desc + (q * Cfg::block >> 4);
+                    const uint64_t qd = q_desc + ((q >> 1) * Cfg::block + (q & 1) * 128 * 128 >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + (q & 1) * 256, kd + ((k >> 2) * (16384 >> 4) + (k & 3) * 2),
+                        mma_ss(tmem + quarter * 128, kd + ((k >> 2) * (16384 >> 4) + (k & 3) * 2),
                                qd + ((k >> 2) * (32768 >> 4) + (k & 3) * 2), id, k > 0);
-                    mma_done(bar(kXbSFull + (q & 1)));
+                    mma_done(bar(kXbSFull + quarter));
                 }
                 if (!ok) break;
                 mma_done(bar(kXbKEmpty + st));
