@@ -720,6 +720,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 float2 *ml = reinterpret_cast<float2 *>(smem);  // [n][rows] maximum, sum; then the part's factor
                 float *top_sum = s_part[0];
                 auto at_of = [&](int k) { return k / (D / 4) * D + k % (D / 4) * 4; };
+                // the sums of this thread's first place, eight parts: on their way beside the maxima
+                float4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    v[q] = q < n && tid < rows * (D / 4)
+                               ? __ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + at_of(tid))) : make_float4(0, 0, 0, 0);
                 for (int k = tid; k < n * rows; k += THREADS)
                     ml[k] = __ldcg(reinterpret_cast<const float2 *>(slot_of(first + k / rows * step) + R * D) + k % rows);
                 __syncthreads();
@@ -745,8 +751,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                         x.z = fmaf(v.z, f, x.z);
                         x.w = fmaf(v.w, f, x.w);
                     };
+                    int q0 = 0;
+                    if (k == tid) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (q < n) add(v[q], q);
+                        q0 = 8;
+                    }
 #pragma unroll 8
-                    for (int q = 0; q < n; ++q) add(__ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + at_of(k))), q);
+                    for (int q = q0; q < n; ++q) add(__ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + at_of(k))), q);
                     if (last)
                         store(r, d, x, top_sum[2 * r + 1]);
                     else
@@ -760,9 +773,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 }
             };
             auto arrive = [&](int32_t *counter, int n) {  // whether this CTA is the last of n
-                __threadfence();
                 __syncthreads();
                 if (tid == 0) {
+                    __threadfence();  // (the CTA's writes, which the barrier has put before)
                     const int k = atomicAdd(counter, 1);
                     s_last = k == n - 1;
                     if (s_last) *counter = 0;
