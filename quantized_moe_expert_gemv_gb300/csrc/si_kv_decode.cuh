@@ -717,8 +717,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             const bool two = nc > 2 * kJoinGroup;
             // `n` parts from part `first`, `step` apart, joined: onto part `first`, or into the result
             auto join = [&](int first, int n, int step, bool last) {
-                float2 *ml = reinterpret_cast<float2 *>(smem);  // [n][rows] maximum, sum; then the part's factor
-                float *top_sum = s_part[0];
+                float2 *ml = reinterpret_cast<float2 *>(smem);  // [n][rows] maximum, sum
                 auto at_of = [&](int k) { return k / (D / 4) * D + k % (D / 4) * 4; };
                 // the sums of this thread's first place, eight parts: on their way beside the maxima
                 float4 v[8];
@@ -729,23 +728,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 for (int k = tid; k < n * rows; k += THREADS)
                     ml[k] = __ldcg(reinterpret_cast<const float2 *>(slot_of(first + k / rows * step) + R * D) + k % rows);
                 __syncthreads();
-                if (tid < rows) {
-                    float top = kNoScore, sum = 0.0f;
-                    for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k * rows + tid].x);
-                    for (int k = 0; k < n; ++k) {
-                        const float f = ex2(ml[k * rows + tid].x - top);
-                        sum = fmaf(ml[k * rows + tid].y, f, sum);
-                        ml[k * rows + tid].x = f;
-                    }
-                    top_sum[2 * tid] = top;
-                    top_sum[2 * tid + 1] = sum;
-                }
-                __syncthreads();
+                auto top_of = [&](int r) {
+                    float top = kNoScore;
+#pragma unroll 8
+                    for (int q = 0; q < n; ++q) top = fmaxf(top, ml[q * rows + r].x);
+                    return top;
+                };
                 for (int k = tid; k < rows * (D / 4); k += THREADS) {
                     const int r = k / (D / 4), d = k % (D / 4) * 4;
+                    // (every thread forms its row's maximum and sum itself: no barrier, nothing in turn)
+                    const float top = top_of(r);
+                    float sum = 0.0f;
                     float4 x = make_float4(0, 0, 0, 0);
                     auto add = [&](const float4 &v, int q) {
-                        const float f = ml[q * rows + r].x;
+                        const float f = ex2(ml[q * rows + r].x - top);
+                        sum = fmaf(ml[q * rows + r].y, f, sum);
                         x.x = fmaf(v.x, f, x.x);
                         x.y = fmaf(v.y, f, x.y);
                         x.z = fmaf(v.z, f, x.z);
@@ -761,15 +758,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
 #pragma unroll 8
                     for (int q = q0; q < n; ++q) add(__ldcg(reinterpret_cast<const float4 *>(slot_of(first + q * step) + at_of(k))), q);
                     if (last)
-                        store(r, d, x, top_sum[2 * r + 1]);
+                        store(r, d, x, sum);
                     else
                         __stcg(reinterpret_cast<float4 *>(slot_of(first) + at_of(k)), x);
-                }
-                if (tid < rows) {
-                    if (last)
-                        store_lse(tid, top_sum[2 * tid], top_sum[2 * tid + 1]);
-                    else
-                        __stcg(reinterpret_cast<float2 *>(slot_of(first) + R * D) + tid, make_float2(top_sum[2 * tid], top_sum[2 * tid + 1]));
+                    if (d == 0) {
+                        if (last)
+                            store_lse(r, top, sum);
+                        else
+                            __stcg(reinterpret_cast<float2 *>(slot_of(first) + R * D) + r, make_float2(top, sum));
+                    }
                 }
             };
             auto arrive = [&](int32_t *counter, int n) {  // whether this CTA is the last of n
@@ -778,8 +775,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                     __threadfence();  // (the CTA's writes, which the barrier has put before)
                     const int k = atomicAdd(counter, 1);
                     s_last = k == n - 1;
-                    if (s_last) *counter = 0;
                     __threadfence();
+                    if (k == n - 1) *counter = 0;  // (its next use is another call's)
                 }
                 __syncthreads();
                 return s_last != 0;
