@@ -485,10 +485,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 chunk(keys.template load<3, 0>(kt), keys.template load<3, 1>(kt), 3);
             }
             uint32_t pb[R8][2];
-            if (t0 + 16 <= lim_min)
-                weights(sc, ks, ks, vs, vs, vs, t0, false, pb);
-            else
-                weights(sc, ks, ks, vs, vs, vs, t0, true, pb);
+            weights(sc, ks, ks, vs, vs, vs, t0, t0 + 16 > lim_min, pb);
             // V^T: keys 2j, 2j+1 and 2j+8, 2j+9; rows g and g + 8 of a row tile are two of this lane's run of d's
             constexpr int HW = D == 64 ? 2 : 4;  // words of a lane's run of d's (8 or 16 of each 64 or 128)
             auto values = [&](const uint32_t (&x)[4][HW], int half) {
