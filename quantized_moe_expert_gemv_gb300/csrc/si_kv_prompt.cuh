@@ -230,17 +230,27 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     row_weights<true>(z, info.k, info.v, qf, v_inv, m, see, tp, sum);
                 l2 = add2(l2, sum);
             } else {
-                float top = -INFINITY, v_top = 0.0f;
+                // (the factors of four columns a load, the largest of V's by the warp together)
+                const float4 *kf4 = reinterpret_cast<const float4 *>(kf), *vf4 = reinterpret_cast<const float4 *>(vf);
+                float top = -INFINITY, v_top;
+                {
+                    const float4 y = vf4[lane];
+                    v_top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+                    for (int o = 16; o; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
+                }
+                const int see = lim - key0;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t z[32];
                     tc::tmem_ld32(ts + 32 * q, z);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int col = 32 * q + k;
-                        if (key0 + col < lim) top = fmaxf(top, __uint_as_float(z[k]) * kf[col]);
-                        v_top = fmaxf(v_top, vf[col]);
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 f = kf4[8 * q + k / 4];
+                        const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (32 * q + k + e < see) top = fmaxf(top, __uint_as_float(z[k + e]) * fs[e]);
                     }
                 }
                 if (i > 0 && !wait(kBarO + x, (i - 1) & 1)) break;
@@ -252,16 +262,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     tc::tmem_ld32(ts + 32 * q, z);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float w[2], pp[2];
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 f = kf4[8 * q + k / 4], g = vf4[8 * q + k / 4];
+                        const float fs[4] = {f.x, f.y, f.z, f.w}, gs[4] = {g.x, g.y, g.z, g.w};
+                        float w[4], pp[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int col = 32 * q + k + e;
-                            pp[e] = key0 + col < lim ? ex2(fmaf(__uint_as_float(z[k + e]), kf[col] * qf, -m)) : 0.0f;
-                            w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (vf[col] * v_inv);
+                        for (int e = 0; e < 4; ++e) {
+                            pp[e] = 32 * q + k + e < see ? ex2(fmaf(__uint_as_float(z[k + e]), fs[e] * qf, -m)) : 0.0f;
+                            w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (gs[e] * v_inv);
                         }
                         l2 = add2(l2, pk2(pp[0], pp[1]));
+                        l2 = add2(l2, pk2(pp[2], pp[3]));
                         p[k / 2] = half2_bits(w[0], w[1]);
+                        p[k / 2 + 1] = half2_bits(w[2], w[3]);
                     }
                     tmem_st16(tp + 16 * q, p);
                 }
