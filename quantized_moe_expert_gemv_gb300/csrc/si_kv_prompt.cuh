@@ -22,9 +22,11 @@
 // are equal.
 // Two row tiles a CTA: every K and V tile is made once for 256 rows; with 128 rows
 // the making (2 x 128 x D codes) alone would take as long as the products.
-// Measured (head_dim 128): prompts of 3500 and 4000 tokens, 32/4 heads, 235 us, 49 %
+// Measured (head_dim 128): prompts of 2900 to 4100 tokens, 32/4 heads, 244 us, 48 %
 // of the measured dense rate (causal products only); 1024 tokens behind 24000,
-// 32/8 heads, 306 to 350 us, 62 to 70 %.
+// 32/8 heads, 311 us (E4M3) and 320 (int8), 69 %; one prompt of 300, 22 us, of which
+// the products are 3: the start, q and the tile with the unfinished page, whose
+// rows and factors come one by one, are the rest.
 #pragma once
 #include "si_kv_decode.cuh"
 #include "si_kv_tc.cuh"

@@ -15,12 +15,12 @@
 // tensor cores, 128 tokens by 128 rows; all of q's rows stay in shared memory while
 // the CTA's share of a kv head's tokens goes by, and a thread holds one token's sum
 // and walks every other block's columns in tensor memory.  Measured: 512 rows a kv
-// head over 4 sequences of 9000 to 16000 tokens, 4 kv heads of 128, 51 us, where the
-// products alone need 14.
+// head over 4 sequences of 9000 to 16000 tokens, 4 kv heads of 128, 38 us, where the
+// products alone need 14: q's rows into shared memory 4 us a segment (two a CTA), a
+// tile 2500 cycles of exponentials and sums (five a score and scheduler) of 3900.
 // Many rows (k_kv_weigh_many): one CTA for 128 tokens, whose K tile stays while
 // q's tiles of 128 rows follow each other through two stages; for 512 rows it
-// took 117 us where the window kernel takes less than half (most of it in a
-// CTA's start).
+// took 117 us where the window kernel takes a third (most of it in a CTA's start).
 #include "si_kv_decode.cuh"
 #include "si_kv_tc.cuh"
 
