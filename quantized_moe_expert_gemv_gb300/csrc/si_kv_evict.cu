@@ -14,7 +14,7 @@
 // Bound: HBM for the move (each kept byte read and written once); the choice reads
 // acc once and is a chain of block-wide steps.  Measured: 8 sequences of 20000 to
 // 32700 tokens, 8 heads of 128, down to 128 pages of 64: 136 us, 75 % of the copy
-// rate, with the kept pages read back (evict alone 73, of which 27 remain with a
+// rate, with the kept pages read back (evict alone 73, of which 26 remain with a
 // budget of ten pages); one of 1500 tokens 8.5 us, two launches' latency.
 #include "si_kv_device.cuh"
 
@@ -47,13 +47,9 @@ __device__ __forceinline__ int block_prefix(bool flag, int *s_warp, int &total) 
     __syncthreads();  // s_warp's earlier use is over
     if (lane == 0) s_warp[warp] = __popc(m);
     __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int w = 0; w < warps; ++w) {
-        before += w < warp ? s_warp[w] : 0;
-        total += s_warp[w];
-    }
-    return before + __popc(m & ((1u << lane) - 1));
+    const int mine = lane < warps ? s_warp[lane] : 0;
+    total = __reduce_add_sync(0xffffffffu, mine);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + __popc(m & ((1u << lane) - 1));
 }
 
 __global__ void __launch_bounds__(kChooseMost) k_kv_choose(Ctx c, const float *acc, int64_t acc_stride, int budget,
