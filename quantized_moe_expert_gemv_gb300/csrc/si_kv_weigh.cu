@@ -374,7 +374,10 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
 
     // Every role walks the same segments (a run of one kv head's tiles), tiles (numbered over all of them) and
     // blocks of 128 rows, each with a quarter of the tensor memory; a tile's blocks are those with a row that sees
-    // its first key.  Warps 0-3 take the even blocks, warps 4-7 the odd ones.
+    // its first key.  Warps 0-3 take the even blocks, warps 4-7 the odd ones.  A segment without rows is the softmax
+    // warps' alone and is in no one's count of tiles or segments: its tiles have no block whose barrier would hold them
+    // until the product warp has seen q's (two such segments in a row could pass that warp by a phase).  With rows,
+    // every tile has a block.
     int seq = share.b;
     long long off = share.off, u = share.begin;
     int tile_no = 0, seg_no = 0;
@@ -416,6 +419,14 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
         const int x = warp >> 2, ch = tid & 3;
         const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         while (next(p)) {
+            if (p.rows == 0) {  // the earlier sums' decay is all: half of the tiles for each half of the warps
+                for (int t = p.first + x; t < p.end; t += 2) {
+                    const int token = t * kTileRows + (tid & 127);
+                    const int64_t acc_at = ((int64_t)p.b * c.Hk + p.h) * a.acc_stride + token;
+                    if (token < p.s.len) a.acc_out[acc_at] = a.acc_in ? a.decay * a.acc_in[acc_at] : 0.0f;
+                }
+                continue;
+            }
             // the rows' values times one power of two (a score is off by less than 2^-32 of the block's largest),
             // a row that is not finite as zeros with the lse NaN
             const int passes = (p.rows + 255) / 256 * 4;  // of 64 rows, to the end of the last block
@@ -521,6 +532,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
         constexpr int CC = D / 64;
         const uint32_t a0 = f16_tile_at(r0, 2 * ch), a1 = f16_tile_at(r0, 2 * ch + 1);
         while (next(p)) {
+            if (p.rows == 0) continue;
             const int paged = p.s.len & ~(c.P - 1);
             const int32_t *table = c.table + (int64_t)p.b * c.table_stride;
             int pg[5];
@@ -583,6 +595,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
         const uint64_t k_desc = tc::sdesc_sw128(base + Cfg::k), q_desc = tc::sdesc_sw128(base);
         if (a.fault) wait(kXbNever, 0);
         while (ok && next(p)) {
+            if (p.rows == 0) continue;
             if (!wait(kXbQ, seg_no & 1)) break;
             const int blocks = blocks_of(p);
             for (int t = p.first; t < p.end; ++t, ++tile_no) {

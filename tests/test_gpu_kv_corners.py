@@ -1,0 +1,38 @@
+"""The 8-bit cache's operators where they can go wrong: empty rows, extreme values, loose bounds, broken neighbours."""
+import math
+
+import pytest
+import torch
+
+from quantized_moe_expert_gemv_gb300 import binding as si
+import kv_reference as ref
+from kv_reference import Shape
+from test_gpu_kv import DEV, Dev, check_attend, make_q, run_evict
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ weigh
+@pytest.mark.parametrize("code,dim,place", [("int8", 128, (63,)), ("e4m3", 64, (0,)), ("int8", 64, (31, 40)), ("e4m3", 128, (5, 6, 62))])
+def test_weigh_a_window_among_sequences_without_rows(code, dim, place):
+    """Sequences that only decay beside ones with a window of rows: a CTA takes several of the former in a row."""
+    shape = Shape(16, 8, dim, 32, code, "bf16")
+    lens = [100 + 7 * (b % 13) for b in range(64)]
+    news = [64 if b in place else 0 for b in range(64)]
+    c = ref.make_cache(shape, lens, news, seed=7)
+    d = Dev(c)
+    q, qd = make_q(c, 6)
+    sm = dim ** -0.5
+    _, lse, _, _ = ref.attend(c, q, sm)
+    lse = lse.float()
+    acc = torch.rand((64, 8, max(lens)), generator=torch.Generator().manual_seed(1))
+    want, A = ref.weigh(c, q, lse, acc, 0.75, sm)
+    for _ in range(20):
+        out = torch.full_like(acc, 9.0).to(DEV)
+        si.si_kv_weigh(d.plan, d.cache, d.batch, qd, lse.to(DEV), acc.to(DEV), out, 0.75, sm, d.scratch)
+        assert d.status() == si.SI_OK
+        got = out.cpu().double()
+        for b, L in enumerate(lens):
+            w = want[b, :, :L]
+            assert ((got[b, :, :L] - w).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * w + 1e-12).all(), b
+            assert (got[b, :, L:] == 9.0).all()
