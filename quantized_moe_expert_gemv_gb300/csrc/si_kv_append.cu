@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(Ctx c, Rows k, Row
 template <int CODE, int DT>
 static cudaError_t append_units(const Ctx &c, Rows k, Rows v, int32_t *lens_out, cudaStream_t s) {
     // a call of n rows completes at most (P - 1 + n) / P pages of a sequence
-    const int pages = max(1, (c.P - 1 + c.max_new) / c.P);
+    // (the bound on n may be any number: the tokens have to fit max_len too)
+    const int pages = max(1, (c.P - 1 + min(c.max_new, c.max_len)) / c.P);
     const int units = c.P * c.D / 16;
     const bool many = pages >= 8;  // a prompt: several pages a CTA (a step has one page at most, and the fewest registers)
     auto go = [&](auto kernel, int pg) {

@@ -36,3 +36,20 @@ def test_weigh_a_window_among_sequences_without_rows(code, dim, place):
             w = want[b, :, :L]
             assert ((got[b, :, :L] - w).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * w + 1e-12).all(), b
             assert (got[b, :, L:] == 9.0).all()
+
+
+# ------------------------------------------------------------------ loose bounds
+def test_append_with_a_loose_bound():
+    """max_new only bounds: the largest number completes the same pages as the exact one."""
+    shape = Shape(4, 2, 64, 16, "int8", "bf16")
+    g = torch.Generator().manual_seed(4)
+    kv = torch.randn((140, 4, 64), generator=g).to(torch.bfloat16).to(DEV)
+    res = []
+    for most in (100, 2 ** 31 - 1):
+        c = ref.make_cache(shape, [5, 60], [100, 40], seed=8, empty=True)
+        d = Dev(c, max_len=110, max_new=most)
+        out = torch.empty_like(d.lens)
+        si.si_kv_append(d.plan, d.cache, d.batch, kv[:, :2], kv[:, 2:], out, d.scratch)
+        assert out.tolist() == [105, 100] and d.status() == si.SI_OK
+        res.append([d.k_codes, d.v_codes, d.k_scale, d.v_scale, d.k_tail.view(torch.int16), d.v_tail.view(torch.int16)])
+    assert all(torch.equal(x, y) for x, y in zip(*res))
