@@ -1,6 +1,7 @@
 // si_kv_api.cu -- the attention block's C ABI (include/si_kv.h): plans,
 // argument checks and stream-ordered launches.  Every argument error is
 // returned before anything is launched.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -104,7 +105,7 @@ Ctx make_ctx(const Plan &p, const si_kv_cache *c, const si_kv_batch *b, void *sc
         x.table_stride = b->table_stride;
         x.B = b->n_seqs;
         x.T = b->total_new;
-        x.max_new = b->max_new;
+        x.max_new = std::min(b->max_new, b->total_new);  // (what max_new leaves open, total_new may not)
         x.max_len = b->max_len;
     }
     return x;

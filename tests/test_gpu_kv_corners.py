@@ -53,3 +53,20 @@ def test_append_with_a_loose_bound():
         assert out.tolist() == [105, 100] and d.status() == si.SI_OK
         res.append([d.k_codes, d.v_codes, d.k_scale, d.v_scale, d.k_tail.view(torch.int16), d.v_tail.view(torch.int16)])
     assert all(torch.equal(x, y) for x, y in zip(*res))
+
+
+@pytest.mark.parametrize("lens,news", [([300, 90], [100, 40]), ([300, 90], [2, 1])], ids=["prompt", "step"])
+def test_attend_and_weigh_with_a_loose_bound(lens, news):
+    """The same outputs where max_new says no more than that a sequence may have all rows, or any number."""
+    shape = Shape(8, 2, 64, 16, "int8", "bf16")
+    c = ref.make_cache(shape, lens, news, seed=8)
+    q, qd = make_q(c, 3)
+    for most in (sum(news), 2 ** 31 - 1):
+        d = Dev(c, max_new=most)
+        out, lse = d.attend(qd, 0.125)
+        check_attend(c, out, lse, q, 0.125)
+        acc = torch.zeros((2, 2, 300), device=DEV)
+        si.si_kv_weigh(d.plan, d.cache, d.batch, qd, lse, None, acc, 1.0, 0.125, d.scratch)
+        want, A = ref.weigh(c, q, lse.cpu(), None, 1.0, 0.125)
+        assert ((acc.cpu().double() - want).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * want + 1e-12).all()
+        assert d.status() == si.SI_OK

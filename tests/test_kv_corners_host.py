@@ -1,0 +1,65 @@
+"""The attention block's host code against a CUDA runtime that only records: what the launchers get, and which
+stream and device a call works on."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from quantized_moe_expert_gemv_gb300 import binding, build
+from test_kv_host import Call, host_plan
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "quantized_moe_expert_gemv_gb300", "csrc")
+
+RECORD = """
+#include "si_kv.h"
+static int g_max_new = -1;
+extern "C" {
+int last_max_new() { return g_max_new; }
+cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int) {
+    *v = a == cudaDevAttrMultiProcessorCount ? 152 : a == cudaDevAttrClockRate ? 2000000 : 232448;
+    return cudaSuccess;
+}
+cudaError_t cudaMemsetAsync(void *, int, size_t, cudaStream_t) { return cudaSuccess; }
+cudaError_t cudaMemset(void *, int, size_t) { return cudaSuccess; }
+cudaError_t cudaMemcpy(void *, const void *, size_t, cudaMemcpyKind) { return cudaSuccess; }
+cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+}
+namespace si { namespace kv {
+size_t scratch_bytes(const Plan &, int, int, int, int) { return kCtrlBytes; }
+static cudaError_t seen(const Ctx &c) { g_max_new = c.max_new; return cudaSuccess; }
+cudaError_t launch_append(const Plan &, const Ctx &c, Rows, Rows, int32_t *, cudaStream_t) { return seen(c); }
+cudaError_t launch_read(const Plan &, const Ctx &c, const int32_t *, int, uint16_t *, uint16_t *, cudaStream_t) { return seen(c); }
+cudaError_t launch_attend(const Plan &, const Ctx &c, Rows, Rows, float *, float, void *, cudaStream_t) { return seen(c); }
+cudaError_t launch_weigh(const Plan &, const Ctx &c, Rows, const float *, const float *, float *, int64_t, float, float, cudaStream_t) { return seen(c); }
+cudaError_t launch_evict(const Plan &, const Ctx &c, const float *, float *, int64_t, int, int, int, const int32_t *, const int32_t *, int32_t *, int32_t *, cudaStream_t) { return seen(c); }
+}}
+"""
+
+
+@pytest.fixture(scope="module")
+def recorder(tmp_path_factory):
+    """csrc/si_kv_api.cu (host code) linked with launchers and runtime calls that record."""
+    d = tmp_path_factory.mktemp("kv_record")
+    (d / "record.cc").write_text(RECORD)
+    cuda = os.path.dirname(os.path.dirname(build._nvcc()))
+    so = str(d / "libkvrecord.so")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", CSRC, "-I", os.path.join(cuda, "include"), "-o", so,
+                    str(d / "record.cc"), "-x", "c++", os.path.join(CSRC, "si_kv_api.cu")], check=True)
+    lib = ctypes.CDLL(so)
+    binding._declare_kv(lib)
+    return lib
+
+
+@pytest.mark.parametrize("name", ["append", "attend", "weigh"])
+def test_the_row_bound_is_what_the_others_leave(recorder, name):
+    """max_new, or total_new where that is less."""
+    plan = host_plan(recorder, 64, 1, 128, 64)
+    for total, most, want in ((6, 4, 4), (6, 2 ** 31 - 1, 6), (2 ** 25, 5, 5)):
+        call = Call(plan)
+        call.batch.total_new, call.batch.max_new = total, most
+        assert call(recorder, name) == binding.SI_OK
+        assert recorder.last_max_new() == want
+    recorder.si_kv_plan_destroy(plan.handle)
