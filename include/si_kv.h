@@ -82,7 +82,7 @@ typedef struct si_kv_cache {
 typedef struct si_kv_batch {
     int32_t n_seqs;             /* 1..SI_KV_MAX_SEQS */
     int32_t total_new;          /* rows of q, k, v, out (>= q_start[n_seqs]) */
-    int32_t max_new;            /* no sequence has more rows */
+    int32_t max_new;            /* no sequence has more rows (nor 2^30 rows times query heads of a kv head) */
     int32_t max_len;            /* no sequence has more tokens, the call's new ones counted */
     const int32_t *q_start;     /* [n_seqs + 1] first row of each sequence, ascending */
     const int32_t *lens;        /* [n_seqs] tokens in the cache (si_kv_append: before the call) */

@@ -19,6 +19,10 @@ struct si_kv_plan_s {
 
 namespace {
 
+// Rows of one sequence and kv head, query heads counted: more break a bound (SI_ERR_DEVICE).  A sequence of
+// SI_KV_MAX_LEN rows and 256 query heads for a kv head has as many.
+constexpr int32_t kMaxRowHeads = 1 << 30;
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -105,7 +109,8 @@ Ctx make_ctx(const Plan &p, const si_kv_cache *c, const si_kv_batch *b, void *sc
         x.table_stride = b->table_stride;
         x.B = b->n_seqs;
         x.T = b->total_new;
-        x.max_new = std::min(b->max_new, b->total_new);  // (what max_new leaves open, total_new may not)
+        // (what max_new leaves open, total_new may not; and the kernels number a kv head's rows in 32 bits)
+        x.max_new = std::min({b->max_new, b->total_new, kMaxRowHeads / x.G});
         x.max_len = b->max_len;
     }
     return x;

@@ -214,17 +214,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
         const int tiles = seq_tiles(c, s.len);
         return tiles == 0 ? 0ll : (long long)(tiles + kDecodeOver) * c.Hk * ((s.n * c.G + R - 1) / R);
     }, [&](int b) { return c.Hk * ((load_seq(c, b).n * c.G + R - 1) / R); }, kDecodeOver + kDecodeAlone);
-    // rows whose sequence has no token at all are in no unit: zeros
-    if (share.some_empty)
-        for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
-            const Seq s = load_seq(c, b);
-            if (s.len > 0) continue;
-            for (int k = tid; k < s.n * c.H * (D / 8); k += THREADS) {
-                const int row = s.row0 + k / (c.H * (D / 8)), head = k / (D / 8) % c.H, d = k % (D / 8) * 8;
-                *reinterpret_cast<uint4 *>(a.out.p + row * a.out.row + head * a.out.head + d) = make_uint4(0, 0, 0, 0);
-                if (a.lse && d == 0) a.lse[(int64_t)row * c.H + head] = -INFINITY;
+    // rows whose sequence has no token at all are in no unit: zeros, a row a CTA at a time
+    if (share.some_empty) {
+        const int lanes = min((int)gridDim.x, c.B);  // sequences at a time
+        if (blockIdx.x < gridDim.x / lanes * lanes)
+            for (int b = blockIdx.x % lanes; b < c.B; b += lanes) {
+                const Seq s = load_seq(c, b);
+                if (s.len > 0) continue;
+                for (int i = blockIdx.x / lanes; i < s.n; i += gridDim.x / lanes)
+                    for (int k = tid; k < c.H * (D / 8); k += THREADS) {
+                        const int row = s.row0 + i, head = k / (D / 8), d = k % (D / 8) * 8;
+                        *reinterpret_cast<uint4 *>(a.out.p + row * a.out.row + head * a.out.head + d) = make_uint4(0, 0, 0, 0);
+                        if (a.lse && d == 0) a.lse[(int64_t)row * c.H + head] = -INFINITY;
+                    }
             }
-        }
+    }
     if (blockIdx.x >= share.ctas) return;
     int b = share.b;
     long long off = share.off, u = share.begin;

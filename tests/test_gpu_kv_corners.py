@@ -70,3 +70,17 @@ def test_attend_and_weigh_with_a_loose_bound(lens, news):
         want, A = ref.weigh(c, q, lse.cpu(), None, 1.0, 0.125)
         assert ((acc.cpu().double() - want).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * want + 1e-12).all()
         assert d.status() == si.SI_OK
+
+
+def test_attend_rows_without_a_token_past_32_bits():
+    """2^20 rows of 64 heads of 256 of a sequence without tokens: 2^31 pieces of 16 bytes, all zeros."""
+    n = 1 << 20
+    c = ref.make_cache(Shape(64, 64, 256, 16, "int8", "bf16"), [0, 20], [n, 1], seed=1)
+    d = Dev(c)
+    q = torch.ones((1, 64, 256), dtype=torch.bfloat16, device=DEV).expand(n + 1, 64, 256)
+    out, lse = d.attend(q, 0.06)
+    assert d.status() == si.SI_OK
+    for x, none in ((out, 0.0), (lse, -math.inf)):
+        for part in x[:n].split(1 << 17):
+            assert (part == none).all()
+    assert torch.isfinite(out[n]).all() and (out[n] != 0).any() and torch.isfinite(lse[n]).all()

@@ -55,9 +55,9 @@ def recorder(tmp_path_factory):
 
 @pytest.mark.parametrize("name", ["append", "attend", "weigh"])
 def test_the_row_bound_is_what_the_others_leave(recorder, name):
-    """max_new, or total_new where that is less."""
+    """max_new, or total_new where that is less, and never more rows than a kv head's can be numbered in 32 bits."""
     plan = host_plan(recorder, 64, 1, 128, 64)
-    for total, most, want in ((6, 4, 4), (6, 2 ** 31 - 1, 6), (2 ** 25, 5, 5)):
+    for total, most, want in ((6, 4, 4), (6, 2 ** 31 - 1, 6), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 30 // 64), (2 ** 25, 5, 5)):
         call = Call(plan)
         call.batch.total_new, call.batch.max_new = total, most
         assert call(recorder, name) == binding.SI_OK
