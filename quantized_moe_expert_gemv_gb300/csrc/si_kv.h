@@ -45,15 +45,19 @@ struct Rows {
     int64_t row, head;  // strides in elements
 };
 
-// Allow kernel F `smem` bytes of dynamic shared memory, once a device (F and smem
-// are the caller's constants; the attribute stays with the function).
+// Allow kernel F `smem` bytes of dynamic shared memory on the current device (the one that a launch goes to,
+// whatever the plan's is), once a device: F and smem are the caller's constants, and the attribute stays with
+// the function.
 template <auto F>
-cudaError_t allow_smem(const Plan &p, int smem) {
+cudaError_t allow_smem(int smem) {
     static std::atomic<unsigned long long> done{0};
-    const unsigned long long bit = 1ull << (p.device & 63);
-    if (p.device < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && p.device < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(F), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
 

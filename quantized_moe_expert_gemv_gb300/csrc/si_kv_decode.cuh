@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
 template <int CODE, int D, int R8>
 cudaError_t decode_launch(const Plan &p, const DecodeArgs &a, cudaStream_t s) {
     using Cfg = DecodeCfg<D, R8>;
-    const cudaError_t e = allow_smem<k_kv_decode<CODE, D, R8>>(p, Cfg::smem);
+    const cudaError_t e = allow_smem<k_kv_decode<CODE, D, R8>>(Cfg::smem);
     if (e != cudaSuccess) return e;
     return launch(k_kv_decode<CODE, D, R8>, dim3(p.sm_count * Cfg::ctas), Cfg::warps * 32, Cfg::smem, s, a);
 }

@@ -211,7 +211,7 @@ cudaError_t launch_evict(const Plan &p, const Ctx &c, const float *acc_in, float
                          int sink, int recent, const int32_t *new_table, const int32_t *new_slots, int32_t *keep,
                          int32_t *lens_out, cudaStream_t s) {
     const size_t smem = (size_t)(c.max_len / c.P) * sizeof(unsigned long long);
-    cudaError_t e = allow_smem<k_kv_choose>(p, SI_KV_MAX_EVICT_PAGES * (int)sizeof(unsigned long long));
+    cudaError_t e = allow_smem<k_kv_choose>(SI_KV_MAX_EVICT_PAGES * (int)sizeof(unsigned long long));
     if (e != cudaSuccess) return e;
     // as many threads as half-warps for a page, up to 1024 (a small cache's block-wide steps are quicker with few)
     const int threads = c.max_len / c.P <= 64 ? 256 : kChooseMost;

@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
 template <int CODE, int D>
 cudaError_t prompt_launch(const Plan &p, const PromptArgs &a, cudaStream_t s) {
     using Cfg = PromptCfg<D>;
-    cudaError_t e = allow_smem<k_kv_prompt<CODE, D>>(p, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_prompt<CODE, D>>(Cfg::smem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = ((int64_t)a.c.max_new * a.c.G + kPrRows - 1) / kPrRows * a.c.Hk * a.c.B * a.splits;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;

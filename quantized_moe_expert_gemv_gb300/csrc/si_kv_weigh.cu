@@ -814,14 +814,14 @@ __global__ void __launch_bounds__(kWmThreads, 2) k_kv_weigh_many(const WeighArgs
 template <int CODE, int D>
 static cudaError_t few(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighCfg<D>;
-    cudaError_t e = allow_smem<k_kv_weigh_few<CODE, D>>(p, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_weigh_few<CODE, D>>(Cfg::smem);
     if (e != cudaSuccess) return e;
     return launch(k_kv_weigh_few<CODE, D>, dim3(p.sm_count * Cfg::ctas), Cfg::warps * 32, Cfg::smem, s, a);
 }
 template <int CODE, int D>
 static cudaError_t many(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighManyCfg<D>;
-    cudaError_t e = allow_smem<k_kv_weigh_many<CODE, D>>(p, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_weigh_many<CODE, D>>(Cfg::smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((a.c.max_len + kTileRows - 1) / kTileRows, a.c.Hk, a.c.B);
     return launch(k_kv_weigh_many<CODE, D>, grid, kWmThreads, Cfg::smem, s, a);
@@ -829,7 +829,7 @@ static cudaError_t many(const Plan &p, const WeighArgs &a, cudaStream_t s) {
 template <int CODE, int D>
 static cudaError_t window(const Plan &p, const WeighArgs &a, cudaStream_t s) {
     using Cfg = WeighWindowCfg<D>;
-    cudaError_t e = allow_smem<k_kv_weigh_window<CODE, D>>(p, Cfg::smem);
+    cudaError_t e = allow_smem<k_kv_weigh_window<CODE, D>>(Cfg::smem);
     if (e != cudaSuccess) return e;
     return launch(k_kv_weigh_window<CODE, D>, dim3(p.sm_count), kWwThreads, Cfg::smem, s, a);
 }

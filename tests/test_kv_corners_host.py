@@ -63,3 +63,35 @@ def test_the_row_bound_is_what_the_others_leave(recorder, name):
         assert call(recorder, name) == binding.SI_OK
         assert recorder.last_max_new() == want
     recorder.si_kv_plan_destroy(plan.handle)
+
+
+ATTRIBUTES = """
+#include "si_kv.h"
+static int g_device = 0, g_set[2] = {0, 0}, g_fail = 0;
+extern "C" {
+cudaError_t cudaGetDevice(int *d) { *d = g_device; return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int) {
+    if (g_fail) return cudaErrorInvalidValue;
+    ++g_set[g_device];
+    return cudaSuccess;
+}
+void kernel() {}
+int call(int device, int fail) { g_device = device; g_fail = fail; return (int)si::kv::allow_smem<&kernel>(100000); }
+int sets(int device) { return g_set[device]; }
+}
+"""
+
+
+def test_shared_memory_is_allowed_once_on_each_device_that_launches(tmp_path):
+    """The attribute belongs to the current device: a call on one device settles nothing for another."""
+    (tmp_path / "attributes.cc").write_text(ATTRIBUTES)
+    cuda = os.path.dirname(os.path.dirname(build._nvcc()))
+    so = str(tmp_path / "libattributes.so")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", CSRC, "-I", os.path.join(cuda, "include"), "-o", so,
+                    str(tmp_path / "attributes.cc")], check=True)
+    lib = ctypes.CDLL(so)
+    assert lib.call(1, 1) != 0 and lib.sets(1) == 0  # a failure is not remembered
+    for _ in range(3):
+        assert lib.call(0, 0) == 0
+        assert lib.call(1, 0) == 0
+    assert lib.sets(0) == lib.sets(1) == 1
