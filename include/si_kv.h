@@ -131,7 +131,9 @@ si_status si_kv_read(si_kv_plan_t plan, const si_kv_cache *cache, const int32_t 
  * out[row][h] = sum_t softmax_t(sm_scale * q[row][h] . k_t) v_t, and, where lse
  * is not NULL, lse[row][h] = log sum_t exp(sm_scale * q . k_t) ([total_new]
  * [n_heads] fp32).  A row that sees no token (lens[b] < n_b) gives zeros and
- * lse -inf.  out must not overlap q. */
+ * lse -inf.  Scores are held in 32 bits: one below their range has no weight, and
+ * a row with one above it, or with all of its scores below it, is NaN.  out
+ * must not overlap q. */
 si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_batch *batch, const si_kv_rows *q,
                        const si_kv_rows *out, float *lse, float sm_scale, void *scratch, size_t scratch_bytes,
                        si_stream_t stream);

@@ -48,7 +48,9 @@ namespace kv {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 4.0f, kWeightUnit = 2048.0f;
-constexpr float kNoScore = -1e30f;  // a running maximum before the first score
+// A running maximum before the first score: the lowest value, which any score that is a number moves (or equals).
+// What is past the range (-inf, of a score that its row sees) has no weight; a row of such scores alone is NaN.
+constexpr float kNoScore = -3.4028234663852886e38f;
 
 // R8: column tiles of 8 rows.  As many warps as the registers allow (the second product's sums are
 // D R8 / 4 a lane), then as many stages as fit 96 KB a CTA.
@@ -64,6 +66,10 @@ struct DecodeCfg {
     static constexpr int smem = ring + q_bytes;
     static_assert(warps * 8 * R8 * D * 4 <= ring, "the warps' results are joined in the ring's place");
 };
+
+// What a row's sums are multiplied by where they have no weight at all: zero for a row that sees no token (the
+// last that it sees is `last`), NaN for one whose scores are all below the range.
+__device__ __forceinline__ float no_weight(int last) { return last < 0 ? 0.0f : __int_as_float(0x7fc00000); }
 
 // Partial results in the scratch: two slots a CTA (an item that began in an
 // earlier CTA, one that goes on in a later one), each [rows][D] sums, then [rows][2]
@@ -408,8 +414,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             for (int n = 0; n < R8; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sc[n][e] *= kf0 * qf[n][e];
-                    sc[n][2 + e] *= kf1 * qf[n][e];
+                    sc[n][e] = __fmul_rn(sc[n][e], kf0 * qf[n][e]);  // (rounded, as the maximum is: see row_weights)
+                    sc[n][2 + e] = __fmul_rn(sc[n][2 + e], kf1 * qf[n][e]);
                     if (masked) {
                         if (t0 + g >= lim[n][e]) sc[n][e] = -INFINITY;
                         if (t0 + g + 8 >= lim[n][e]) sc[n][2 + e] = -INFINITY;
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
         };
         auto store = [&](int r, int d, float4 x, float sum) {
             const int rr = rb * R + r, row = s.row0 + rr / c.G, head = h * c.G + rr % c.G;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = sum == 0.0f ? no_weight(old + rr / c.G) : 1.0f / sum;
             uint2 y;
             if (bf16)
                 y = make_uint2(pack2<SI_KV_BF16>(x.x * inv, x.y * inv), pack2<SI_KV_BF16>(x.z * inv, x.w * inv));

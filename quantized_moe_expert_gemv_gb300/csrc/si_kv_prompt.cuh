@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         const uint32_t ts = tmem + lanes + kTmS, tp = tmem + lanes + kTmP + x * 64, to = tmem + lanes + kTmO + x * 128;
         float m = kNoScore, v_ref = 1e-30f, v_inv = kWeightUnit / 1e-30f;
         f32x2 l2 = pk2(0.0f, 0.0f);
+        bool far = false;  // a row of the warp has its maximum past kFar
         const int n = ntx[x];
         for (int i = 0; i < n; ++i) {
             const int key0 = (t_first + i) * kPrKeys;
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     v_ref = v_top;
                     v_inv = kWeightUnit / v_top;
                 }
+                far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != kNoScore);
                 if (i > 0) {
 #pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
@@ -222,14 +224,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 const int see = lim - key0;
                 const bool all = __all_sync(0xffffffffu, !live || see >= kPrKeys);
                 f32x2 sum;
-                const float top = (all ? row_top<false>(z, info.k, see) : row_top<true>(z, info.k, see)) * qf;
+                const float top = all ? row_top<false>(z, info.k, qf, see) : row_top<true>(z, info.k, qf, see);
                 if (i > 0 && !wait(kBarO + x, (i - 1) & 1)) break;  // P and O are free: the last second product is done
                 tc::fence_after_sync();
                 adjust(top, v_top);
-                if (all)
-                    row_weights<false>(z, info.k, info.v, qf, v_inv, m, see, tp, sum);
+                if (all && !far)
+                    row_weights<false>(z, info.k, info.v, qf, v_inv, m, far, see, tp, sum);
                 else
-                    row_weights<true>(z, info.k, info.v, qf, v_inv, m, see, tp, sum);
+                    row_weights<true>(z, info.k, info.v, qf, v_inv, m, far, see, tp, sum);
                 l2 = add2(l2, sum);
             } else {
                 // (the factors of four columns a load, the largest of V's by the warp together)
@@ -252,12 +254,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (32 * q + k + e < see) top = fmaxf(top, __uint_as_float(z[k + e]) * fs[e]);
+                            if (32 * q + k + e < see) top = fmaxf(top, __fmul_rn(__uint_as_float(z[k + e]), fs[e] * qf));
                     }
                 }
                 if (i > 0 && !wait(kBarO + x, (i - 1) & 1)) break;
                 tc::fence_after_sync();
-                adjust(top * qf, v_top);
+                adjust(top, v_top);
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t z[32], p[16];
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         float w[4], pp[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            pp[e] = 32 * q + k + e < see ? ex2(fmaf(__uint_as_float(z[k + e]), fs[e] * qf, -m)) : 0.0f;
+                            pp[e] = 32 * q + k + e < see ? ex2(__fmul_rn(__uint_as_float(z[k + e]), fs[e] * qf) - m) : 0.0f;
                             w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (gs[e] * v_inv);
                         }
                         l2 = add2(l2, pk2(pp[0], pp[1]));
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         up2(l2, l, l_odd);
         l += l_odd;
         if (ok) {
-            const float f = v_ref / kWeightUnit, inv = l == 0.0f ? 0.0f : f / l;
+            const float f = v_ref / kWeightUnit, inv = l == 0.0f ? no_weight(lim - 1) : f / l;
             if (a.splits == 1) {
                 uint16_t *dst = a.out.p + row * a.out.row + head * a.out.head;
 #pragma unroll
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
         o.z = fmaf(y.z, f, o.z);
         o.w = fmaf(y.w, f, o.w);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? no_weight(s.len - s.n + row - s.row0) : 1.0f / l;
     uint2 y;
     if (a.bf16)
         y = make_uint2(pack2<SI_KV_BF16>(o.x * inv, o.y * inv), pack2<SI_KV_BF16>(o.z * inv, o.w * inv));

@@ -188,9 +188,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // One row's scores of a tile of full pages (kf, vf: a factor for every 16 tokens): z raw, the first `see` of them
 // visible (MASK; else all).
-// The largest score over the row's factor.
+// The largest score: z times the factors, rounded.
 template <bool MASK>
-__device__ __forceinline__ float row_top(const uint32_t (&z)[4][32], const float *kf, int see) {
+__device__ __forceinline__ float row_top(const uint32_t (&z)[4][32], const float *kf, float qf, int see) {
     float top = -INFINITY;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -203,16 +203,22 @@ __device__ __forceinline__ float row_top(const uint32_t (&z)[4][32], const float
         b = max3(b, at(8), at(9));
         a = max3(a, at(10), at(11));
         b = max3(b, at(12), at(13));
-        top = fmaxf(top, max3(a, b, fmaxf(at(14), at(15))) * kf[q]);
+        top = fmaxf(top, __fmul_rn(max3(a, b, fmaxf(at(14), at(15))), kf[q] * qf));
     }
     return top;
 }
 // Their weights 2^(score - m), with their sum, and in tensor memory at ts (two a column) the weights
-// times V's factors and v_inv, as fp16.
+// times V's factors and v_inv, as fp16.  m is taken from the product of z and the factors before that is rounded: off by
+// up to 2^-24 m from the score that became m, nothing where m is small, but 2^30 would leave no weight or an infinite
+// one.  So rows past kFar (`far`: the warp has one) take the form with MASK, which rounds the product first.  (A packed
+// product and a packed sum in turn were measured to be joined into one step, hence the zero.  A third form for such
+// rows costs all others registers: prompts 255 to 290 us, with the sum in this form 249, without it 243.)
+constexpr float kFar = 1048576.0f;
 template <bool MASK>
 __device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const float *kf, const float *vf, float qf, float v_inv,
-                                            float m, int see, uint32_t ts, f32x2 &sum) {
-    const f32x2 m2 = pk2(-m, -m);
+                                            float m, bool far, int see, uint32_t ts, f32x2 &sum) {
+    const float now = MASK && far ? 0.0f : -m, then = MASK && far ? -m : 0.0f;
+    const f32x2 now2 = pk2(now, now), then2 = pk2(then, then);
     f32x2 s0 = pk2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -220,7 +226,9 @@ __device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const fl
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float f = kf[2 * q + k / 16] * qf;
-            up2(fma2(pk2(__uint_as_float(z[q][k]), __uint_as_float(z[q][k + 1])), pk2(f, f), m2), y[k], y[k + 1]);
+            f32x2 s = fma2(pk2(__uint_as_float(z[q][k]), __uint_as_float(z[q][k + 1])), pk2(f, f), now2);
+            if (MASK) s = add2(s, then2);
+            up2(s, y[k], y[k + 1]);
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) {

@@ -84,3 +84,35 @@ def test_attend_rows_without_a_token_past_32_bits():
         for part in x[:n].split(1 << 17):
             assert (part == none).all()
     assert torch.isfinite(out[n]).all() and (out[n] != 0).any() and torch.isfinite(lse[n]).all()
+
+
+# ------------------------------------------------------------------ extreme scores
+def low_cache(length, news, k):
+    """Every key the same: `k` in the pages, twice that in the unfinished page's rows."""
+    c = ref.make_cache(Shape(4, 2, 64, 16, "int8", "bf16"), [length], [news], seed=2)
+    c.t["k_codes"].fill_(127)
+    c.t["k_scale"].fill_(k / 127)
+    c.t["k_tail"].fill_(2 * k)
+    return c
+
+
+@pytest.mark.parametrize("length,news", [(48, 1), (15, 1), (45, 10), (100, 100), (2000, 90), (5003, 1)])
+def test_attend_scores_far_below_zero(length, news):
+    """Scores of -8e34: a row takes what it sees as it would at any other height."""
+    c = low_cache(length, news, 1e17)
+    q = torch.full((news, 4, 64), -1e17).to(torch.bfloat16)
+    d = Dev(c)
+    out, lse = d.attend(q.to(DEV), 0.125)
+    check_attend(c, out, lse, q, 0.125)
+    assert d.status() == si.SI_OK
+
+
+@pytest.mark.parametrize("length,news", [(48, 1), (100, 100), (5003, 1), (2000, 90)])
+def test_attend_scores_past_the_range(length, news):
+    """Scores of -8e38 and past all the range of 32 bits: NaN, as for +8e38, and not the zeros of a row that sees nothing."""
+    c = low_cache(length, news, 1e19)
+    d = Dev(c)
+    for sign in (-1, 1):
+        q = torch.full((news, 4, 64), sign * 1e19).to(torch.bfloat16)
+        out, lse = d.attend(q.to(DEV), 0.125)
+        assert torch.isnan(out).all() and not torch.isfinite(lse).any()
