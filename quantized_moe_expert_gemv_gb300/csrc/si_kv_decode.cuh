@@ -394,10 +394,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 }
             }
         };
-        // Raw scores of keys t0 + g, t0 + g + 8 to the second product's operand: factors kf of the two
-        // keys, vf of their V; updates m, l and o's units.
-        auto weights = [&](float (&sc)[R8][4], float kf0, float kf1, float vf0, float vf1, float v_top, int t0, bool masked,
-                           uint32_t (&pb)[R8][2]) {
+        auto raise = [&](float v_top) {
             if (v_top > v_ref) {
                 const float f = v_ref / v_top;
                 v_ref = v_top;
@@ -409,6 +406,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[n][mt][e] *= f;
             }
+        };
+        // Raw scores of keys t0 + g, t0 + g + 8 to the second product's operand: factors kf of the two
+        // keys, vf of their V, v_inv of the rows (a function of n and e); updates m, l and o.
+        auto weights = [&](float (&sc)[R8][4], float kf0, float kf1, float vf0, float vf1, auto inv_of, int t0, bool masked,
+                           uint32_t (&pb)[R8][2]) {
             bool over = false;
 #pragma unroll
             for (int n = 0; n < R8; ++n)
@@ -446,14 +448,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                     }
                 }
             }
-            const float w0 = vf0 * v_inv, w1 = vf1 * v_inv;
 #pragma unroll
             for (int n = 0; n < R8; ++n) {
+                const float w[4] = {vf0 * inv_of(n, 0), vf0 * inv_of(n, 1), vf1 * inv_of(n, 0), vf1 * inv_of(n, 1)};
                 float p[4], y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     p[e] = ex2(sc[n][e] - m[n][e & 1]);
-                    y[e] = p[e] * (e < 2 ? w0 : w1);
+                    y[e] = p[e] * w[e];
                     // (a page without a scale makes NaN of the weights that see it, and of no other)
                     if (masked && p[e] == 0.0f) y[e] = 0.0f;
                 }
@@ -496,7 +498,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 chunk(keys.template load<3, 0>(kt), keys.template load<3, 1>(kt), 3);
             }
             uint32_t pb[R8][2];
-            weights(sc, ks, ks, vs, vs, vs, t0, t0 + 16 > lim_min, pb);
+            raise(vs);  // (rows that do not see the page see no later one of this warp's either)
+            weights(sc, ks, ks, vs, vs, [&](int, int) { return v_inv; }, t0, t0 + 16 > lim_min, pb);
             // V^T: keys 2j, 2j+1 and 2j+8, 2j+9; rows g and g + 8 of a row tile are two of this lane's run of d's
             constexpr int HW = D == 64 ? 2 : 4;  // words of a lane's run of d's (8 or 16 of each 64 or 128)
             auto values = [&](const uint32_t (&x)[4][HW], int half) {
@@ -602,9 +605,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 row_scale(amax, vmul[k], vf[k]);
                 if (!(key_of(k) < tail && s.slot >= 0)) vf[k] = 0.0f, vmul[k] = 0.0f;
             }
-            float v_top = fmaxf(fmaxf(vf[0], vf[1]), fmaxf(vf[2], vf[3]));  // (NaN leaves it)
-            v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, 1));
-            v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, 2));
             // those of this lane's scores' keys, g and g + 8, are with the lanes of j = g / 2
             float of[4];
 #pragma unroll
@@ -613,8 +613,38 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
             for (int n = 0; n < R8; ++n)  // rows that pad see no more than the tail's own tokens
 #pragma unroll
                 for (int e = 0; e < 2; ++e) lim[n][e] = min(lim[n][e], s.len);
+            // The weights are relative to the largest V scale so far, or, where rows see different tokens, to the largest
+            // that each row sees: a later token's, however large, takes no bits of them.  (Those of the rows lie in the
+            // place of the maxima that the join is about to get: registers are short here.)
+            const float vk[2] = {g & 1 ? of[1] : of[0], g & 1 ? of[3] : of[2]};
+            auto top_of = [&](float x) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            };
+            const bool alike = lim_min >= s.len;
+            if (alike) {
+                raise(top_of(fmaxf(vk[0], vk[1])));  // (NaN leaves it)
+            } else {
+#pragma unroll
+                for (int n = 0; n < R8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = paged + key0 + g < lim[n][e] ? fmaxf(vk[0], 0.0f) : 0.0f;
+                        const float vr = fmaxf(v_ref, top_of(paged + key0 + 8 + g < lim[n][e] ? fmaxf(vk[1], x) : x));
+                        const float f = v_ref / vr;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[n][mt][e] *= f;
+                            o[n][mt][2 + e] *= f;
+                        }
+                        if (g == 0) *reinterpret_cast<float2 *>(s_ml[w][n * 8 + 2 * j + e]) = make_float2(vr / kWeightUnit, kWeightUnit / vr);
+                    }
+                __syncwarp();
+            }
             uint32_t pb[R8][2];
-            weights(sc, kf[0], kf[1], g & 1 ? of[1] : of[0], g & 1 ? of[3] : of[2], v_top, paged + key0, true, pb);
+            weights(sc, kf[0], kf[1], vk[0], vk[1], [&](int n, int e) { return alike ? v_inv : s_ml[w][n * 8 + 2 * j + e][1]; },
+                    paged + key0, true, pb);
 #pragma unroll
             for (int z = 0; z < VW; ++z) {  // values d = 8 z .. of the lane's run: row tiles 4 z ..
                 uint32_t x[4][4];
@@ -632,6 +662,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
 #pragma unroll
                     for (int n = 0; n < R8; ++n) mma16816(o[n][4 * z + q], va, pb[n][0], pb[n][1]);
                 }
+            }
+            if (!alike) {  // these tokens are the warp's last: its sums go on in their own units
+#pragma unroll
+                for (int n = 0; n < R8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = s_ml[w][n * 8 + 2 * j + e][0];
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[n][mt][e] *= f;
+                            o[n][mt][2 + e] *= f;
+                        }
+                    }
+                v_ref = kWeightUnit;
+                __syncwarp();
             }
         }
 

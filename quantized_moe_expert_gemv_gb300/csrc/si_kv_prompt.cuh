@@ -42,10 +42,12 @@ static_assert(kPrRegSoftmax >= 128 && kPrRegTiles <= 128 && kPrRegMma <= 128 &&
                   2 * kPrRegSoftmax + kPrRegTiles + kPrRegMma <= 4 * 128,
               "more than the launch's registers would be waited for without end, and dec only goes down");
 constexpr int kPrFactorSlots = 4, kPrInfoSlots = 8;
-// What a tile of full pages needs for each 16 tokens: the page (0 where the table names none), K's and V's scale (NaN there).
+// What a tile of full pages needs for each 16 tokens: the page (0 where the table names none), K's and V's scale (NaN
+// there), and the largest V scale of the 16-token groups before each (NaN left out).
 struct PromptInfo {
     int32_t page[8];
-    float k[8], v[8];
+    float k[8], v[8], v_upto[9];
+    float pad[3];
 };
 
 template <int D>
@@ -54,12 +56,12 @@ struct PromptCfg {
     static constexpr int q = 0;
     static constexpr int k = 2 * tile;
     static constexpr int v = k + 2 * tile;
-    static constexpr int factors = v + 2 * tile;                       // [slots][2][128] floats
-    static constexpr int info = factors + kPrFactorSlots * 2 * 128 * 4;  // [slots][3][8]: see PromptInfo
-    static constexpr int bars = info + kPrInfoSlots * 96;
+    static constexpr int factors = v + 2 * tile;                       // [slots][3][128] floats: K's, V's, V's largest up to there
+    static constexpr int info = factors + kPrFactorSlots * 3 * 128 * 4;  // [slots]: PromptInfo
+    static constexpr int bars = info + kPrInfoSlots * (int)sizeof(PromptInfo);
     static constexpr int smem = bars + 32 * 8 + 1024;                  // + alignment slack
 };
-enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarInfo = 17, kBarNever = 19 };
+enum PromptBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11, kBarO = 13, kBarSFree = 15, kBarInfo = 17, kBarNever = 19, kBarFactors = 21 };
 // Tensor memory columns: one S (the row tiles take turns: a softmax thread has its whole row in registers
 // before the other tile's product is issued), P of each row tile, O of each.
 constexpr int kTmS = 0, kTmP = 128, kTmO = 256;
@@ -79,6 +81,21 @@ struct PromptArgs {
 
 // The CTA's first barrier, which each role reaches from its own code once its first loads are under way.
 __device__ __forceinline__ void role_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPrThreads) : "memory"); }
+// The largest of the 128 factors at f up to each, to the 128 places behind them (NaN left out): a warp, four a lane.
+__device__ __forceinline__ void factors_upto(float *f, int lane) {
+    float4 y = reinterpret_cast<const float4 *>(f)[lane];
+    y.x = fmaxf(y.x, 0.0f);
+    y.y = fmaxf(y.x, y.y);
+    y.z = fmaxf(y.y, y.z);
+    y.w = fmaxf(y.z, y.w);
+    float upto = y.w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const float up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto = fmaxf(upto, up);
+    }
+    const float up = __shfl_up_sync(0xffffffffu, upto, 1), before = lane == 0 ? 0.0f : up;
+    reinterpret_cast<float4 *>(f + 128)[lane] = make_float4(fmaxf(before, y.x), fmaxf(before, y.y), fmaxf(before, y.z), upto);
+}
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         const int n = ntx[x];
         for (int i = 0; i < n; ++i) {
             const int key0 = (t_first + i) * kPrKeys;
-            const float *kf = factors + (i % kPrFactorSlots) * 256, *vf = kf + 128;
+            const float *kf = factors + (i % kPrFactorSlots) * 384, *vf = kf + 128;
             if (!wait(kBarS + x, i & 1)) break;
             tc::fence_after_sync();
             const bool whole = key0 + kPrKeys <= paged;                 // a factor for every 16 keys
@@ -215,13 +232,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32(ts + 32 * q, z[q]);
                 const PromptInfo &info = infos[i % kPrInfoSlots];
-                float v_top = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v_top = fmaxf(v_top, info.v[q]);
+                // (the largest that the row sees: a later page's scale, however large, takes no bits of its weights)
+                const int see = lim - key0;
+                const float v_top = info.v_upto[min(max(see + 15, 0) >> 4, 8)];
                 tc::tmem_wait_ld();
                 tc::fence_before_sync();
                 mbar_arrive(bar(kBarSFree + x));
-                const int see = lim - key0;
                 const bool all = __all_sync(0xffffffffu, !live || see >= kPrKeys);
                 f32x2 sum;
                 const float top = all ? row_top<false>(z, info.k, qf, see) : row_top<true>(z, info.k, qf, see);
@@ -234,15 +250,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                     row_weights<true>(z, info.k, info.v, qf, v_inv, m, far, see, tp, sum);
                 l2 = add2(l2, sum);
             } else {
-                // (the factors of four columns a load, the largest of V's by the warp together)
+                // (the factors of four columns a load)
                 const float4 *kf4 = reinterpret_cast<const float4 *>(kf), *vf4 = reinterpret_cast<const float4 *>(vf);
-                float top = -INFINITY, v_top;
-                {
-                    const float4 y = vf4[lane];
-                    v_top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-                    for (int o = 16; o; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
-                }
                 const int see = lim - key0;
+                const float v_top = see > 0 ? vf[127 + min(see, kPrKeys)] : 0.0f;  // (the largest up to the row's last column)
+                float top = -INFINITY;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t z[32];
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         const uint32_t a0 = f16_tile_at(r0, 2 * ch), a1 = f16_tile_at(r0, 2 * ch + 1);
         auto store = [&](uint32_t tile, int i, bool v) {
             const int key0 = (t_first + i) * kPrKeys;
-            float *kf = factors + (i % kPrFactorSlots) * 256;
+            float *kf = factors + (i % kPrFactorSlots) * 384;
             if (key0 + kPrKeys <= paged) {
                 const uint4(&x)[4 * CC] = v ? vx : kx;
                 codes_to_tile<CODE, 0>(x[0], tile + a0, tile + a1);
@@ -401,6 +413,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         if (nt > 0) wait(kBarInfo, 0);
         load(0, false);
         load(0, true);
+        int slow = 0;  // tiles without a page's scale for each column so far
         for (int i = 0; i < nt; ++i) {
             const int st = i & 1;
             const bool whole = (t_first + i + 1) * kPrKeys <= paged;
@@ -411,6 +424,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             if (!whole) {
                 if (i >= 2 && !wait(kBarVEmpty + st, ((i >> 1) - 1) & 1)) break;
                 store(base + Cfg::v + st * Cfg::tile, i, true);
+                mbar_arrive(bar(kBarFactors));
+                if (warp == 8) {
+                    if (!wait(kBarFactors, slow & 1)) break;
+                    factors_upto(factors + (i % kPrFactorSlots) * 384 + 128, lane);
+                }
+                ++slow;
             }
             tc::fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + st));
@@ -442,6 +461,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             }
             mbar_init(bar(kBarNever), 1);
             mbar_init(bar(kBarNever + 1), 1);
+            mbar_init(bar(kBarFactors), 128);
             fence_mbar_init();
         }
         __syncwarp();
@@ -533,11 +553,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
         look(0, page, ks, vs);
         for (int j = 0; j < nt; ++j) {
             if (j >= 2 && !wait(kBarKFull + (j & 1), ((j - 2) >> 1) & 1)) break;
+            float upto = fmaxf(vs, 0.0f);
+            for (int o = 1; o < 8; o <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto = fmaxf(upto, up);
+            }
             if (lane < 8) {
                 PromptInfo &info = infos[j % kPrInfoSlots];
                 info.page[lane] = page;
                 info.k[lane] = ks;
                 info.v[lane] = vs;
+                info.v_upto[lane + 1] = upto;
+                if (lane == 0) info.v_upto[0] = 0.0f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarInfo + (j & 1)));

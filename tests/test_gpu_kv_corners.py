@@ -116,3 +116,31 @@ def test_attend_scores_past_the_range(length, news):
         q = torch.full((news, 4, 64), sign * 1e19).to(torch.bfloat16)
         out, lse = d.attend(q.to(DEV), 0.125)
         assert torch.isnan(out).all() and not torch.isfinite(lse).any()
+
+
+# ------------------------------------------------------------------ what a row does not see
+@pytest.mark.parametrize("length,news,page", [(30, 12, 64), (300, 25, 64), (9, 3, 16), (200, 60, 32), (130, 130, 64), (1000, 150, 16)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attend_a_later_token_of_any_size(length, news, page, dim):
+    """V of the last tokens 2^40 times as large as the others': the rows before them are within the usual bounds.  (Of the rows
+    that see them, weights below 2^-36 of the largest V fall among fp16's smallest values: half a step for each token.)"""
+    shape = Shape(8, 2, dim, page, "int8", "bf16")
+    c = ref.make_cache(shape, [length, 20], [news, 1], seed=3)
+    q, qd = make_q(c, 4)
+    sm = dim ** -0.5
+    out, lse, _, _ = ref.attend(c, q, sm)
+    last = max(1, news // 3)
+    for t in range(length - last, length):
+        if t >= length // page * page:
+            c.t["v_tail"][int(c.slots[0]), :, t % (2 * page)] *= 2.0 ** 40
+        elif t % page == 0:  # (a page of later tokens alone)
+            c.t["v_scale"][int(c.table[0, t // page])] *= 2.0 ** 40
+    d = Dev(c)
+    got, z = d.attend(qd, sm)
+    first, half = max(0, news - last), torch.finfo(torch.bfloat16).eps / 2
+    want, _, S, _ = ref.attend(c, q, sm)
+    assert torch.equal(want[:first], out[:first])
+    tol = half * want.abs() + (2.0 ** -11 + 2.0 ** -14) * S + 2.0 ** -25
+    tol[first:news] += length * 2.0 ** -36 * ref.history(c, "v", 0).abs().amax()
+    assert ((got.double().cpu() - want).abs() <= tol).all()
+    assert ((z.double().cpu() - lse).abs() <= 2.0 ** -14).all()
