@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 for (int e = 0; e < 4; ++e) {
                     p[e] = ex2(sc[n][e] - m[n][e & 1]);
                     y[e] = p[e] * w[e];
-                    // (a page without a scale makes NaN of the weights that see it, and of no other)
-                    if (masked && p[e] == 0.0f) y[e] = 0.0f;
+                    // (a page without a scale makes NaN of what sees it, however small its weight, and of no other)
+                    if (masked && t0 + g + 8 * (e >> 1) >= lim[n][e & 1]) y[e] = 0.0f;
                 }
                 l[n][0] += p[0] + p[2];
                 l[n][1] += p[1] + p[3];

@@ -284,8 +284,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                         float w[4], pp[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            pp[e] = 32 * q + k + e < see ? ex2(__fmul_rn(__uint_as_float(z[k + e]), fs[e] * qf) - m) : 0.0f;
-                            w[e] = pp[e] == 0.0f ? 0.0f : pp[e] * (gs[e] * v_inv);
+                            const bool in = 32 * q + k + e < see;
+                            pp[e] = in ? ex2(__fmul_rn(__uint_as_float(z[k + e]), fs[e] * qf) - m) : 0.0f;
+                            w[e] = in ? pp[e] * (gs[e] * v_inv) : 0.0f;
                         }
                         l2 = add2(l2, pk2(pp[0], pp[1]));
                         l2 = add2(l2, pk2(pp[2], pp[3]));

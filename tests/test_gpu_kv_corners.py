@@ -144,3 +144,22 @@ def test_attend_a_later_token_of_any_size(length, news, page, dim):
     tol[first:news] += length * 2.0 ** -36 * ref.history(c, "v", 0).abs().amax()
     assert ((got.double().cpu() - want).abs() <= tol).all()
     assert ((z.double().cpu() - lse).abs() <= 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("n", [20, 40])
+def test_attend_a_page_without_a_v_scale_and_weights_that_vanish(n):
+    """What attends to a token of such a page is NaN also where the token's weight is less than 32 bits hold."""
+    c = ref.make_cache(Shape(4, 2, 64, 16, "int8", "bf16"), [40], [n], seed=2)
+    c.t["k_codes"].fill_(127)
+    c.t["k_codes"][int(c.table[0, 1])] = -127
+    c.t["k_scale"].fill_(1.0 / 127)
+    c.t["k_tail"].fill_(1.0)
+    d = Dev(c)
+    q = torch.ones((n, 4, 64), dtype=torch.bfloat16)
+    good, z = d.attend(q.to(DEV), 4.0)
+    check_attend(c, good, z, q, 4.0)
+    d.v_scale[int(c.table[0, 1]), 1] = math.nan
+    out, lse = d.attend(q.to(DEV), 4.0)
+    sees = torch.arange(n, device=DEV) + 40 - n >= 16
+    assert torch.equal(lse, z) and torch.equal(out[:, :2], good[:, :2]) and torch.equal(out[~sees], good[~sees])
+    assert torch.isnan(out[sees, 2:]).all()
