@@ -591,7 +591,9 @@ __global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
     if (rh >= (int64_t)c.T * c.H) return;
     const int d = (int)(at % (D / 4)) * 4;
     const int row = (int)(rh / c.H), head = (int)(rh % c.H);
-    // rows of no sequence were not computed: the sequence of a row is the last one that starts at or before it
+    // The sequence of a row is the last one that starts at or before it, where all starts ascend.  One that does not may
+    // lead the search astray (and the products' kernel has reported it): then every sequence is tried.  Rows of
+    // none were not computed.
     int lo = 0, hi = c.B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -600,7 +602,9 @@ __global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
         else
             hi = mid;
     }
-    const Seq s = load_seq(c, lo);
+    Seq s = load_seq(c, lo);
+    if (*c.status != SI_OK)
+        for (int b = 0; b < c.B && (row < s.row0 || row >= s.row0 + s.n); ++b) s = load_seq(c, b);
     if (row < s.row0 || row >= s.row0 + s.n) return;
     const float *ml = a.partial + (int64_t)a.splits * c.T * c.H * D;
     float m = kNoScore, l = 0.0f;

@@ -163,3 +163,19 @@ def test_attend_a_page_without_a_v_scale_and_weights_that_vanish(n):
     sees = torch.arange(n, device=DEV) + 40 - n >= 16
     assert torch.equal(lse, z) and torch.equal(out[:, :2], good[:, :2]) and torch.equal(out[~sees], good[~sees])
     assert torch.isnan(out[sees, 2:]).all()
+
+
+def test_attend_a_broken_start_leaves_the_other_sequences_whole():
+    """A start outside the rows, in a call that is split along the keys: its two sequences are reported, the others right."""
+    c = ref.make_cache(Shape(8, 2, 128, 64, "int8", "bf16"), [4000, 3900, 4000, 3800], [70, 70, 70, 70], seed=3)
+    q, qd = make_q(c, 4)
+    good, z = Dev(c).attend(qd, 0.09)
+    check_attend(c, good, z, q, 0.09)
+    for at, value, left in ((2, 99999, (0, 3)), (2, -5, (0, 3)), (1, 500, (2, 3)), (3, 0, (0, 1))):
+        d = Dev(c)
+        d.q_start[at] = value
+        out, lse = d.attend(qd, 0.09)
+        assert d.status() == si.SI_ERR_DEVICE
+        for b in left:
+            r = slice(70 * b, 70 * b + 70)
+            assert torch.equal(out[r], good[r]) and torch.equal(lse[r], z[r]), (at, value, b)
