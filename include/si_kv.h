@@ -133,7 +133,8 @@ si_status si_kv_read(si_kv_plan_t plan, const si_kv_cache *cache, const int32_t 
  * [n_heads] fp32).  A row that sees no token (lens[b] < n_b) gives zeros and
  * lse -inf.  Scores are held in 32 bits: one below their range has no weight, and
  * a row with one above it, or with all of its scores below it, is NaN.  out
- * must not overlap q. */
+ * must not overlap q (checked where their strides are the same), and its rows and
+ * heads must not overlap one another. */
 si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_batch *batch, const si_kv_rows *q,
                        const si_kv_rows *out, float *lse, float sm_scale, void *scratch, size_t scratch_bytes,
                        si_stream_t stream);

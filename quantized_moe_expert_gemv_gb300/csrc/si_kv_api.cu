@@ -85,6 +85,32 @@ si_status check_rows(const Plan &p, const si_kv_rows *r, bool written) {
     return SI_OK;
 }
 
+// Whether D values at elements x + r row + h head and D at y + r' row + h' head can share one, for |r - r'| < T and
+// |h - h'| < H; `self`: the same operand, in which r = r' and h = h' is one place.
+bool strides_meet(int64_t apart, int64_t row, int64_t head, int64_t T, int64_t H, int64_t D, bool self) {
+    for (int64_t h = 1 - H; h < H; ++h) {
+        const int64_t at = apart + h * head;  // of which multiples of row, up to T - 1 of them, may make less than D
+        const int64_t near = row == 0 ? 0 : -at / row;
+        for (int64_t r = std::max(near - 1, 1 - T); r <= std::min(near + 1, T - 1); ++r)
+            if ((!self || r != 0 || h != 0) && std::abs(at + r * row) < D) return true;
+    }
+    return false;
+}
+// out's rows and heads may not meet one another; nor q's, as far as their strides are alike (else only the places of
+// which both have the first).
+si_status check_out(const Plan &p, const si_kv_rows *q, const si_kv_rows *out, int64_t T) {
+    const int64_t D = p.desc.head_dim, H = p.desc.n_heads;
+    const bool spans = out->row_stride >= (H - 1) * out->head_stride + D || out->head_stride >= (T - 1) * out->row_stride + D;
+    if (!spans && strides_meet(0, out->row_stride, out->head_stride, T, H, D, true)) return SI_ERR_INVALID_ARG;
+    const int64_t apart = (int64_t)(reinterpret_cast<intptr_t>(out->data) - reinterpret_cast<intptr_t>(q->data)) / 2;
+    const bool alike = (q->row_stride == out->row_stride || T == 1) && (q->head_stride == out->head_stride || H == 1);
+    const int64_t reach = (T - 1) * out->row_stride + (H - 1) * out->head_stride + D;
+    if (alike ? std::abs(apart) < reach && strides_meet(apart, out->row_stride, out->head_stride, T, H, D, false)
+              : std::abs(apart) < D)
+        return SI_ERR_INVALID_ARG;
+    return SI_OK;
+}
+
 Ctx make_ctx(const Plan &p, const si_kv_cache *c, const si_kv_batch *b, void *scratch) {
     Ctx x{};
     x.kc = static_cast<uint8_t *>(c->k_codes);
@@ -222,6 +248,7 @@ si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
     if (!aligned(lse, 4)) return SI_ERR_MISALIGNED;
     SI_KV_TRY(check_scratch(plan->p, batch, scratch, scratch_bytes));
     if (batch->total_new == 0 || batch->max_new == 0) return SI_OK;
+    SI_KV_TRY(check_out(plan->p, q, out, batch->total_new));
     return launched(si::kv::launch_attend(plan->p, make_ctx(plan->p, cache, batch, scratch), make_rows(q),
                                           make_rows(out), lse, sm_scale, scratch, (cudaStream_t)stream));
 }

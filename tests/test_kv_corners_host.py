@@ -60,6 +60,7 @@ def test_the_row_bound_is_what_the_others_leave(recorder, name):
     for total, most, want in ((6, 4, 4), (6, 2 ** 31 - 1, 6), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 30 // 64), (2 ** 25, 5, 5)):
         call = Call(plan)
         call.batch.total_new, call.batch.max_new = total, most
+        call.out = binding.si_kv_rows(0x90000, 64 * 128, 128)
         assert call(recorder, name) == binding.SI_OK
         assert recorder.last_max_new() == want
     recorder.si_kv_plan_destroy(plan.handle)
@@ -95,3 +96,58 @@ def test_shared_memory_is_allowed_once_on_each_device_that_launches(tmp_path):
         assert lib.call(0, 0) == 0
         assert lib.call(1, 0) == 0
     assert lib.sets(0) == lib.sets(1) == 1
+
+
+def test_outputs_that_overlap_are_refused(recorder):
+    """8 heads of 128 in 6 rows: strides that put two rows or heads in one place, and outputs in q's place."""
+    plan = host_plan(recorder, 8, 2, 128, 64)
+
+    def attend(q, out, rows=6):
+        call = Call(plan)
+        call.batch.total_new = rows
+        call.rows, call.out = binding.si_kv_rows(*q), binding.si_kv_rows(*out)
+        return call(recorder, "attend")
+
+    far, q = 0x900000, (0x80000, 1024, 128)
+    for strides in ((128, 128), (512, 128), (128, 640), (1016, 128), (136, 136), (256, 128), (640, 256)):
+        assert attend(q, (far, *strides)) == binding.SI_ERR_INVALID_ARG, strides
+    for strides in ((1024, 128), (1032, 128), (128, 768), (4096, 384), (136, 816), (256, 1536 + 128), (1024 + 128, 144)):
+        assert attend(q, (far, *strides)) == binding.SI_OK, strides
+    # neither stride spans the other dimension, and no two places meet: rows at 2 x 128, heads at odd multiples
+    assert attend(q, (far, 256, 128 * 13)) == binding.SI_OK
+    assert attend(q, (far, 128, 128), rows=1) == binding.SI_OK   # one row
+    # q's place, one row on, half a head on; q's own buffer where the parts of a projection lie side by side
+    assert attend(q, q) == attend(q, (0x80000 + 2048, 1024, 128)) == attend(q, (0x80000 + 128, 1024, 128)) == binding.SI_ERR_INVALID_ARG
+    wide = (0x80000, 4096, 128)
+    assert attend(wide, (0x80000 + 2048, 4096, 128)) == binding.SI_OK
+    assert attend(wide, (0x80000 - 2048, 4096, 128)) == binding.SI_OK
+    assert attend(wide, (0x80000 + 4096 * 2 - 2048 + 256, 4096, 128)) == binding.SI_ERR_INVALID_ARG  # its last head is the next row's first
+    assert attend((0x80000, 0, 128), (0x80000, 1024, 128)) == binding.SI_ERR_INVALID_ARG
+    recorder.si_kv_plan_destroy(plan.handle)
+
+
+def brute(places, D):
+    at = sorted(places)
+    return any(b - a < D for a, b in zip(at, at[1:]))
+
+
+def test_overlap_of_any_strides(recorder):
+    """Against every pair of places, for small rows and heads."""
+    import random
+    rng = random.Random(3)
+    plan = host_plan(recorder, 6, 2, 64, 64)
+    seen = set()
+    for _ in range(3000):
+        rows, row, head = rng.randrange(1, 9), 8 * rng.randrange(8, 80), 8 * rng.randrange(8, 80)
+        call = Call(plan)
+        call.batch.total_new = rows
+        call.out = binding.si_kv_rows(0x900000, row, head)
+        call.rows = binding.si_kv_rows(0x900000 + 16 * rng.randrange(-600, 600), row, head)
+        out = [r * row + h * head for r in range(rows) for h in range(6)]
+        apart = (call.rows.data - 0x900000) // 2
+        meets = any(abs(x - y - apart) < 64 for x in out for y in out)
+        want = binding.SI_ERR_INVALID_ARG if brute(out, 64) or meets else binding.SI_OK
+        assert call(recorder, "attend") == want, (rows, row, head, apart)
+        seen.add((brute(out, 64), meets))
+    assert len(seen) == 4
+    recorder.si_kv_plan_destroy(plan.handle)
