@@ -165,7 +165,11 @@ si_status si_kv_weigh(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_b
  * are not written); keep[b][g][i] the kept page numbers, -1 past their count;
  * lens_out[b] = min(F, budget) * P + lens[b] mod P.  The unfinished page's rows
  * go to the ring place of the new length in slot new_slots[b] (NULL: the
- * batch's own slots).  The old pages are left as they are.  sink + recent <=
+ * batch's own slots): the sequence's own slot, or one that holds no unfinished
+ * rows of another sequence of the call and is not another's new one (else
+ * SI_ERR_DEVICE, and the rows stay where they are).  The rows of the page before are
+ * not carried over: a step cannot be taken back past an eviction's page
+ * boundary.  The old pages are left as they are.  sink + recent <=
  * budget; max_len / P <= SI_KV_MAX_EVICT_PAGES; acc_stride >= max_len for both;
  * acc_out and lens_out must not overlap acc_in and lens; q_start is not read. */
 si_status si_kv_evict(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_batch *batch, const float *acc_in,

@@ -10,7 +10,8 @@
 // still share the prefix, until the digit's bin holds exactly the pages still
 // wanted.  Equal keys go to the lower page, by a count over the pages in order.
 // Move (k_kv_move, one CTA for each new page, and one for the rest): codes,
-// scale and sums are copied as they are.
+// scale and sums are copied as they are; the unfinished page's rows only where
+// no other sequence's lie or go.
 // Bound: HBM for the move (each kept byte read and written once); the choice reads
 // acc once and is a chain of block-wide steps.  Measured: 8 sequences of 20000 to
 // 32700 tokens, 8 heads of 128, down to 128 pages of 64: 136 us, 75 % of the copy
@@ -197,7 +198,20 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(Ctx c, const float *ac
         if (tid == 0) set_status(c.status, SI_ERR_DEVICE);
         return;
     }
-    if (s.slot < 0 || (slot == s.slot && ((F ^ n_keep) & 1) == 0)) return;
+    if (s.slot < 0 || r == 0 || (slot == s.slot && ((F ^ n_keep) & 1) == 0)) return;
+    if (slot != s.slot) {
+        // all sequences' rows move at once: the slot may hold no other's (which may have to be read yet, or stay), nor be
+        // another's new one
+        bool taken = false;
+        for (int k = tid; k < c.B; k += kMoveThreads) {
+            const int len = c.lens[k], own = c.slots ? c.slots[k] : k;
+            if (k != b && len >= 0 && len <= c.max_len && len % P != 0) taken |= own == slot || new_slots[k] == slot;
+        }
+        if (__syncthreads_or(taken)) {
+            if (tid == 0) set_status(c.status, SI_ERR_DEVICE);
+            return;
+        }
+    }
     const int upr = c.D / 8;
     for (int u = tid; u < r * upr; u += kMoveThreads) {
         const int t = u / upr, d = u % upr * 8;

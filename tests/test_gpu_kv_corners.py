@@ -179,3 +179,33 @@ def test_attend_a_broken_start_leaves_the_other_sequences_whole():
         for b in left:
             r = slice(70 * b, 70 * b + 70)
             assert torch.equal(out[r], good[r]) and torch.equal(lse[r], z[r]), (at, value, b)
+
+
+# ------------------------------------------------------------------ evict
+def test_evict_into_another_sequences_slot():
+    """A new slot that holds another sequence's unfinished rows, or that two take, is reported and not written to."""
+    shape = Shape(2, 2, 64, 16, "int8", "bf16")
+    lens = [100, 107, 96, 55]  # the third has no unfinished rows
+    c = ref.make_cache(shape, lens, [1] * 4, seed=7, spare_pages=20, spare_slots=4)
+    s = c.slots.tolist()
+    free = [x for x in range(c.n_slots) if x not in s]
+    used = set(c.table[c.table >= 0].tolist())
+    table = torch.tensor([p for p in range(c.n_pages) if p not in used][:16], dtype=torch.int32).view(4, 4)
+    acc = torch.rand((4, 2, 107))
+    for new, bad in (([s[1], s[0], s[2], s[3]], {0, 1}), ([s[1], s[1], s[2], s[3]], {0}), ([s[2], s[1], s[0], s[3]], set()),
+                     ([free[0], s[0], s[2], free[1]], {1}), ([free[0], free[1], s[2], free[0]], {0, 3}),
+                     ([s[0], s[1], s[1], s[3]], set())):
+        d = Dev(c)
+        acc_out, keep, lens_out = run_evict(d, acc.to(DEV), 4, 0, 1, table.to(DEV), torch.tensor(new, dtype=torch.int32, device=DEV))
+        assert d.status() == (si.SI_ERR_DEVICE if bad else si.SI_OK), new
+        assert lens_out.tolist() == [4 * 16 + 4, 4 * 16 + 11, 4 * 16, 3 * 16 + 7]
+        want = {w: c.t[w].clone() for w in ("k_tail", "v_tail")}
+        for b, L in enumerate(lens):
+            n, r = min(4, L // 16), L % 16
+            assert keep[b, 0, :n].tolist() == ref.keep_pages(acc[b, 0], L, 16, 4, 0, 1)
+            if b not in bad:
+                was, now = torch.arange(L - r, L) % 32, torch.arange(n * 16, n * 16 + r) % 32
+                for w in want:
+                    want[w][new[b], :, now] = c.t[w][s[b]][:, was]
+        for w in want:
+            assert torch.equal(getattr(d, w).cpu().view(torch.int16), want[w].view(torch.int16)), (new, w)
