@@ -156,8 +156,8 @@ si_status si_kv_weigh(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_b
 /* Evict by accumulated weight: each kv head of each sequence keeps at most
  * `budget` of its F = lens[b] / P full pages (and the unfinished page): the
  * first `sink`, the last `recent`, and of the others those with the largest sum
- * of acc over their tokens (summed in 64 or twice 32 bits; ties stay with the lower page;
- * NaN counts as largest), in their order.  The kept pages' codes and scales
+ * of acc over their tokens (exact to 2^-49 of a page's largest value, in any order of
+ * its tokens; ties stay with the lower page; NaN counts as largest), in their order.  The kept pages' codes and scales
  * are copied as they are to the pages new_table[b][0 .. min(F, budget) - 1],
  * so they are not rounded again; which page a slot of the new table holds may
  * differ from head to head.  new_table names pages that no sequence of the

@@ -2,8 +2,8 @@
 // each kv head's pages, and their move.
 //
 // Choice (k_kv_choose, one CTA for each sequence and kv head).  A page's score
-// is the sum of acc over its tokens in twice 32 bits (a page that is kept by a
-// last-bit difference of a 32-bit sum would depend on the order of the sum).  Scores
+// is the sum of acc over its tokens, in whole numbers (a page that is kept by a
+// last-bit difference would depend on the order of the sum).  Scores
 // become 64-bit keys whose unsigned order is the scores' order, the protected
 // pages get the largest key, and a radix selection finds the key of the last
 // page that stays: 8 bits a pass from the top, a histogram of the keys that
@@ -32,13 +32,27 @@ __device__ __forceinline__ unsigned long long score_key(double x) {
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
-// Sums in twice 32 bits: s + e is the sum so far, e what its additions have rounded off (the error of each
-// addition is a number of 32 bits and is found by additions; D. Knuth's two-sum).  A page of 64 tokens is off by
-// less than 2^-40 of its sum; the 64-bit unit, of two lanes a cycle and SM, took 17 us for 32768 tokens.
-__device__ __forceinline__ void add_two(float &s, float &e, float x) {
-    const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
-    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
-    s = t;
+// A page's sum, in whole units of 2^(top - 182), where top is the largest exponent field of its values: a value is its
+// 24 bits shifted by what its exponent is below the top (up to 32 to the left, bits further down are cut off), below 2^56, so
+// 64 of them fit 64 bits.  Whole numbers add up to the same in any order: pages of the same values tie.  The sum is
+// exact where the values lie within 2^32 of one another, and else off by less than 2^-49 of the largest.  (In 64-bit floating
+// point, of two lanes a cycle and SM, 32768 tokens took 17 us.)
+__device__ __forceinline__ int exponent_of(float x) { return (__float_as_uint(x) >> 23) & 255; }
+__device__ __forceinline__ long long in_units(float x, int top) {
+    const uint32_t u = __float_as_uint(x);
+    const int e = exponent_of(x), down = top - max(e, 1);
+    const unsigned long long m = (unsigned long long)((u & 0x7fffffu) | (e ? 0x800000u : 0u)) << 32;
+    const long long v = down < 64 ? (long long)(m >> down) : 0;
+    return u >> 31 ? -v : v;
+}
+
+// score_key of such a sum (its 53 leading bits), by its bits: the 64-bit unit's conversion and product take longer.
+__device__ __forceinline__ unsigned long long units_key(long long v, int top) {
+    if (v == 0) return 0x8000000000000000ull;
+    const unsigned long long mag = v < 0 ? 0ull - (unsigned long long)v : (unsigned long long)v;
+    const int zeros = __clzll((long long)mag);
+    const unsigned long long u = (unsigned long long)(63 - zeros + top - 182 + 1023) << 52 | (mag << zeros << 1) >> 12;
+    return v < 0 ? ~(u | 0x8000000000000000ull) : u | 0x8000000000000000ull;
 }
 
 // Exclusive prefix of a 0/1 flag over the CTA's threads in order; `total` = their sum.
@@ -85,20 +99,23 @@ __global__ void __launch_bounds__(kChooseMost) k_kv_choose(Ctx c, const float *a
         for (int q = 0; q < 8; ++q) {
             const int j = j0 + q * step;
             if (j >= F) break;
-            float hi = x[q][0], lo = 0.0f;
-#pragma unroll
-            for (int e = 1; e < 4; ++e) add_two(hi, lo, x[q][e]);
-            for (int o = 8; o; o >>= 1) {
-                const float y = __shfl_xor_sync(half, hi, o), z = __shfl_xor_sync(half, lo, o);
-                add_two(hi, lo, y);
-                lo += z;
-            }
-            double sum = (double)hi + (double)lo;
-            if (!(fabsf(hi) <= 3.4e38f)) {  // infinite, NaN, or past 32 bits' range: in 64 bits after all
-                sum = ((double)x[q][0] + (double)x[q][1]) + ((double)x[q][2] + (double)x[q][3]);
+            int top = max(max(exponent_of(x[q][0]), exponent_of(x[q][1])), max(exponent_of(x[q][2]), exponent_of(x[q][3])));
+            top = max(__reduce_max_sync(half, top), 1);
+            unsigned long long key;
+            if (top < 255) {
+                const unsigned long long v = (in_units(x[q][0], top) + in_units(x[q][1], top)) +
+                                             (in_units(x[q][2], top) + in_units(x[q][3], top));
+                // (16 lanes' sum modulo 2^64, by 22 bits at a time)
+                const unsigned long long a0 = __reduce_add_sync(half, (unsigned)(v & 0x3fffff));
+                const unsigned long long a1 = __reduce_add_sync(half, (unsigned)(v >> 22 & 0x3fffff));
+                const unsigned long long a2 = __reduce_add_sync(half, (unsigned)(v >> 44));
+                key = units_key((long long)(a0 + (a1 << 22) + (a2 << 44)), top);
+            } else {  // a value that is not finite
+                double sum = ((double)x[q][0] + (double)x[q][1]) + ((double)x[q][2] + (double)x[q][3]);
                 for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
+                key = score_key(sum);
             }
-            if (l16 == 0) s_key[j] = j < sink || j >= F - recent ? ~0ull : score_key(sum);
+            if (l16 == 0) s_key[j] = j < sink || j >= F - recent ? ~0ull : key;
         }
     }
     __syncthreads();

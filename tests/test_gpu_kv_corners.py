@@ -209,3 +209,68 @@ def test_evict_into_another_sequences_slot():
                     want[w][new[b], :, now] = c.t[w][s[b]][:, was]
         for w in want:
             assert torch.equal(getattr(d, w).cpu().view(torch.int16), want[w].view(torch.int16)), (new, w)
+
+
+def kept_exactly(acc, length, page, budget):
+    """keep_pages with sums that are rounded once (math.fsum)."""
+    full = length // page
+    score = [math.fsum(acc[j * page:(j + 1) * page].tolist()) for j in range(full)]
+    return sorted(sorted(range(full), key=lambda j: (-score[j], j))[:budget])
+
+
+def choose(acc, page, budget):
+    """The pages that si_kv_evict keeps of one sequence, acc [heads, tokens]."""
+    heads, length = acc.shape
+    c = ref.make_cache(Shape(heads, heads, 64, page, "int8", "bf16"), [length], [1], seed=7, spare_pages=budget)
+    used = set(c.table[c.table >= 0].tolist())
+    table = torch.tensor([[p for p in range(c.n_pages) if p not in used][:budget]], dtype=torch.int32, device=DEV)
+    d = Dev(c)
+    _, keep, _ = run_evict(d, acc[None].to(DEV), budget, 0, 0, table, None)
+    assert d.status() == si.SI_OK
+    return keep[0].tolist()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_evict_pages_of_the_same_values_tie(page):
+    """A page's sum does not depend on the order of its tokens: ties stay with the lower pages, whatever the values' spread."""
+    g = torch.Generator().manual_seed(3)
+    acc = torch.empty((4, 300 * page))
+    for h, spread in enumerate((2.0, 8.0, 24.0, 60.0)):
+        x = torch.exp2(-spread * torch.rand(page, generator=g)) * torch.rand(page, generator=g)
+        acc[h] = torch.cat([x[torch.randperm(page, generator=g)] for _ in range(300)])
+    assert choose(acc, page, 120) == [list(range(120))] * 4
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_evict_pages_whose_sums_differ_in_the_last_bits(page):
+    """Sums that differ near the last of 53 bits, their tokens in any order; negative, tiny and huge ones."""
+    g = torch.Generator().manual_seed(5)
+    rows = []
+    for scale in (1.0, 2.0 ** -140, 2.0 ** 121, -1.0):
+        pages = []
+        step = torch.randperm(200, generator=g).tolist()
+        for j in range(200):
+            x = (torch.randint(1, 1 << 20, (page - 1,), generator=torch.Generator().manual_seed(9)).double() * 2.0 ** -20)
+            small = 2.0 ** -24 + step[j] * 2.0 ** -47
+            x = torch.cat([x, torch.tensor([small], dtype=torch.float64)]) * scale
+            if abs(scale) < 2.0 ** -126:  # (the smallest values have fewer bits)
+                x = x[torch.randperm(page, generator=g)] * torch.randint(1, 4, (1,), generator=g)
+            pages.append(x[torch.randperm(page, generator=g)].float())
+        rows.append(torch.cat(pages))
+    acc = torch.stack(rows)
+    got = choose(acc, page, 77)
+    for h in range(4):
+        assert got[h] == kept_exactly(acc[h], 200 * page, page, 77), h
+
+
+def test_evict_sums_that_are_not_finite():
+    """+inf above every sum, NaN above it, -inf below; sums past 32 bits' range are numbers."""
+    acc = torch.rand((1, 8 * 16), generator=torch.Generator().manual_seed(1))
+    acc[0, 16] = math.inf          # page 1
+    acc[0, 40] = math.nan          # page 2
+    acc[0, 50] = -math.inf         # page 3
+    acc[0, 64:80] = 3.0e38         # page 4: 4.8e39
+    acc[0, 80:96] = 2.9e38         # page 5
+    acc[0, 96], acc[0, 97] = math.inf, -math.inf  # page 6: NaN
+    for budget, want in ((1, [2]), (2, [2, 6]), (3, [1, 2, 6]), (4, [1, 2, 4, 6]), (5, [1, 2, 4, 5, 6]), (7, [0, 1, 2, 4, 5, 6, 7])):
+        assert choose(acc, 16, budget) == [want]
