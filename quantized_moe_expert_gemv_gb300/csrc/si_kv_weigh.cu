@@ -282,16 +282,21 @@ struct WeighWindowCfg {
     static constexpr int block = 256 * D * 2;                  // 256 rows of q: [D / 64][256 rows][128 bytes]
     static constexpr int tile = kTileRows * D * 2;
     static constexpr int k = 2 * block;
-    static constexpr int lse = k + 2 * tile;                   // [512] -lse log2 e
-    static constexpr int keyf = lse + kWwRows * 4;             // [4][128]
+    static constexpr int lse = k + 2 * tile;                   // [512] -lse log2 e, then [512] each row's factor
+    static constexpr int keyf = lse + 2 * kWwRows * 4;         // [4][128]
     static constexpr int part = keyf + 4 * 128 * 4;            // [2][128]
     static constexpr int bars = part + 2 * 128 * 4;
     static constexpr int smem = bars + 16 * 8 + 1024;
 };
 enum WindowBar { kXbQ = 0, kXbKFull = 1, kXbKEmpty = 3, kXbSFull = 5, kXbSEmpty = 9, kXbNever = 13 };
 
-// 128 columns of a lane's token: 2^(kf S - lse), added up.  MASK: columns below r_min see nothing of it.
-template <bool MASK>
+// The rows of a segment have one power of two where their largest values lie within 2^8 of one another (a score is then off
+// by less than 2^-23 of what the row's largest value makes of it, as much as its sum in 32 bits); else each its own, and a
+// factor for each column.
+constexpr float kWindowApart = 256.0f;
+// 128 columns of a lane's token: 2^(kf S - lse), added up.  MASK: columns below r_min see nothing of it; APART: columns
+// have factors, behind the 512 lse.
+template <bool MASK, bool APART>
 __device__ __forceinline__ void window_sums(uint32_t ts, const float4 *rl, f32x2 kf2, int r_min, f32x2 &sum, f32x2 &sum1) {
     uint32_t z[2][32];
     tc::tmem_ld32(ts, z[0]);
@@ -303,9 +308,15 @@ __device__ __forceinline__ void window_sums(uint32_t ts, const float4 *rl, f32x2
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
             const float4 l = rl[8 * e + k / 4];
+            f32x2 f0 = kf2, f1 = kf2;
+            if constexpr (APART) {
+                const float4 f = rl[kWwRows / 4 + 8 * e + k / 4];
+                f0 = mul2(kf2, pk2(f.x, f.y));
+                f1 = mul2(kf2, pk2(f.z, f.w));
+            }
             float w[4];
-            up2(fma2(pk2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), kf2, pk2(l.x, l.y)), w[0], w[1]);
-            up2(fma2(pk2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), kf2, pk2(l.z, l.w)), w[2], w[3]);
+            up2(fma2(pk2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), f0, pk2(l.x, l.y)), w[0], w[1]);
+            up2(fma2(pk2(__uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])), f1, pk2(l.z, l.w)), w[2], w[3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 w[i] = ex2(w[i]);
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
     using Cfg = WeighWindowCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t s_tmem;
-    __shared__ uint32_t s_top;  // the rows' largest magnitude (bits)
+    __shared__ uint32_t s_top, s_low;  // the largest and the smallest of the rows' largest magnitudes (bits; without zeros)
     const Ctx &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform)
     const bool bf16 = a.bf16;
@@ -354,6 +365,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
         mbar_init(bar(kXbNever), 1);
         fence_mbar_init();
         s_top = 0;
+        s_low = 0x7f800000;
     }
     if (warp == 12) {
         tc::tmem_alloc(smem_addr(&s_tmem), 512);
@@ -427,13 +439,14 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                 }
                 continue;
             }
-            // the rows' values times one power of two (a score is off by less than 2^-32 of the block's largest),
-            // a row that is not finite as zeros with the lse NaN
+            // the rows' values times a power of two (one for all, if they are of a size), a row that is not finite as
+            // zeros with the lse NaN
             const int passes = (p.rows + 255) / 256 * 4;  // of 64 rows, to the end of the last block
             auto row_ptr = [&](int r) -> const uint16_t * {
                 return a.q.p + (p.s.row0 + r / c.G) * a.q.row + (p.h * c.G + r % c.G) * a.q.head;
             };
-            uint32_t top = 0, fine = 0;  // a bit a pass
+            uint32_t top = 0, low = 0x7f800000, fine = 0;  // a bit a pass
+            float *rowf = lse_s + kWwRows;  // first each row's largest, then its factor
             auto place = [&](int r, int q, int e) {
                 const int unit = 2 * (ch + 4 * q) + e;
                 return base + (r >> 8) * Cfg::block + (unit >> 3) * 32768 + (r & 255) * 128 + (((unit ^ r) & 7) << 4);
@@ -460,6 +473,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                     if (m <= 3.4e38f) {
                         top = max(top, __float_as_uint(m));
+                        if (m > 0.0f) low = min(low, __float_as_uint(m));
                         fine |= 1u << (k0 + k);
                     }
 #pragma unroll
@@ -467,19 +481,32 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             sts128(place(r, q, e), v[k].y[q][e].x, v[k].y[q][e].y, v[k].y[q][e].z, v[k].y[q][e].w);
-                    if (ch == 0)  // (a row that pads weighs nothing)
+                    if (ch == 0) {  // (a row that pads weighs nothing)
                         lse_s[r] = m <= 3.4e38f ? -l[k] * kLog2e : __int_as_float(0x7fc00000);
+                        rowf[r] = m;
+                    }
                 }
             }
-            for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (lane == 0) atomicMax(&s_top, top);  // (a maximum: the order does not matter)
+            top = __reduce_max_sync(0xffffffffu, top);
+            low = __reduce_min_sync(0xffffffffu, low);
+            if (lane == 0) {  // (extremes: the order does not matter)
+                atomicMax(&s_top, top);
+                atomicMin(&s_low, low);
+            }
             softmax_sync();
             // ... then each thread's own places scaled
             float mul, f;
             row_scale(__uint_as_float(s_top), mul, f);
+            const bool apart = __uint_as_float(s_top) * (1.0f / kWindowApart) > __uint_as_float(s_low);
             for (int k = 0; k < passes; ++k) {
                 const int r = 64 * k + (tid >> 2);
-                const float by = fine >> k & 1 ? mul : 0.0f;
+                float by = fine >> k & 1 ? mul : 0.0f;
+                if (apart) {
+                    float own;
+                    row_scale(rowf[r], by, own);
+                    __syncwarp();
+                    if (ch == 0) rowf[r] = own;
+                }
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q)
 #pragma unroll
@@ -491,10 +518,10 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
             }
             tc::fence_proxy_async_smem();
             softmax_sync();
-            if (tid == 0) s_top = 0;  // (read by everyone; its next use is a barrier away)
+            if (tid == 0) s_top = 0, s_low = 0x7f800000;  // (read by everyone; their next use is a barrier away)
             mbar_arrive(bar(kXbQ));
             const int blocks = blocks_of(p);
-            const float scale = f * a.scale2;
+            const float scale = (apart ? 1.0f : f) * a.scale2;
             // (a warp whose wait ran out goes on through the tiles, without waits, for the barriers' sake)
             for (int t = p.first; t < p.end; ++t, ++tile_no) {
                 const int token = t * kTileRows + (tid & 127), r_min = max(0, token - p.old) * c.G;
@@ -512,10 +539,12 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                     const f32x2 kf2 = pk2(kf, kf);
                     const int r0 = q * 128;
                     const float4 *rl = reinterpret_cast<const float4 *>(lse_s + r0);
-                    if (__all_sync(0xffffffffu, r0 >= r_min))
-                        window_sums<false>(ts + quarter * 128, rl, kf2, 0, sum, sum1);
+                    if (apart)
+                        window_sums<true, true>(ts + quarter * 128, rl, kf2, r_min - r0, sum, sum1);
+                    else if (__all_sync(0xffffffffu, r0 >= r_min))
+                        window_sums<false, false>(ts + quarter * 128, rl, kf2, 0, sum, sum1);
                     else
-                        window_sums<true>(ts + quarter * 128, rl, kf2, r_min - r0, sum, sum1);
+                        window_sums<true, false>(ts + quarter * 128, rl, kf2, r_min - r0, sum, sum1);
                     tc::fence_before_sync();
                     mbar_arrive(bar(kXbSEmpty + quarter));
                 }

@@ -274,3 +274,56 @@ def test_evict_sums_that_are_not_finite():
     acc[0, 96], acc[0, 97] = math.inf, -math.inf  # page 6: NaN
     for budget, want in ((1, [2]), (2, [2, 6]), (3, [1, 2, 6]), (4, [1, 2, 4, 6]), (5, [1, 2, 4, 5, 6]), (7, [0, 1, 2, 4, 5, 6, 7])):
         assert choose(acc, 16, budget) == [want]
+
+
+@pytest.mark.parametrize("apart", [2, 20, 30, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_weigh_a_window_of_rows_of_very_different_size(dtype, apart):
+    """Each row keeps its bits beside one 2^apart as large.  (The large row has its values where the keys are zero, so that
+    every score is of the order of one.)"""
+    if dtype == "f16" and apart > 14:
+        apart = 14
+    shape = Shape(8, 2, 128, 32, "int8", dtype)
+    c = ref.make_cache(shape, [400, 130], [32, 17], seed=4)
+    for n in ("k_codes", "k_tail"):
+        c.t[n][..., :32] = 0
+    q, _ = make_q(c, 6)
+    q[:, :, :32] = 0
+    for row, head in ((3, 1), (20, 6), (40, 0)):
+        q[row, head] = 0
+        q[row, head, :32] = 2.0 ** apart
+    d = Dev(c)
+    sm = 128 ** -0.5
+    _, lse, _, _ = ref.attend(c, q, sm)
+    lse = lse.float()
+    want, A = ref.weigh(c, q, lse, None, 1.0, sm)
+    out = torch.zeros((2, 2, 400), device=DEV)
+    si.si_kv_weigh(d.plan, d.cache, d.batch, q.to(DEV), lse.to(DEV), None, out, 1.0, sm, d.scratch)
+    got = out.cpu().double()
+    for b, L in enumerate(c.lens):
+        w = want[b, :, :L]
+        assert ((got[b, :, :L] - w).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * w).all()
+    assert d.status() == si.SI_OK
+
+
+def test_weigh_a_window_with_rows_that_are_not_finite_or_zero():
+    """A row with an infinity makes NaN of what it sees, in its kv head alone; rows of zeros weigh all tokens alike."""
+    shape = Shape(8, 2, 64, 16, "e4m3", "bf16")
+    c = ref.make_cache(shape, [200], [40], seed=4)
+    q, _ = make_q(c, 6)
+    q[5:9] = 0
+    lse = ref.attend(c, q, 0.125)[1].float()
+    want, A = ref.weigh(c, q, lse, None, 1.0, 0.125)
+    d = Dev(c)
+    out = torch.zeros((1, 2, 200), device=DEV)
+    for bad in (None, math.inf, math.nan):
+        if bad is not None:
+            q[10, 1, 3] = bad
+        si.si_kv_weigh(d.plan, d.cache, d.batch, q.to(DEV), lse.to(DEV), None, out, 1.0, 0.125, d.scratch)
+        got = out.cpu().double()
+        close = (got - want).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * want
+        assert close[0, 1].all()
+        if bad is None:
+            assert close[0, 0].all()
+        else:
+            assert torch.isnan(got[0, 0, :171]).all() and close[0, 0, 171:].all()
