@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R8>::warps * 32, DecodeCfg<D, R8>
                 p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
                 ks = vs = __int_as_float(0x7fc00000);
                 if (p >= 0) {
-                    ks = __ldg(c.ks + (int64_t)p * c.Hk + h);
-                    vs = __ldg(c.vs + (int64_t)p * c.Hk + h);
+                    ks = c.ks[(int64_t)p * c.Hk + h];
+                    vs = c.vs[(int64_t)p * c.Hk + h];
                 }
                 p = max(p, 0);  // (not one of the cache's pages: the first one's codes, and NaN for what sees them)
             }

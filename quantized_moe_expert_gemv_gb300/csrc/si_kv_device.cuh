@@ -12,7 +12,8 @@ namespace si {
 namespace kv {
 
 // The start of every kernel: the next one may be launched, and this one goes on once the one before it
-// in the stream has ended.
+// in the stream has ended.  What it reads may thus be written while it is already there, so no load of the cache,
+// the tables or the lse may be one of memory that stays as it is for the kernel's life (ld.global.nc, __ldg).
 __device__ __forceinline__ void start_after() {
     pdl_launch_dependents();
     pdl_wait();

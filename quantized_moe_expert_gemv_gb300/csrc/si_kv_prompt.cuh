@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
                 const uint8_t *at = (v ? v_own : k_own) + row_at((uint32_t)info.page[(r0 >> 4) + 2 * k], k);
 #pragma unroll
                 for (int q = 0; q < CC; ++q) {
-                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + 64 * q));
+                    const uint4 y = *reinterpret_cast<const uint4 *>(at + 64 * q);
                     if (v)
                         vx[k * CC + q] = y;
                     else
@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_kv_prompt(const PromptArgs a)
             if (lane >= 8 || j >= nt || key0 + kPrKeys > paged) return;
             const int64_t p = load_page(c, b, (key0 + 16 * lane) >> a.log_page);
             page = p < 0 ? 0 : (int)p;
-            ks = p < 0 ? __int_as_float(0x7fc00000) : __ldg(c.ks + p * c.Hk + h);
-            vs = p < 0 ? __int_as_float(0x7fc00000) : __ldg(c.vs + p * c.Hk + h);
+            ks = p < 0 ? __int_as_float(0x7fc00000) : c.ks[p * c.Hk + h];
+            vs = p < 0 ? __int_as_float(0x7fc00000) : c.vs[p * c.Hk + h];
         };
         int page = 0;
         float ks = 0.0f, vs = 0.0f;

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::warps * 32, WeighCfg<D>::ctas) k_
                 float f = 0.0f;
                 if (i < count) {
                     p = (int)load_page(c, b, (p_first + W * i) >> (a.log_page - 4));
-                    f = p >= 0 ? __ldg(c.ks + (int64_t)p * c.Hk + h) : __int_as_float(0x7fc00000);
+                    f = p >= 0 ? c.ks[(int64_t)p * c.Hk + h] : __int_as_float(0x7fc00000);
                     p = max(p, 0);  // (not one of the cache's pages: the first one's codes, and NaN for their weights)
                 }
                 if (set) {
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                     const int r = 64 * (k0 + k) + (tid >> 2);
                     v[k].load(r < p.rows ? row_ptr(r) : a.q.p, r < p.rows, ch);
                     l[k] = ch == 0 && r < p.rows
-                               ? __ldg(a.lse + (int64_t)(p.s.row0 + r / c.G) * c.H + p.h * c.G + r % c.G) : INFINITY;
+                               ? a.lse[(int64_t)(p.s.row0 + r / c.G) * c.H + p.h * c.G + r % c.G] : INFINITY;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
             auto pages = [&](int t) {
                 if (t >= p.end || !whole(t)) return;
 #pragma unroll
-                for (int k = 0; k < 5; ++k) pg[k] = __ldg(table + ((t * kTileRows + (k < 4 ? r0 + 32 * k : pt)) >> a.log_page));
+                for (int k = 0; k < 5; ++k) pg[k] = table[(t * kTileRows + (k < 4 ? r0 + 32 * k : pt)) >> a.log_page];
             };
             auto load = [&](int t) {
                 if (t >= p.end || !whole(t)) return;
@@ -580,9 +580,9 @@ __global__ void __launch_bounds__(kWwThreads, 1) k_kv_weigh_window(const WeighAr
                 for (int k = 0; k < 4; ++k) {
                     const uint8_t *from = c.kc + page_at(c, named(pg[k]) ? pg[k] : 0, p.h) + ((r0 + 32 * k) & (c.P - 1)) * D + ch * 16;
 #pragma unroll
-                    for (int q = 0; q < CC; ++q) kx[k * CC + q] = __ldg(reinterpret_cast<const uint4 *>(from + 64 * q));
+                    for (int q = 0; q < CC; ++q) kx[k * CC + q] = *reinterpret_cast<const uint4 *>(from + 64 * q);
                 }
-                kfx = __ldg(c.ks + (int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + p.h);
+                kfx = c.ks[(int64_t)(named(pg[4]) ? pg[4] : 0) * c.Hk + p.h];
                 if (!named(pg[4])) {
                     set_status(c.status, SI_ERR_DEVICE);
                     kfx = __int_as_float(0x7fc00000);

@@ -327,3 +327,44 @@ def test_weigh_a_window_with_rows_that_are_not_finite_or_zero():
             assert close[0, 0].all()
         else:
             assert torch.isnan(got[0, 0, :171]).all() and close[0, 0, 171:].all()
+
+
+# ------------------------------------------------------------------ calls in a row
+@pytest.mark.parametrize("code,dim", [("int8", 128), ("e4m3", 64)])
+def test_steps_in_a_row_are_the_steps_one_by_one(code, dim):
+    """Append, attend and weigh of 80 steps without a wait between them (each kernel starts while the one before it ends)
+    give what they give with a wait after every call."""
+    shape = Shape(8, 4, dim, 16, code, "bf16")
+    B, steps = 40, 80
+    lens = [20 + 11 * b for b in range(B)]
+    g = torch.Generator().manual_seed(2)
+    kv = torch.randn((steps, B, 8, dim), generator=g).bfloat16().to(DEV)
+    q = torch.randn((steps, B, 8, dim), generator=g).bfloat16().to(DEV)
+
+    def run(wait):
+        c = ref.make_cache(shape, lens, [steps] * B, seed=5, empty=True)
+        c.news = [1] * B
+        most = max(lens) + steps
+        d = Dev(c, max_len=most)
+        outs, acc = [], torch.zeros((B, 4, most), device=DEV)
+        before, after = d.lens, torch.empty_like(d.lens)
+        for i in range(steps):
+            b0 = si.kv_batch(B, B, 1, most, d.q_start, before, d.table, d.slots)
+            b1 = si.kv_batch(B, B, 1, most, d.q_start, after, d.table, d.slots)
+            out, lse = torch.empty_like(q[i]), torch.empty((B, 8), device=DEV)
+            outs += [out, lse]
+            si.si_kv_append(d.plan, d.cache, b0, kv[i, :, :4], kv[i, :, 4:], after, d.scratch)
+            if wait:
+                torch.cuda.synchronize()
+            si.si_kv_attend(d.plan, d.cache, b1, q[i], out, lse, 0.1, d.scratch)
+            if wait:
+                torch.cuda.synchronize()
+            si.si_kv_weigh(d.plan, d.cache, b1, q[i], lse, acc, acc, 0.9, 0.1, d.scratch)
+            if wait:
+                torch.cuda.synchronize()
+            before, after = after, before
+        assert d.status() == si.SI_OK
+        return outs + [acc, before]
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(run(False), want))
