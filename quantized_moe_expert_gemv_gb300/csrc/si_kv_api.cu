@@ -304,7 +304,8 @@ si_status si_kv_read_status(si_kv_plan_t plan, const void *scratch, si_stream_t 
     SI_KV_TRY(launched(cudaStreamSynchronize((cudaStream_t)stream)));
     SI_KV_TRY(launched(cudaMemcpy(&word, scratch, sizeof(word), cudaMemcpyDeviceToHost)));
     if (word == 0) return SI_OK;
-    SI_KV_TRY(launched(cudaMemset(const_cast<void *>(scratch), 0, sizeof(word))));
+    // (cleared in the stream's order: a call that follows in it may report at once)
+    SI_KV_TRY(launched(cudaMemsetAsync(const_cast<void *>(scratch), 0, sizeof(word), (cudaStream_t)stream)));
     return (si_status)word;
 }
 

@@ -14,16 +14,21 @@ CSRC = os.path.join(ROOT, "quantized_moe_expert_gemv_gb300", "csrc")
 
 RECORD = """
 #include "si_kv.h"
-static int g_max_new = -1;
+#include <cstring>
+static int g_max_new = -1, g_word = 0, g_cleared_elsewhere = 0;
+static void *g_cleared_in = nullptr;
 extern "C" {
 int last_max_new() { return g_max_new; }
+void report(int word) { g_word = word; g_cleared_in = nullptr; g_cleared_elsewhere = 0; }
+void *cleared_in() { return g_cleared_in; }
+int cleared_elsewhere() { return g_cleared_elsewhere; }
 cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int) {
     *v = a == cudaDevAttrMultiProcessorCount ? 152 : a == cudaDevAttrClockRate ? 2000000 : 232448;
     return cudaSuccess;
 }
-cudaError_t cudaMemsetAsync(void *, int, size_t, cudaStream_t) { return cudaSuccess; }
-cudaError_t cudaMemset(void *, int, size_t) { return cudaSuccess; }
-cudaError_t cudaMemcpy(void *, const void *, size_t, cudaMemcpyKind) { return cudaSuccess; }
+cudaError_t cudaMemsetAsync(void *, int, size_t, cudaStream_t s) { g_cleared_in = s; g_word = 0; return cudaSuccess; }
+cudaError_t cudaMemset(void *, int, size_t) { g_cleared_elsewhere = 1; g_word = 0; return cudaSuccess; }
+cudaError_t cudaMemcpy(void *to, const void *, size_t, cudaMemcpyKind) { std::memcpy(to, &g_word, 4); return cudaSuccess; }
 cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaGetLastError() { return cudaSuccess; }
 }
@@ -150,4 +155,15 @@ def test_overlap_of_any_strides(recorder):
         assert call(recorder, "attend") == want, (rows, row, head, apart)
         seen.add((brute(out, 64), meets))
     assert len(seen) == 4
+    recorder.si_kv_plan_destroy(plan.handle)
+
+
+def test_the_status_is_cleared_in_the_callers_stream(recorder):
+    """A clear in another stream could come after what the stream's next call reports."""
+    recorder.cleared_in.restype = ctypes.c_void_p
+    plan = host_plan(recorder, 8, 2, 128, 64)
+    recorder.report(binding.SI_ERR_DEVICE)
+    assert recorder.si_kv_read_status(plan.handle, 0x10000, 0x5000) == binding.SI_ERR_DEVICE
+    assert recorder.cleared_in() == 0x5000 and not recorder.cleared_elsewhere()
+    assert recorder.si_kv_read_status(plan.handle, 0x10000, 0x5000) == binding.SI_OK
     recorder.si_kv_plan_destroy(plan.handle)
