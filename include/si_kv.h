@@ -145,7 +145,9 @@ si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
  * for t < lens[b]; entries past that are not written.  The call's own tokens
  * (the last n_b) have no earlier sum: acc_in is read for t < lens[b] - n_b
  * only, and may be NULL (no earlier sums at all).  q and lse are those of
- * si_kv_attend, or of a prompt's last rows alone.  acc_in, acc_out:
+ * si_kv_attend, or of a prompt's last rows alone: then the prompt's tokens before
+ * those rows count as old, and the caller zeroes their entries of acc_in first
+ * (si_kv_evict leaves old sums past its new lengths).  acc_in, acc_out:
  * [n_seqs][Hkv][acc_stride] fp32, acc_stride >= max_len; they may be the same
  * array.  The sums are taken in a fixed order (the same inputs give the same
  * bits). */

@@ -120,14 +120,15 @@ class DecoderLayer:
         last = [min(n, self.window) for n in counts]
         if last != list(counts):
             at, rows = 0, []
-            for n, m in zip(counts, last):
+            for b, (n, m) in enumerate(zip(counts, last)):
                 rows += range(at + n - m, at + n)
                 at += n
+                # new tokens before the window have no earlier sum: what lies in their place is an evicted one's
+                self.acc[b, :, self.host_lens[b] - n:self.host_lens[b] - m] = 0
             rows = torch.tensor(rows, device=self.dev)
             q, lse = q[rows], lse[rows]
-        first = not self.acc.any() if max(counts) > 1 else False
-        si.si_kv_weigh(self.plan, self.cache, self._batch(last, self.lens), q, lse, None if first else self.acc, self.acc,
-                       self.decay, self.sm, scratch)
+        si.si_kv_weigh(self.plan, self.cache, self._batch(last, self.lens), q, lse, self.acc, self.acc, self.decay, self.sm,
+                       scratch)
 
     def evict(self) -> bool:
         """Back to the budget, where a sequence is past it: the kept pages move to fresh ones, the old ones are free."""
