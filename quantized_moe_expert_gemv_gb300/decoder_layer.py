@@ -60,16 +60,12 @@ class DecoderLayer:
         self.host_lens = [0] * n_seqs                   # the same on the host, which hands out the pages
         self.positions = [0] * n_seqs                   # tokens seen, evicted ones among them
         self.acc, self.acc_next = (torch.zeros((n_seqs, kv, max_len), device=dev) for _ in range(2))
-        self.scratch = torch.empty(0, dtype=torch.uint8, device=dev)
+        # scratch for the largest call, once: the errors that the device reports lie in it until they are read
+        need = si.si_kv_scratch_bytes(self.plan, n_seqs, n_seqs * max_len, max_len, max_len)
+        self.scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        si.si_kv_scratch_init(self.plan, self.scratch)
 
     # ---------------------------------------------------------------- pieces
-    def _scratch(self, rows: int, most: int) -> torch.Tensor:
-        need = si.si_kv_scratch_bytes(self.plan, self.n, rows, most, self.max_len)
-        if self.scratch.numel() < need:
-            self.scratch = torch.empty(need, dtype=torch.uint8, device=self.dev)
-            si.si_kv_scratch_init(self.plan, self.scratch)
-        return self.scratch
-
     def _batch(self, counts, lens) -> si.si_kv_batch:
         starts = [0]
         for n in counts:
@@ -102,20 +98,19 @@ class DecoderLayer:
         q, k, v = qk[:, :h], qk[:, h:], qkv[:, h + kv:]   # strided views: no copies
 
         self._reserve(counts)
-        scratch = self._scratch(rows, max(counts))
-        si.si_kv_append(self.plan, self.cache, self._batch(counts, self.lens), k, v, self.lens_next, scratch)
+        si.si_kv_append(self.plan, self.cache, self._batch(counts, self.lens), k, v, self.lens_next, self.scratch)
         self.lens, self.lens_next = self.lens_next, self.lens
         for b, n in enumerate(counts):
             self.host_lens[b] += n
             self.positions[b] += n
         out = torch.empty((rows, h, d), dtype=torch.bfloat16, device=self.dev)
         lse = torch.empty((rows, h), device=self.dev)
-        si.si_kv_attend(self.plan, self.cache, self._batch(counts, self.lens), q, out, lse, self.sm, scratch)
-        self._weigh(counts, q, lse, scratch)
+        si.si_kv_attend(self.plan, self.cache, self._batch(counts, self.lens), q, out, lse, self.sm, self.scratch)
+        self._weigh(counts, q, lse)
         self.last = (q, out, lse)
         return x + torch.nn.functional.linear(out.view(rows, h * d), self.w_out)
 
-    def _weigh(self, counts, q, lse, scratch) -> None:
+    def _weigh(self, counts, q, lse) -> None:
         """The weights that each sequence's last rows (a window of a prompt, or the step's one) gave the cache."""
         last = [min(n, self.window) for n in counts]
         if last != list(counts):
@@ -128,7 +123,7 @@ class DecoderLayer:
             rows = torch.tensor(rows, device=self.dev)
             q, lse = q[rows], lse[rows]
         si.si_kv_weigh(self.plan, self.cache, self._batch(last, self.lens), q, lse, self.acc, self.acc, self.decay, self.sm,
-                       scratch)
+                       self.scratch)
 
     def evict(self) -> bool:
         """Back to the budget, where a sequence is past it: the kept pages move to fresh ones, the old ones are free."""

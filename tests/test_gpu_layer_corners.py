@@ -45,3 +45,14 @@ def test_a_second_prompt_starts_without_sums():
             assert ((got - w).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * w + 1e-12).all(), b
     layer.evict = evict
     assert layer.evict() and layer.status() == 0
+
+
+def test_an_error_before_a_larger_call_is_still_reported():
+    from quantized_moe_expert_gemv_gb300 import binding as si
+    layer = tiny()
+    layer.attention(rows(60, 1), [20, 20, 20])
+    layer.table[1, 0] = 10 ** 6
+    layer.attention(rows(3, 2), [1, 1, 1])
+    layer.table[1, 0] = layer.pages[1][0]
+    layer.attention(rows(400, 3), [150, 130, 120])
+    assert layer.status() == si.SI_ERR_DEVICE and layer.status() == si.SI_OK
