@@ -22,7 +22,6 @@ struct Plan {
     si_kv_desc desc;
     int device;
     int sm_count;
-    int smem_optin;
     long long wait_budget;  // SM cycles a device-side wait may spin before reporting SI_ERR_TIMEOUT
     bool fault_wait;        // test mode: the many-row attention first waits on a barrier nothing arrives at
 };

@@ -164,9 +164,8 @@ si_status si_kv_plan(const si_kv_desc *desc, int cuda_device, si_kv_plan_t *out)
     if (!out) return SI_ERR_INVALID_ARG;
     *out = nullptr;
     SI_KV_TRY(validate_desc(desc));
-    int sms = 0, smem = 0, khz = 0;
+    int sms = 0, khz = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, cuda_device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, cuda_device) != cudaSuccess ||
         cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, cuda_device) != cudaSuccess) {
         cudaGetLastError();
         return SI_ERR_CUDA;
@@ -176,7 +175,6 @@ si_status si_kv_plan(const si_kv_desc *desc, int cuda_device, si_kv_plan_t *out)
     h->p.desc = *desc;
     h->p.device = cuda_device;
     h->p.sm_count = sms;
-    h->p.smem_optin = smem;
     h->p.wait_budget = khz > 0 ? (long long)khz * 1000 : 2000000000ll;  // about one second
     // SI_FAULT_WAIT_BUDGET as for si_moe_plan: its cycle count is the budget, and a wait runs out for certain
     h->p.fault_wait = false;
