@@ -93,7 +93,8 @@ typedef struct si_kv_batch {
 
 /* A 16-bit [rows][heads][D] operand: element (r, h, d) is at r*row_stride +
  * h*head_stride + d (strides in elements, multiples of 8), so the three parts
- * of a fused projection need no copy. */
+ * of a fused projection need no copy.  data (and si_kv_weigh's lse) may be NULL
+ * where total_new is 0. */
 typedef struct si_kv_rows {
     void *data;
     int64_t row_stride;

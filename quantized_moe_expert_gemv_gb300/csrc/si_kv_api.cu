@@ -77,8 +77,9 @@ si_status check_batch(const Plan &p, const si_kv_batch *b, bool rows) {
     return SI_OK;
 }
 
-si_status check_rows(const Plan &p, const si_kv_rows *r, bool written) {
-    if (!r || !r->data) return SI_ERR_INVALID_ARG;
+// (without rows there may be no data)
+si_status check_rows(const Plan &p, const si_kv_rows *r, const si_kv_batch *b, bool written) {
+    if (!r || (!r->data && b->total_new > 0)) return SI_ERR_INVALID_ARG;
     if (r->row_stride < 0 || r->head_stride < 0) return SI_ERR_INVALID_ARG;
     if (written && (r->row_stride < p.desc.head_dim || r->head_stride < p.desc.head_dim)) return SI_ERR_INVALID_ARG;
     if (!aligned(r->data, 16) || r->row_stride % 8 || r->head_stride % 8) return SI_ERR_MISALIGNED;
@@ -213,8 +214,8 @@ si_status si_kv_append(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
     if (!plan || !lens_out) return SI_ERR_INVALID_ARG;
     SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, true));
-    SI_KV_TRY(check_rows(plan->p, k, false));
-    SI_KV_TRY(check_rows(plan->p, v, false));
+    SI_KV_TRY(check_rows(plan->p, k, batch, false));
+    SI_KV_TRY(check_rows(plan->p, v, batch, false));
     if (!aligned(lens_out, 4)) return SI_ERR_MISALIGNED;
     const size_t n = (size_t)batch->n_seqs * sizeof(int32_t);
     if (overlap(lens_out, n, batch->lens, n)) return SI_ERR_INVALID_ARG;
@@ -241,8 +242,8 @@ si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
     if (!plan || !(sm_scale >= 0.0f) || !std::isfinite(sm_scale)) return SI_ERR_INVALID_ARG;
     SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, true));
-    SI_KV_TRY(check_rows(plan->p, q, false));
-    SI_KV_TRY(check_rows(plan->p, out, true));
+    SI_KV_TRY(check_rows(plan->p, q, batch, false));
+    SI_KV_TRY(check_rows(plan->p, out, batch, true));
     if (!aligned(lse, 4)) return SI_ERR_MISALIGNED;
     SI_KV_TRY(check_scratch(plan->p, batch, scratch, scratch_bytes));
     if (batch->total_new == 0 || batch->max_new == 0) return SI_OK;
@@ -254,12 +255,12 @@ si_status si_kv_attend(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_
 si_status si_kv_weigh(si_kv_plan_t plan, const si_kv_cache *cache, const si_kv_batch *batch, const si_kv_rows *q,
                       const float *lse, const float *acc_in, float *acc_out, int64_t acc_stride, float decay,
                       float sm_scale, void *scratch, size_t scratch_bytes, si_stream_t stream) {
-    if (!plan || !lse || !acc_out || !(sm_scale >= 0.0f) || !std::isfinite(sm_scale) || !std::isfinite(decay))
+    if (!plan || !acc_out || !(sm_scale >= 0.0f) || !std::isfinite(sm_scale) || !std::isfinite(decay))
         return SI_ERR_INVALID_ARG;
     SI_KV_TRY(check_cache(cache));
     SI_KV_TRY(check_batch(plan->p, batch, true));
-    SI_KV_TRY(check_rows(plan->p, q, false));
-    if (acc_stride < batch->max_len) return SI_ERR_INVALID_ARG;
+    SI_KV_TRY(check_rows(plan->p, q, batch, false));
+    if (acc_stride < batch->max_len || (!lse && batch->total_new > 0)) return SI_ERR_INVALID_ARG;
     if (!aligned(lse, 4) || !aligned(acc_in, 4) || !aligned(acc_out, 4)) return SI_ERR_MISALIGNED;
     if (acc_in && acc_in != acc_out) {  // the same array, or arrays apart
         const size_t n = (size_t)batch->n_seqs * plan->p.desc.n_kv_heads * (size_t)acc_stride * sizeof(float);

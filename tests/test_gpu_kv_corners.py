@@ -368,3 +368,25 @@ def test_steps_in_a_row_are_the_steps_one_by_one(code, dim):
     want = run(True)
     for _ in range(3):
         assert all(torch.equal(x, y) for x, y in zip(run(False), want))
+
+
+# ------------------------------------------------------------------ no rows at all
+def test_calls_without_rows():
+    """Nothing appended, nothing attended, sums that only decay: empty tensors are taken."""
+    shape = Shape(4, 2, 64, 16, "int8", "bf16")
+    c = ref.make_cache(shape, [40, 0, 33], [0, 0, 0], seed=3)
+    d = Dev(c)
+    none = torch.empty((0, 4, 64), dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty((0, 4), device=DEV)
+    out = torch.full_like(d.lens, -7)
+    si.si_kv_append(d.plan, d.cache, d.batch, none[:, :2], none[:, 2:], out, d.scratch)
+    assert out.tolist() == c.lens
+    si.si_kv_attend(d.plan, d.cache, d.batch, none, torch.empty_like(none), lse, 0.1, d.scratch)
+    acc = torch.rand((3, 2, 40), device=DEV)
+    got = torch.full_like(acc, 9.0)
+    si.si_kv_weigh(d.plan, d.cache, d.batch, none, lse, acc, got, 0.5, 0.1, d.scratch)
+    for b, L in enumerate(c.lens):
+        assert torch.equal(got[b, :, :L], 0.5 * acc[b, :, :L]) and (got[b, :, L:] == 9.0).all()
+    assert d.status() == si.SI_OK
+    for t in (d.k_codes, d.v_codes):
+        assert torch.equal(t.cpu().view(torch.uint8), c.t["k_codes" if t is d.k_codes else "v_codes"].view(torch.uint8))

@@ -167,3 +167,20 @@ def test_the_status_is_cleared_in_the_callers_stream(recorder):
     assert recorder.cleared_in() == 0x5000 and not recorder.cleared_elsewhere()
     assert recorder.si_kv_read_status(plan.handle, 0x10000, 0x5000) == binding.SI_OK
     recorder.si_kv_plan_destroy(plan.handle)
+
+
+@pytest.mark.parametrize("name", ["append", "attend", "weigh"])
+def test_calls_without_rows_need_no_data(recorder, name):
+    """An empty tensor has no address."""
+    plan = host_plan(recorder, 8, 2, 128, 64)
+    for total, want in ((0, binding.SI_OK), (1, binding.SI_ERR_INVALID_ARG)):
+        call = Call(plan)
+        call.batch.total_new = total
+        call.rows.data = call.out.data = None
+        if name == "weigh":
+            call.a["lse"] = None
+        assert call(recorder, name) == want
+    if name == "weigh":
+        call.rows.data = 0x80000
+        assert call(recorder, name) == binding.SI_ERR_INVALID_ARG
+    recorder.si_kv_plan_destroy(plan.handle)
