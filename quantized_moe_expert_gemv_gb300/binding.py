@@ -444,9 +444,15 @@ def si_kv_plan_status(desc: si_kv_desc, cuda_device: int = 0) -> int:
 def kv_cache(k_codes, v_codes, k_scale, v_scale, k_tail, v_tail) -> si_kv_cache:
     """k_codes, v_codes [n_pages, Hkv, P, D] 8-bit; k_scale, v_scale [n_pages, Hkv] float32; k_tail, v_tail
     [n_slots, Hkv, 2P, D] 16-bit; all contiguous.  The structure keeps them alive."""
-    for t in (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail):
-        if not t.is_contiguous():
-            raise ValueError("the cache's tensors are contiguous")
+    tensors = (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail)
+    if not all(t.is_contiguous() for t in tensors):
+        raise ValueError("the cache's tensors are contiguous")
+    if [t.element_size() for t in tensors] != [1, 1, 4, 4, 2, 2]:
+        raise ValueError("codes have 8 bits, scales 32 and the rings 16")
+    n, heads, page, dim = k_codes.shape if k_codes.dim() == 4 else (0, 0, 0, 0)
+    if not (v_codes.shape == k_codes.shape and tuple(k_scale.shape) == tuple(v_scale.shape) == (n, heads)
+            and k_tail.shape == v_tail.shape and tuple(k_tail.shape[1:]) == (heads, 2 * page, dim)):
+        raise ValueError("codes [n_pages, Hkv, P, D], scales [n_pages, Hkv], rings [n_slots, Hkv, 2P, D]")
     c = si_kv_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail), _ptr(v_tail),
                     k_codes.shape[0], k_tail.shape[0])
     c.held = (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail)
@@ -458,6 +464,13 @@ def kv_batch(n_seqs, total_new, max_new, max_len, q_start, lens, page_table, slo
     (page_table's rows may be strided).  The structure keeps them alive."""
     if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table is [n_seqs, columns] with columns next to each other")
+    if any("int32" not in str(t.dtype) for t in (q_start, lens, page_table, slots) if t is not None):
+        raise ValueError("q_start, lens, page_table and slots are int32")
+    for t, n in ((q_start, n_seqs + 1), (lens, n_seqs), (slots, n_seqs)):
+        if t is not None and (t.dim() != 1 or t.shape[0] < n or not t.is_contiguous()):
+            raise ValueError("q_start [n_seqs + 1], lens [n_seqs] and slots [n_seqs], each contiguous")
+    if page_table.shape[0] < n_seqs:
+        raise ValueError("page_table has a row for each sequence")
     stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
     b = si_kv_batch(n_seqs, total_new, max_new, max_len, _ptr(q_start), _ptr(lens), _ptr(page_table), _ptr(slots),
                     stride)
@@ -471,6 +484,15 @@ def _rows(t) -> si_kv_rows:
     if len(strides) != 3 or strides[2] != 1:
         raise ValueError("q, k, v and out are [rows, heads, D] with D contiguous")
     return si_kv_rows(t.data_ptr(), strides[0], strides[1])
+
+
+def _sums(batch, acc_in, acc_out) -> int:
+    """The one stride of both arrays of sums."""
+    if not acc_out.is_contiguous() or acc_out.dim() != 3 or acc_out.shape[0] < batch.n_seqs:
+        raise ValueError("acc_out is [n_seqs, Hkv, acc_stride], contiguous")
+    if acc_in is not None and (acc_in.shape != acc_out.shape or not acc_in.is_contiguous()):
+        raise ValueError("acc_in has acc_out's shape, contiguous")
+    return acc_out.shape[2]
 
 
 def _nbytes(t) -> int:
@@ -548,9 +570,9 @@ def si_kv_attend(plan, cache: si_kv_cache, batch: si_kv_batch, q, out, lse, sm_s
 def si_kv_weigh(plan, cache: si_kv_cache, batch: si_kv_batch, q, lse, acc_in, acc_out, decay, sm_scale, scratch,
                 stream=None, raw_status=False):
     """acc_in (or None) and acc_out: [n_seqs, Hkv, acc_stride] float32, contiguous."""
+    stride = _sums(batch, acc_in, acc_out)
     st = _kv_fn("si_kv_weigh")(plan.handle, cache, batch, _rows(q), lse.data_ptr(), _opt(acc_in), acc_out.data_ptr(),
-                               acc_out.shape[2], decay, sm_scale, scratch.data_ptr(), _nbytes(scratch),
-                               _kv_stream(stream))
+                               stride, decay, sm_scale, scratch.data_ptr(), _nbytes(scratch), _kv_stream(stream))
     return _kv_done(st, "si_kv_weigh", raw_status)
 
 
@@ -558,7 +580,10 @@ def si_kv_evict(plan, cache: si_kv_cache, batch: si_kv_batch, acc_in, acc_out, b
                 new_slots, keep, lens_out, scratch, stream=None, raw_status=False):
     """new_table [n_seqs, budget], keep [n_seqs, Hkv, budget] int32; acc_in, acc_out [n_seqs, Hkv, acc_stride];
     new_slots [n_seqs] int32 or None (the batch's own)."""
-    st = _kv_fn("si_kv_evict")(plan.handle, cache, batch, acc_in.data_ptr(), acc_out.data_ptr(), acc_in.shape[2], budget,
+    stride = _sums(batch, acc_in, acc_out)
+    if not (new_table.is_contiguous() and keep.is_contiguous() and new_table.shape[-1] == keep.shape[-1] == budget):
+        raise ValueError("new_table [n_seqs, budget] and keep [n_seqs, Hkv, budget] are contiguous")
+    st = _kv_fn("si_kv_evict")(plan.handle, cache, batch, acc_in.data_ptr(), acc_out.data_ptr(), stride, budget,
                                sink, recent, new_table.data_ptr(), _opt(new_slots), keep.data_ptr(),
                                lens_out.data_ptr(), scratch.data_ptr(), _nbytes(scratch), _kv_stream(stream))
     return _kv_done(st, "si_kv_evict", raw_status)
