@@ -390,3 +390,23 @@ def test_calls_without_rows():
     assert d.status() == si.SI_OK
     for t in (d.k_codes, d.v_codes):
         assert torch.equal(t.cpu().view(torch.uint8), c.t["k_codes" if t is d.k_codes else "v_codes"].view(torch.uint8))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attend_and_weigh_a_chunk_among_steps(dim):
+    """One call with a chunk of a prompt, steps of 30 sequences, one of two tokens and one without any."""
+    shape = Shape(8, 2, dim, 32, "int8", "bf16")
+    lens = [700] + [17 * b + 1 for b in range(30)] + [60, 45]
+    c = ref.make_cache(shape, lens, [90] + [1] * 30 + [2, 0], seed=5)
+    d = Dev(c)
+    q, qd = make_q(c, 6)
+    sm = dim ** -0.5
+    out, lse = d.attend(qd, sm)
+    check_attend(c, out, lse, q, sm)
+    acc = torch.full((33, 2, 700), 9.0, device=DEV)
+    si.si_kv_weigh(d.plan, d.cache, d.batch, qd, lse, None, acc, 1.0, sm, d.scratch)
+    want, A = ref.weigh(c, q, lse.cpu(), None, 1.0, sm)
+    for b, L in enumerate(lens):
+        w = want[b, :, :L]
+        assert ((acc[b, :, :L].cpu().double() - w).abs() <= (2.0 ** -16 * A + 2.0 ** -19) * w + 1e-12).all(), b
+    assert d.status() == si.SI_OK
