@@ -603,9 +603,12 @@ __global__ void __launch_bounds__(256) k_kv_join(const PromptArgs a) {
             hi = mid;
     }
     Seq s = load_seq(c, lo);
-    if (*c.status != SI_OK)
-        for (int b = 0; b < c.B && (row < s.row0 || row >= s.row0 + s.n); ++b) s = load_seq(c, b);
-    if (row < s.row0 || row >= s.row0 + s.n) return;
+    auto out = [&]() { return row < s.row0 || row >= s.row0 + s.n; };
+    if (out()) {
+        if (*c.status == SI_OK) return;
+        for (int b = 0; b < c.B && out(); ++b) s = load_seq(c, b);
+        if (out()) return;
+    }
     const float *ml = a.partial + (int64_t)a.splits * c.T * c.H * D;
     float m = kNoScore, l = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
