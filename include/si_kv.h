@@ -129,6 +129,8 @@ si_status si_kv_read(si_kv_plan_t plan, const si_kv_cache *cache, const int32_t 
 
 /* Causal attention of each sequence's last n_b tokens (lens counts them; they
  * have been appended): row i sees tokens 0 .. lens[b] - n_b + i.
+ * (The kernel goes by max_new: a chunk of a prompt and the steps of many other
+ * sequences are faster in two calls than in one.)
  * out[row][h] = sum_t softmax_t(sm_scale * q[row][h] . k_t) v_t, and, where lse
  * is not NULL, lse[row][h] = log sum_t exp(sm_scale * q . k_t) ([total_new]
  * [n_heads] fp32).  A row that sees no token (lens[b] < n_b) gives zeros and

@@ -20,10 +20,15 @@ static bool many_rows(const Plan &p, int max_new) {
 // makes the call shortest with, from bounds that the host has: the longest CTA,
 // the waves of CTAs over the SMs (a CTA an SM), the mean work; a key tile takes
 // 1.6 us, a wave's start and end 8, the join of parts 6 and 0.9 for each MB of
-// partial results.  Measured, one part against the chosen number: 300 new tokens
-// behind 20000, 8 heads: 249 and 58 us (8 parts); 512 behind 8000, 32 heads: 121 and
-// 86 us (2).  Where it stays at one part, two would take: 1349 new tokens, 16
-// heads: 47 instead of 36 us; 1024 behind 24000, 32 heads: 353 instead of 306.
+// partial results (measured at head_dim 128).  In a graph, int8, one part against
+// the chosen number: 300 new tokens behind 20000, 8/8 heads: 264 and 57 us (8 parts);
+// 512 behind 8000, 32/8 heads: 124 and 94 us (2).  Where it stays at one part, two would
+// take: 1349 new tokens, 16/8 heads: 51 instead of 33 us; 1024 behind 24000, 32/8 heads:
+// 376 instead of 343, and 289 instead of 277 at head_dim 64.
+// The estimate takes the call's rows as full blocks of kPrRows.  A call of one chunk and
+// many steps has more CTAs than that, each nearly empty, and is better made as two: 512 new
+// tokens behind 8000 and a token of each of 63 sequences of 8000, 32/8 heads, took 551 us in
+// one call and 286 in two.
 // The partial results are bounded: kPartialRows rows (query heads counted) for an SM.
 constexpr int kMaxSplits = 32, kPartialRows = 4 * kPrRows;
 static int prompt_splits(const Plan &p, int total_new, int max_new, int max_len) {

@@ -13,9 +13,9 @@
 // bytes a cycle and SM at the measured copy rate.  Measured (head_dim 128, bytes
 // that cannot be spared over the time): 64 sequences of 200 to 16300 tokens, 32/8
 // heads, 177 us, 88 % of the copy rate.  Two of 90000 to 131000, 64/8 heads of 64,
-// 55 us, 73 %.  24 of up to 6000 with 2 to 6 new tokens, 16/8 heads of 256, where
-// the sums' registers leave half the warps: 80 us, 60 %.  Short calls are latency:
-// 12.0 us for one sequence of 1000 tokens (11.7 in a graph): start and lengths 2,
+// 54 us, 75 %.  24 of up to 6000 with 2 to 6 new tokens, 16/8 heads of 256, where
+// the sums' registers leave half the warps: 84 us, 58 %.  Short calls are latency:
+// 12.1 us for one sequence of 1000 tokens (11.7 in a graph): start and lengths 2,
 // pages and codes 2, a warp's and the CTA's sums 4, the join of 16 CTAs 3.
 //  * Products: keys are the 16 rows of the warp-level product and q's rows its 8
 //    columns (S^T = K Q^T, then O^T = V^T P^T), so a step of 8 query heads for
@@ -35,7 +35,7 @@
 //  * The maximum is lazy: m moves only when a score passes it by more than 4
 //    (a vote a piece instead of shuffles), and p stays below 2^4.
 //  * p times the page's V scale is rounded to fp16 for the second product.  The
-//    scale is taken relative to the largest so far, so that the products stay
+//    scale is taken relative to the largest so far that the row sees, so that the products stay
 //    inside fp16: p < 2^4, scale/reference <= 1, times 2^11: at most 2^15; a
 //    weight of one keeps its eleven bits down to a relative scale of 2^-25.
 //    (bf16 weights, without the reference, have eight: half a step of the
@@ -138,8 +138,8 @@ struct Share {
     bool some_empty;
 };
 // Where items are short (`alone` units or fewer on average) there are no more CTAs than items, `items_of(b)` of
-// sequence b: an item in one CTA needs no join.  (One sequence, 4 kv heads: 9.4 instead of 11.8 us at 100
-// tokens, 14.7 instead of 13.7 us at 1000.)
+// sequence b: an item in one CTA needs no join.  (One sequence, 4 kv heads, in a graph: 8.1 us in one CTA an
+// item and 10.7 split at 100 tokens, 10.0 and 11.1 at 300; at 1000, where the rule splits, 13.7 and 11.9.)
 template <int WARPS, typename F, typename G>
 __device__ __forceinline__ Share take_share(int B, F units_of, G items_of, int alone) {
     __shared__ long long s_scan[WARPS];

@@ -14,9 +14,9 @@
 // no other sequence's lie or go.
 // Bound: HBM for the move (each kept byte read and written once); the choice reads
 // acc once and is a chain of block-wide steps.  Measured: 8 sequences of 20000 to
-// 32700 tokens, 8 heads of 128, down to 128 pages of 64: 136 us, 75 % of the copy
-// rate, with the kept pages read back (evict alone 73, of which 26 remain with a
-// budget of ten pages); one of 1500 tokens 8.5 us, two launches' latency.
+// 32700 tokens, 8 heads of 128, down to 128 pages of 64: 128 us, 80 % of the copy
+// rate, with the kept pages read back (evict alone 65, of which 25 remain with a
+// budget of ten pages); one of 1500 tokens 9 us, two launches' latency.
 #include "si_kv_device.cuh"
 
 namespace si {

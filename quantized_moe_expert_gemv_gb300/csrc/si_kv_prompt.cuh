@@ -12,7 +12,7 @@
 // warps 8-11 turn codes into fp16 tiles in shared memory (K with d innermost, V
 // with d innermost too: the second product takes V as its transposed operand);
 // warps 12 and 13 issue the two row tiles' products; warp 14 looks up pages and
-// scales ahead (warp 15 only lends its registers).  While one row tile's products
+// scales ahead, with the largest V scale up to each (warp 15 only lends its registers).  While one row tile's products
 // run, the other's softmax does.
 // Bound: at D = 128 a pair of row tiles and 128 keys takes 2048 cycles of the
 // tensor cores (32 steps of 128 x 128 x 16, 64 cycles each) beside 1024 of the
@@ -22,9 +22,9 @@
 // are equal.
 // Two row tiles a CTA: every K and V tile is made once for 256 rows; with 128 rows
 // the making (2 x 128 x D codes) alone would take as long as the products.
-// Measured (head_dim 128): prompts of 2900 to 4100 tokens, 32/4 heads, 244 us, 48 %
+// Measured (head_dim 128): prompts of 2900 to 4100 tokens, 32/4 heads, 253 us, 46 %
 // of the measured dense rate (causal products only); 1024 tokens behind 24000,
-// 32/8 heads, 311 us (E4M3) and 320 (int8), 69 %; one prompt of 300, 22 us, of which
+// 32/8 heads, 311 us (E4M3, 69 %) and 343 (int8, whose codes take longer to convert); one prompt of 300, 22 us, of which
 // the products are 3: the start, q and the tile with the unfinished page, whose
 // rows and factors come one by one, are the rest.
 #pragma once

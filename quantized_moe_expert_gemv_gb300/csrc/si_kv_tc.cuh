@@ -212,7 +212,8 @@ __device__ __forceinline__ float row_top(const uint32_t (&z)[4][32], const float
 // up to 2^-24 m from the score that became m, nothing where m is small, but 2^30 would leave no weight or an infinite
 // one.  So rows past kFar (`far`: the warp has one) take the form with MASK, which rounds the product first.  (A packed
 // product and a packed sum in turn were measured to be joined into one step, hence the zero.  A third form for such
-// rows costs all others registers: prompts 255 to 290 us, with the sum in this form 249, without it 243.)
+// rows costs all others registers: the prompts of si_kv_prompt.cuh took 255 to 290 us, with the sum in this form 249,
+// without either 243.)
 constexpr float kFar = 1048576.0f;
 template <bool MASK>
 __device__ __forceinline__ void row_weights(const uint32_t (&z)[4][32], const float *kf, const float *vf, float qf, float v_inv,

@@ -15,12 +15,12 @@
 // tensor cores, 128 tokens by 128 rows; all of q's rows stay in shared memory while
 // the CTA's share of a kv head's tokens goes by, and a thread holds one token's sum
 // and walks every other block's columns in tensor memory.  Measured: 512 rows a kv
-// head over 4 sequences of 9000 to 16000 tokens, 4 kv heads of 128, 38 us, where the
+// head over 4 sequences of 9000 to 16000 tokens, 4 kv heads of 128, 39 us, where the
 // products alone need 14: q's rows into shared memory 4 us a segment (two a CTA), a
 // tile 2500 cycles of exponentials and sums (five a score and scheduler) of 3900.
 // Many rows (k_kv_weigh_many): one CTA for 128 tokens, whose K tile stays while
 // q's tiles of 128 rows follow each other through two stages; for 512 rows it
-// took 117 us where the window kernel takes a third (most of it in a CTA's start).
+// takes 112 us where the window kernel takes 39 (most of it in a CTA's start).
 #include "si_kv_decode.cuh"
 #include "si_kv_tc.cuh"
 
@@ -40,6 +40,8 @@ struct WeighArgs {
 
 // The barrier of the window kernel's softmax warps.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+// Tiles that a segment's start counts as in the window kernel's even split.  (512 rows a kv head over four sequences of
+// 12500 tokens, 4 kv heads: 43.1 us with 1, 38.7 with 3, 39.4 with 6.)
 constexpr int kWindowOver = 3;
 constexpr int kWeighRows = 64;  // rows whose operand lies in shared memory at a time
 
