@@ -151,7 +151,6 @@ def _handles(s):
         s["scales_out"] = torch.empty((kb, stride), device=DEV) if c["codes"] else None
         s["mats"] = [None if m is None else si.fp8_mat(m) for m in (s["x"], s["residual"], s["s_out"], s["y_out"])]
         s["rows"] = si.fp8_rows(s["codes_out"], s["scales_out"]) if c["codes"] else None
-        s["outputs"] = dict(residual=s["s_out"], y=s["y_out"], codes=s["codes_out"], scales=s["scales_out"][:, :t] if c["codes"] else None)
         return
     if c["op"] == "pack":
         s["codes_out"] = torch.empty((c["n"], k), dtype=E4M3, device=DEV)
@@ -177,7 +176,8 @@ def _own_norm(s):
     x, residual, s_out, y = s["mats"]
     t = s["case"]["rows"]
     s["si"].si_fp8_norm(s["plan"], x, residual, s["gain"], s["eps"], s_out, y, s["rows"], t)
-    return s["outputs"]
+    scales = s["scales_out"]
+    return dict(residual=s["s_out"], y=s["y_out"], codes=s["codes_out"], scales=None if scales is None else scales[:, :t])
 
 
 def _own_pack(s):
