@@ -69,6 +69,13 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, long l
     if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_spin(bar, parity, budget);
 }
+// The last phases of a ring of N barriers of which `n` were used in all: nobody else waits for them, and they complete before
+// the CTA gives the barriers' memory back.  After a wait that ran out they may never.
+template <int N>
+__device__ __forceinline__ void drain(uint32_t bars, int n, long long budget, volatile int *err) {
+    for (int q = n > N ? n - N : 0; q < n && !*err; ++q)
+        if (!mbar_wait_bounded(bars + 8 * (q % N), (q / N) & 1, budget)) break;
+}
 // A place in a ring of N barriers, and the parity of its next phase.
 template <int N>
 struct Ring {
@@ -706,6 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
             if (rank == 0)  // what both CTAs issued has landed
                 for (int q = it > C::kStages ? it - C::kStages : 0; q < it; ++q)
                     mbar_wait_bounded(full + 8 * (q % C::kStages), (q / C::kStages) & 1, kDrain);
+            drain<C::kStages>(empty, it, a.wait_budget, err);
         } else if (warp == 1 && rank == 0) {
             const uint64_t desc = tc::sdesc_sw128(smem_addr(sm));
             Ring<C::kStages> st;
@@ -727,8 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
                 st.next();
                 buf.next();
             }
-            mma_pair_done(fin);  // every product is done before either CTA gives its memory back
-            mbar_wait_spin(fin, 0, kDrain);
+            mma_pair_done(fin);
         }
         __syncwarp();
     } else {
@@ -850,6 +857,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
+    // Every product is done before either CTA gives its memory back, and every signal of the products has arrived: they go
+    // to both CTAs, and each waits for its own last ones (the cluster's barrier orders threads, not signals under way).
+    if (warp == 1) {
+        mbar_wait_spin(fin, 0, kDrain);
+        __syncwarp();
+    }
     // After a wait that ran out: copies that the even CTA did not wait for (the odd CTA's own, and boxes of `add`) land
     // within microseconds, before either CTA goes.
     if (*err)
