@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(192, Few<TN>::kCtas) k_matmul_few(const __grid
             }
             for (int q = k > C::kStages ? k - C::kStages : 0; q < k; ++q)  // what was issued has landed
                 mbar_wait_bounded(full + 8 * (q % C::kStages), (q / C::kStages) & 1, kDrain);
+            drain<C::kStages>(empty, k, a.wait_budget, err);
         }
         __syncwarp();
     } else if (warp == 1) {

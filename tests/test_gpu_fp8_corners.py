@@ -37,3 +37,10 @@ def check_back_to_back(sizes, reps):
                                    [(100, 5120, 256), (300, 640, 256)]], ids=str)
 def test_pairs_hand_over_their_memory(sizes):
     check_back_to_back(sizes, 1600)
+
+
+# A call of few rows and blocks ends right after its products; kernels of all kinds take each other's place.
+@pytest.mark.parametrize("sizes", [[(1, 5120, 16)], [(3, 5120, 640), (40, 5120, 128)], [(64, 2048, 512), (17, 2048, 144)],
+                                   [(128, 5120, 640), (3, 5120, 640), (120, 12800, 128), (64, 2048, 512)]], ids=str)
+def test_few_rows_hand_over_their_memory(sizes):
+    check_back_to_back(sizes, 1600)
