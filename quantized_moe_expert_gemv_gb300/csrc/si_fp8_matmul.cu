@@ -805,6 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
                     sw[j] = a.w_scale[to + (more ? here.w : next.w)];
                     const f32x2 scale2 = pack2(scale, scale);
                     if (!mbar_try_wait(d_full + 8 * buf.at, buf.phase)) wait_full();
+                    __syncwarp();  // (each lane waited for itself, and the reads below are the warp's)
                     tc::fence_after_sync();
                     const uint32_t from = lane_addr + NT * buf.at;
                     uint32_t v[2][16];
@@ -868,6 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kManyThreads, 1)
     // within microseconds, before either CTA goes.
     if (*err)
         for (const long long t0 = clock64(); clock64() - t0 < kLinger;) __nanosleep(1000);
+    __syncwarp();
     cluster_sync();  // (nothing more arrives from the other CTA)
     if (warp == 1) {
         tc::fence_after_sync();
