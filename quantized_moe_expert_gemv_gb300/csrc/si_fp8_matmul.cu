@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(192, Few<TN>::kCtas) k_matmul_few(const __grid
             buf.next();
             sw = ahead;
         }
+        __syncwarp();  // (the barriers below are the warp's)
         // Sums to the CTAs that store them: [CTA that they come from][row / S][128 rows of the weights].
         const float *const part = reinterpret_cast<const float *>(sm + (S == 1 ? 0 : C::kParts));
         const uint32_t part_addr = smem_addr(part) + 4 * r;
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(192, Few<TN>::kCtas) k_matmul_few(const __grid
             }
         }
     }
+    __syncwarp();
     if (warp < 2 || S == 1) cluster_wait();
     tc::fence_before_sync();
     __syncthreads();
