@@ -845,6 +845,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             if (rank == 0)  // the even CTA's full covers the copies of both CTAs
                 for (int q = (step > kNS ? step - kNS : 0); q < step; ++q)
                     mbar_wait_bounded_cluster(full + 8 * (q % kNS), (q / kNS) & 1, kDrainG);
+            // the MMA threads' last signals, to both CTAs, have arrived before this CTA gives its barriers' memory
+            // back: nobody else waits for them (after a wait that ran out they may never come)
+            for (int q = (step > kNS ? step - kNS : 0); q < step && !*verr; ++q)
+                if (!mbar_wait_bounded_cluster(empty + 8 * (q % kNS), (q / kNS) & 1, budget)) break;
         }
         __syncwarp();
     } else if (warp == 1 || warp == 3) {
