@@ -815,4 +815,6 @@ def si_fp8_matmul(plan: Fp8Plan, rows: si_fp8_rows, weight: si_fp8_weight, add, 
 
 
 def si_fp8_read_status(plan: Fp8Plan, scratch, stream=None) -> int:
-    return load_library().si_fp8_read_status(plan.handle, _ptr(scratch), _stream(stream))
+    """The status recorded in `scratch` (SI_OK if none), cleared by the call; SI_ERR_INVALID_ARG where the plan's device is
+    not the current one."""
+    return load_library().si_fp8_read_status(plan.handle, _fp8_scratch(plan, scratch), _fp8_stream(plan, stream))

@@ -286,6 +286,7 @@ si_status si_fp8_matmul(si_fp8_plan_t plan, const si_fp8_rows *rows, const si_fp
 si_status si_fp8_read_status(si_fp8_plan_t plan, const void *scratch, si_stream_t stream) {
     if (!plan || !scratch) return SI_ERR_INVALID_ARG;
     if (!aligned(scratch, 16)) return SI_ERR_MISALIGNED;
+    SI_FP8_TRY(check_device(plan->p));
     int32_t word = 0;
     SI_FP8_TRY(launched(cudaStreamSynchronize((cudaStream_t)stream)));
     SI_FP8_TRY(launched(cudaMemcpy(&word, scratch, sizeof(word), cudaMemcpyDeviceToHost)));
