@@ -698,13 +698,17 @@ def fp8_mat(t) -> si_fp8_mat:
     return m
 
 
+def _fp8_types(codes, scales) -> None:
+    if str(codes.dtype) not in ("torch.float8_e4m3fn", "torch.uint8") or "float32" not in str(scales.dtype):
+        raise ValueError("codes are E4M3's 8 bits (float8_e4m3fn, or uint8 that holds them), scales are float32")
+
+
 def fp8_rows(codes, scales) -> si_fp8_rows:
-    """codes [rows, K] float8_e4m3fn (or another 8-bit type), scales [ceil(K / 128), scale_stride] float32, both
+    """codes [rows, K] float8_e4m3fn (or uint8 that holds its bits), scales [ceil(K / 128), scale_stride] float32, both
     contiguous.  The structure keeps them alive."""
     if codes.dim() != 2 or scales.dim() != 2 or not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("codes [rows, K] and scales [ceil(K / 128), scale_stride] are contiguous")
-    if codes.element_size() != 1 or "float32" not in str(scales.dtype):
-        raise ValueError("codes have 8 bits, scales are float32")
+    _fp8_types(codes, scales)
     (n, k), (kb, stride) = codes.shape, scales.shape
     if kb != -(-k // SI_FP8_BLOCK) or stride < n:
         raise ValueError("scales have a row for each 128 columns, with a value for each row of codes")
@@ -714,12 +718,11 @@ def fp8_rows(codes, scales) -> si_fp8_rows:
 
 
 def fp8_weight(codes, scales) -> si_fp8_weight:
-    """codes [N, K] float8_e4m3fn (or another 8-bit type), scales [ceil(N / 128), ceil(K / 128)] float32, both
+    """codes [N, K] float8_e4m3fn (or uint8 that holds its bits), scales [ceil(N / 128), ceil(K / 128)] float32, both
     contiguous.  The structure keeps them alive."""
     if codes.dim() != 2 or scales.dim() != 2 or not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("codes [N, K] and scales [ceil(N / 128), ceil(K / 128)] are contiguous")
-    if codes.element_size() != 1 or "float32" not in str(scales.dtype):
-        raise ValueError("codes have 8 bits, scales are float32")
+    _fp8_types(codes, scales)
     if tuple(scales.shape) != tuple(-(-n // SI_FP8_BLOCK) for n in codes.shape):
         raise ValueError("scales have a value for each block of 128 x 128 codes")
     w = si_fp8_weight(codes.data_ptr(), scales.data_ptr())

@@ -31,3 +31,19 @@ def test_the_binding_reads_the_status_in_the_plans_stream(monkeypatch):
     monkeypatch.setattr(binding, "_fp8_scratch", lambda plan, scratch: 77)
     assert binding.si_fp8_read_status(plan, None) == (0, 77, 1001)
     assert binding.si_fp8_read_status(plan, None, 5) == (0, 77, 5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.int8, torch.bool], ids=str)
+def test_codes_of_another_8_bit_type_are_refused(dtype):
+    """Their bits would be read as E4M3."""
+    codes = torch.zeros(6, 300, dtype=torch.uint8).view(dtype)
+    for make, scales in ((binding.fp8_rows, torch.zeros(3, 8)), (binding.fp8_weight, torch.zeros(1, 3))):
+        with pytest.raises(ValueError, match="8 bits"):
+            make(codes, scales)
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e4m3fn, torch.uint8], ids=str)
+def test_codes_in_e4m3_or_its_bytes_are_taken(dtype, monkeypatch):
+    monkeypatch.setattr(binding, "_on_device", lambda *tensors: 0)  # (tensors in host memory here)
+    codes = torch.zeros(6, 300, dtype=torch.uint8).view(dtype)
+    assert binding.fp8_rows(codes, torch.zeros(3, 8)).rows == 6 and binding.fp8_weight(codes, torch.zeros(1, 3)).rows == 6
