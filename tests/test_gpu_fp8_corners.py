@@ -1,9 +1,10 @@
-"""The dense block's products where one call's shared memory passes to the next at once."""
+"""The dense block's products where one call's shared memory passes to the next at once, waits that run out in each of the
+kernels, and memory that no call takes."""
 import pytest
 import torch
 
 import fp8_reference as ref
-from test_gpu_fp8 import DEV, Product
+from test_gpu_fp8 import DEV, Product, empty_rows, randn
 from quantized_moe_expert_gemv_gb300 import binding as si
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,49 @@ def test_pairs_hand_over_their_memory(sizes):
                                    [(128, 5120, 640), (3, 5120, 640), (120, 12800, 128), (64, 2048, 512)]], ids=str)
 def test_few_rows_hand_over_their_memory(sizes):
     check_back_to_back(sizes, 1600)
+
+
+# 304 and 5000 columns: outputs by boxes, alone, with `add` by boxes, and with one of another type; 300: rows that end anywhere
+@pytest.mark.parametrize("out,add", [("f32", None), ("bf16", None), ("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32")])
+@pytest.mark.parametrize("t,n", [(1, 304), (40, 304), (300, 304), (300, 5000), (300, 300)])
+def test_each_wait_that_runs_out_is_reported(monkeypatch, t, n, out, add):
+    monkeypatch.setenv("SI_FAULT_WAIT_BUDGET", "2000000")
+    p = Product(t, n, 512, seed=1)
+    monkeypatch.delenv("SI_FAULT_WAIT_BUDGET")
+    q = Product(t, n, 512, seed=1)
+    a = None if add is None else randn(p.g, t, n, dtype=ref.TYPES[add])
+    got = torch.empty((t, n), dtype=ref.TYPES[out], device=DEV)
+    for _ in range(2):
+        p(got, a)
+        assert p.status() == si.SI_ERR_TIMEOUT and p.status() == si.SI_OK
+        q(got, a)  # (the next call, right after it, is as good as ever)
+        ref.check_out(got, *q.want(a), 512)
+        assert q.status() == si.SI_OK
+
+
+def test_calls_take_no_memory():
+    """Neither the device's, once the kernels have been loaded, nor torch's."""
+    plans = []
+    for t, n, k in ((1, 640, 512), (40, 640, 512), (300, 640, 512), (300, 5000, 512), (300, 301, 512)):
+        p = Product(t, n, k, seed=2)
+        codes, scales = empty_rows(t, k)
+        weight = si.fp8_weight(torch.empty_like(p.w_codes), torch.empty_like(p.w_scales))
+        w, x = randn(p.g, n, k), randn(p.g, t, k, dtype=torch.bfloat16)
+        plans.append((p, w, weight, x, torch.empty_like(x), torch.ones(k, device=DEV), si.fp8_rows(codes, scales),
+                      torch.empty((t, n), dtype=torch.bfloat16, device=DEV)))
+
+    def calls():
+        for p, w, weight, x, y, gain, rows, out in plans:
+            si.si_fp8_pack(p.plan, w, weight)
+            si.si_fp8_norm(p.plan, x, x, gain, 1e-6, y, None, rows, p.t)
+            for add in (None, out):
+                si.si_fp8_matmul(p.plan, rows, weight, add, out, p.t, p.scratch)
+
+    def held():
+        torch.cuda.synchronize()
+        return torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()
+    calls()
+    before = held()
+    for _ in range(20):
+        calls()
+    assert held() == before
