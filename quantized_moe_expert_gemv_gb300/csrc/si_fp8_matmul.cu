@@ -154,8 +154,8 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t rank, f
 // M) and the rows the second (N = TN, of which the tile may hold fewer), so that no product works on rows that are not
 // there.  A cluster of S CTAs shares a tile, each with its part of the blocks of columns: that brings enough loads into
 // flight where there are few tiles.  Row t's sums are added up by CTA t mod S, which the others send theirs, in the CTAs'
-// order.  1 x 5120 x 2048: 3.5 us in a graph (start, copy, four blocks, join); 1 x 100003 x 2048: 34 us, 6.0 TB/s.  Warp 0 loads, warp 1 issues the products, and warps 2 to 5 add the blocks' sums up, one row of the weights a
-// thread.
+// order.  1 x 5120 x 2048: 3.6 us in a graph (start, copy, four blocks, join); 1 x 100003 x 2048: 34.6 us, 5.9 TB/s.
+// Warp 0 loads, warp 1 issues the products, and warps 2 to 5 add the blocks' sums up, one row of the weights a thread.
 template <int TN>
 __global__ void __launch_bounds__(192, Few<TN>::kCtas) k_matmul_few(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                                                     const MatmulArgs a, int t_tiles, int S) {
@@ -411,7 +411,7 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, in
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Eight neighbouring values of `add`, or fewer at its end.
+// Eight neighbouring values of `add`, all of them there.
 __device__ __forceinline__ void add8(const Mat &m, int64_t at, float (&v)[8]) {
     float r[8];
     if (m.dtype == SI_FP8_F32) widen8<true>(load8<true>(m.p, at), false, r);
@@ -634,7 +634,7 @@ __device__ __forceinline__ void regs_up() {
 // What bounds it: a block's products take 512 cycles at NT = 256 (600 beside the copies into shared memory), but with two
 // buffers of sums the next but one waits until all of a block's sums have been read, a chain of about 690 cycles a block
 // (signal 72, reading about 450, the slower CTA's signal to the issuing warp 259).  4096 x 5120 x 2048: 39 us, 2.2 PFLOP/s;
-// 8192^3: 349 us, 3.15 PFLOP/s (in long runs at the power limit 2.5 to 2.9).
+// 8192^3: 350 us, 3.14 PFLOP/s (in long runs at the power limit 2.5 to 2.9).
 // MODE, a kernel for each, as what one does not need costs its loop registers: kPlain stores `out` by boxes; kAddBoxes also
 // has `add` by boxes (16-bit values of out's type): a box is fetched while the blocks are added up, into the shared memory
 // that its outputs leave from; kAny takes every other case (rows that begin or end anywhere, `add` of another type or one
@@ -938,7 +938,8 @@ cudaError_t launch_many(const Plan &p, const MatmulArgs &a, cudaStream_t s) {
 }
 
 // How many CTAs share a tile of few rows: a power of two, as many as two CTAs an SM (three are no faster), eight CTAs and
-// a block of columns for each leave.  (One CTA more than there is room for costs as much as all: 1 x 5120 x 2048 takes 3.5 us with 4; 5.6 with 8, two CTAs an SM.)
+// a block of columns for each leave.  (One CTA more than there is room for costs as much as all: 1 x 5120 x 2048 takes 3.6 us
+// with 4; 5.6 with 8, two CTAs an SM.)
 int few_share(const Plan &p, const MatmulArgs &a, int TN) {
     const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.T + TN - 1) / TN);
     int S = 1;
@@ -974,8 +975,8 @@ cudaError_t launch_few(const Plan &p, const MatmulArgs &a, cudaStream_t s) {
 cudaError_t launch_matmul(const Plan &p, const MatmulArgs &a, cudaStream_t s) {
     if (a.T <= 16) return launch_few<16>(p, a, s);
     if (a.T <= 32) return launch_few<32>(p, a, s);
-    // Tiles of 64 rows pay as long as four CTAs or more share each of them: 200 x 2048 x 4096 takes 8.8 us so and 11.4 by
-    // pairs, 128 x 5120 x 2048 (two CTAs a tile) 9.3 and 8.1.
+    // Tiles of 64 rows pay as long as four CTAs or more share each of them: 200 x 2048 x 4096 takes 8.9 us so and 11.4 by
+    // pairs, 128 x 5120 x 2048 (two CTAs a tile) 9.3 and 7.8.
     if (a.T <= 64 || few_share(p, a, 64) >= 4) return launch_few<64>(p, a, s);
     // A round of tiles of 256 columns takes 1.2 to 1.45 times as long as one of 128 (K = 2048 to 8192).
     const int64_t m = (a.T + 255) / 256, pairs = p.sm_count / 2;

@@ -35,10 +35,12 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t (&m)[V]) {
 
 // One row by W warps, R rows a CTA at a time; a thread holds V pieces of eight columns in registers, so a row is read
 // once.  16 neighbouring lanes hold the 128 columns of a scale.  RES: 0 no residual, 1 in 16 bits, 2 in 32.
-// Memory's rate bounds it where there are many rows, and the instructions come near: each CTA goes on from row to row, a
-// row's loads are on their way while the row before is reduced, quantised and stored, the gain stays in registers, and one
-// division of each kind and one exchange serves the blocks of V pieces.  16384 rows of 2048 in bf16 with a residual, 235 MB:
-// 49 us, 71% of the copy rate; without one and without a gain, 6001 rows of 4096, 74 MB: 16.4 us, 66%.
+// Many rows: each CTA goes on from row to row, a row's loads are on their way while the row before is reduced, quantised and
+// stored, the gain stays in registers, and one division of each kind and one exchange serves the blocks of V pieces.
+// 16384 rows of 2048 in bf16 with a residual, 235 MB: 49 us, 71% of the copy rate; without one and without a gain, 6001 rows
+// of 4096, 74 MB: 16.4 us, 66%.  Neither memory nor the instructions are what it waits for: with a residual (34 instructions
+// a value, 31 warps an SM) the schedulers issue in two thirds of the cycles and DRAM is busy for half, without (14 a value,
+// 15 warps) in 59% and for a third.  The rest is the latency of a row's chain, with too few rows under way on an SM.
 template <int V, bool X32, int RES>
 __global__ void __launch_bounds__(512, V > 2 ? 1 : 2) k_norm(const NormArgs a, int W, int R) {
     __shared__ float s_sum[2][32];
@@ -204,6 +206,7 @@ cudaError_t norm_by_size(const Plan &p, const NormArgs &a, cudaStream_t s) {
     // One piece a thread for few rows, where only the time of one row counts (1 x 2048: 2.0 us).  For more, two pieces, or
     // four of one 16-bit operand, as far as a row fills the lanes with them: 16384 x 2048 in bf16 takes 55, 49 and 67 us
     // with one, two and four where there is a residual (which then leaves too few threads), 44, 31 and 29 where there is none.
+    // Rows of more than 512, 1024 and 2048 pieces take two, four and eight at least, so that 16 warps hold them.
     const int pieces = (a.K + 7) / 8;  // of eight columns
     const bool few = a.T <= 2 * p.sm_count && pieces <= 512;
     auto fills = [&](int V) { return (pieces + 32 * V - 1) / (32 * V) * 32 * V * 4 <= pieces * 5; };
